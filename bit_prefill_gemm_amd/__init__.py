@@ -13,7 +13,8 @@ Public names mirror the C ABI in include/bpg.h:
     moe_route_sort, w4a4_grouped_gemm_gather, swiglu_quantize_h32, moe_combine;
     and rotations over 64 or 128 values: rotate_pack_weights_rot,
     quantize_act_rot, w4a4_gemm_rot; and bf16 output: w4a4_gemm_bf16,
-    w4a4_grouped_gemm_bf16
+    w4a4_grouped_gemm_bf16; and what sits between the products of a block:
+    rmsnorm_quantize_act, dequantize_act, w4a4_gemm_epilogue, moe_route_topk
 
 The binding is loaded lazily so that ``bit_prefill_gemm_amd.synth`` (input
 generators) imports without the HIP library.
@@ -26,6 +27,7 @@ _BINDING_NAMES = {
     "moe_route_sort", "w4a4_grouped_gemm_gather", "swiglu_quantize_h32", "moe_combine",
     "rotate_pack_weights_rot", "quantize_act_rot", "w4a4_gemm_rot",
     "w4a4_gemm_bf16", "w4a4_grouped_gemm_bf16",
+    "rmsnorm_quantize_act", "dequantize_act", "w4a4_gemm_epilogue", "moe_route_topk",
 }
 
 

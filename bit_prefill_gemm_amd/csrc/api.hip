@@ -46,6 +46,11 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // prompt batches)
 constexpr int64_t kMaxSortExperts = 512;
 constexpr int64_t kMaxSortEntries = (int64_t)1 << 20;
+// routing: a wave holds the choices and the group scores of a token one per lane
+constexpr int64_t kMaxTopk = 64;
+constexpr int64_t kMaxGroups = 64;
+// norm: a row stays in one workgroup's registers
+constexpr int64_t kMaxNormK = (int64_t)1 << 16;
 
 bpg_status launch_status(hipError_t e) { return e == hipSuccess ? BPG_OK : BPG_ERR_LAUNCH; }
 
@@ -310,10 +315,24 @@ bpg_status quantize_checked(const void *x, bpg_x_dtype dt, int64_t m, int64_t k,
                                               scales, static_cast<hipStream_t>(stream)));
 }
 
-// y: fp32 [m][ldy], or bf16 bits when y_bf16 (rows 16-byte aligned either way)
+bool dtype_ok(bpg_x_dtype dt) { return dt == BPG_X_F32 || dt == BPG_X_BF16; }
+
+bool rotation_ok(int rotation)
+{
+    return rotation == 0 || rotation == 32 || rotation == 64 || rotation == 128;
+}
+
+bool aligned_to(const void *p, bpg_x_dtype dt)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (dt == BPG_X_BF16 ? 1u : 3u)) == 0;
+}
+
+// y: fp32 [m][ldy], or bf16 bits when y_bf16 (rows 16-byte aligned either
+// way); ep: the epilogue, or null for none (its own checks are done)
 bpg_status gemm_checked(const void *codes, const float *scales, int act_bits, int64_t m,
                         const bpg_weights_desc *w, const void *w_dev, void *y, bool y_bf16,
-                        int64_t ldy, void *stream, uint32_t rotation)
+                        int64_t ldy, void *stream, uint32_t rotation,
+                        const bpg_epilogue *ep = nullptr)
 {
     if (!w)
         return BPG_ERR_NULL;
@@ -349,6 +368,15 @@ bpg_status gemm_checked(const void *codes, const float *scales, int act_bits, in
     else
         p.y = static_cast<float *>(y);
     p.ldy = ldy;
+    if (ep) {
+        p.ep.bias = ep->bias;
+        p.ep.bias_bf16 = ep->bias_dt == BPG_X_BF16;
+        p.ep.residual = ep->residual;
+        p.ep.residual_bf16 = ep->residual_dt == BPG_X_BF16;
+        p.ep.ldr = ep->ldr;
+        p.ep.act = (int)ep->act;
+        p.epilogue = true;
+    }
     return launch_status(bpg::launch_gemm(p, static_cast<hipStream_t>(stream)));
 }
 
@@ -383,6 +411,73 @@ bpg_status quantize_act_unrotated(const void *x, bpg_x_dtype dt, int64_t m, int6
     return quantize_checked(x, dt, m, k, ldx, act_bits, codes, scales, stream, 0);
 }
 
+bpg_status rmsnorm_quantize_act(const void *x, bpg_x_dtype x_dt, int64_t ldx,
+                                const void *residual, bpg_x_dtype residual_dt, int64_t ldr,
+                                void *h, int64_t ldh, const void *weight, bpg_x_dtype weight_dt,
+                                float eps, int64_t m, int64_t k, int act_bits, int rotation,
+                                void *codes, float *scales, void *stream)
+{
+    if (!dtype_ok(x_dt) || (residual && !dtype_ok(residual_dt)) ||
+        (weight && !dtype_ok(weight_dt)) || (act_bits != 4 && act_bits != 8))
+        return BPG_ERR_DTYPE;
+    constexpr int64_t kMaxLd = (int64_t)1 << 40;
+    if (!rotation_ok(rotation) || m < 0 || m > ((int64_t)1 << 31) - 1 || k <= 0 || k > kMaxNormK ||
+        k % (rotation > 32 ? rotation : 32) != 0 || ldx < k || ldx > kMaxLd ||
+        (residual && (ldr < k || ldr > kMaxLd)) || (residual && h && (ldh < k || ldh > kMaxLd)) ||
+        !(eps > 0.0f) || !std::isfinite(eps))
+        return BPG_ERR_SHAPE;
+    if (m > 0 && (!x || !codes || !scales))
+        return BPG_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(weight) ||
+        ldx % 4 != 0 || (residual && (!aligned16(residual) || ldr % 4 != 0)) ||
+        (residual && h && (!aligned16(h) || ldh % 4 != 0)))
+        return BPG_ERR_ALIGN;
+    bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    bpg::NormProblem p{};
+    p.x = x;
+    p.x_bf16 = x_dt == BPG_X_BF16;
+    p.ldx = ldx;
+    p.residual = residual;
+    p.residual_bf16 = residual ? residual_dt == BPG_X_BF16 : p.x_bf16;
+    p.ldr = residual ? ldr : 0;
+    p.h = residual ? h : nullptr;
+    p.ldh = ldh;
+    p.weight = weight;
+    p.weight_bf16 = weight_dt == BPG_X_BF16;
+    p.eps = eps;
+    p.m = m;
+    p.k = k;
+    p.act_bits = act_bits;
+    p.rot = rotation;
+    p.codes = codes;
+    p.scales = scales;
+    return launch_status(bpg::launch_norm_quantize(p, static_cast<hipStream_t>(stream)));
+}
+
+bpg_status dequantize_act(const void *codes, const float *scales, int act_bits, int rotation,
+                          int64_t m, int64_t k, void *y, bpg_x_dtype y_dt, int64_t ldy,
+                          void *stream)
+{
+    if (!dtype_ok(y_dt) || (act_bits != 4 && act_bits != 8))
+        return BPG_ERR_DTYPE;
+    if (!rotation_ok(rotation) || m < 0 || m > ((int64_t)1 << 31) - 1 || k <= 0 ||
+        k > ((int64_t)1 << 30) || k % (rotation > 32 ? rotation : 32) != 0 || ldy < k ||
+        ldy > ((int64_t)1 << 40))
+        return BPG_ERR_SHAPE;
+    if (m > 0 && (!codes || !scales || !y))
+        return BPG_ERR_NULL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(y) || ldy % 4 != 0)
+        return BPG_ERR_ALIGN;
+    bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    return launch_status(bpg::launch_dequantize(codes, scales, act_bits, rotation, m, k, y,
+                                                y_dt == BPG_X_BF16, ldy,
+                                                static_cast<hipStream_t>(stream)));
+}
+
 bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64_t m,
                      const bpg_weights_desc *w, const void *w_dev, float *y, int64_t ldy,
                      void *stream)
@@ -395,6 +490,29 @@ bpg_status w4a4_gemm_bf16(const void *codes, const float *scales, int act_bits, 
                           void *stream)
 {
     return gemm_checked(codes, scales, act_bits, m, w, w_dev, y, true, ldy, stream, 32);
+}
+
+bpg_status w4a4_gemm_epilogue(const void *codes, const float *scales, int act_bits, int rotation,
+                              int64_t m, const bpg_weights_desc *w, const void *w_dev,
+                              const bpg_epilogue *ep, void *y, bpg_x_dtype y_dt, int64_t ldy,
+                              void *stream)
+{
+    if (!w || !ep)
+        return BPG_ERR_NULL;
+    if (!dtype_ok(y_dt) || (ep->bias && !dtype_ok(ep->bias_dt)) ||
+        (ep->residual && !dtype_ok(ep->residual_dt)))
+        return BPG_ERR_DTYPE;
+    if (ep->act < BPG_ACT_NONE || ep->act > BPG_ACT_GELU_TANH)
+        return BPG_ERR_DTYPE;
+    if (!rotation_ok(rotation))
+        return BPG_ERR_SHAPE;
+    if (ep->residual && (ep->ldr < w->n || ep->ldr > ((int64_t)1 << 40)))
+        return BPG_ERR_SHAPE;
+    if ((ep->bias && !aligned_to(ep->bias, ep->bias_dt)) ||
+        (ep->residual && !aligned_to(ep->residual, ep->residual_dt)))
+        return BPG_ERR_ALIGN;
+    return gemm_checked(codes, scales, act_bits, m, w, w_dev, y, y_dt == BPG_X_BF16, ldy, stream,
+                        (uint32_t)rotation, ep);
 }
 
 bpg_status w4a4_gemm_unrotated(const void *codes, const float *scales, int act_bits, int64_t m,
@@ -559,6 +677,51 @@ bpg_status w4a4_grouped_gemm_gather(const void *codes, const float *scales, int 
 {
     return grouped_checked(codes, scales, act_bits, true, src_rows, row_ids_dev, total_rows,
                            expert_offsets_dev, w, w_dev, y, false, ldy, stream);
+}
+
+bpg_status moe_route_topk(const void *logits_dev, bpg_x_dtype dt, int64_t tokens, int64_t experts,
+                          int64_t ldl, bpg_score score, const float *bias_dev, int64_t groups,
+                          int64_t topk_groups, bpg_group_score group_score, int64_t topk,
+                          int renormalize, float scale, int32_t *expert_of_dev,
+                          float *weights_dev, void *stream)
+{
+    if (!dtype_ok(dt) || (score != BPG_SCORE_SOFTMAX && score != BPG_SCORE_SIGMOID) ||
+        (group_score != BPG_GROUP_MAX && group_score != BPG_GROUP_TOP2))
+        return BPG_ERR_DTYPE;
+    if (tokens < 0 || tokens > kMaxSortEntries || experts < 1 || experts > kMaxSortExperts ||
+        ldl < experts || ldl > ((int64_t)1 << 40) || groups < 1 || groups > kMaxGroups ||
+        experts % groups != 0 || topk_groups < 1 || topk_groups > groups || topk < 1 ||
+        topk > kMaxTopk || topk > topk_groups * (experts / groups) ||
+        tokens * topk > kMaxSortEntries || !std::isfinite(scale) ||
+        (group_score == BPG_GROUP_TOP2 && groups > 1 && experts / groups < 2))
+        return BPG_ERR_SHAPE;
+    if (tokens > 0 && (!logits_dev || !expert_of_dev || !weights_dev))
+        return BPG_ERR_NULL;
+    if (!aligned_to(logits_dev, dt) ||
+        ((reinterpret_cast<uintptr_t>(bias_dev) | reinterpret_cast<uintptr_t>(expert_of_dev) |
+          reinterpret_cast<uintptr_t>(weights_dev)) &
+         3u) != 0)
+        return BPG_ERR_ALIGN;
+    bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    bpg::RouteProblem p{};
+    p.logits = logits_dev;
+    p.bias = bias_dev;
+    p.expert_of = expert_of_dev;
+    p.weights = weights_dev;
+    p.tokens = tokens;
+    p.ldl = ldl;
+    p.experts = (int)experts;
+    p.topk = (int)topk;
+    p.groups = (int)groups;
+    p.kept = (int)topk_groups;
+    p.scale = scale;
+    p.logits_bf16 = dt == BPG_X_BF16;
+    p.sigmoid = score == BPG_SCORE_SIGMOID;
+    p.pair = group_score == BPG_GROUP_TOP2;
+    p.renormalize = renormalize != 0;
+    return launch_status(bpg::launch_route_topk(p, static_cast<hipStream_t>(stream)));
 }
 
 bpg_status moe_route_sort(const int32_t *expert_of_dev, int64_t tokens, int64_t topk,

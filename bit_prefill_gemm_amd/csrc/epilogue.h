@@ -1,0 +1,62 @@
+// epilogue.h -- bias, activation and residual applied to a dense product's
+// fp32 results before the store (gfx950).  Internal; included by the dense
+// product kernels, whose template argument EP selects the form with it.
+//
+//   y = act(v + bias[column]) + residual[row][column]
+//
+// each step in fp32, rounded once to the output's type at the store.  The
+// kernels load every residual value of a lane before they store its first
+// result: the residual may be y itself, so a load after a store could not be
+// moved ahead of it and would wait for it.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bpg.h"
+#include "internal.h"
+
+namespace bpg {
+namespace {
+
+__device__ __forceinline__ float ep_load(const void *p, bool bf16, int64_t i)
+{
+    return bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16)
+                : static_cast<const float *>(p)[i];
+}
+
+// 1 / (1 + e^-x)
+__device__ __forceinline__ float ep_sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// the activation of N values of a lane (act is uniform across the launch)
+template <int N>
+__device__ __forceinline__ void ep_activate(int act, float (&v)[N])
+{
+    switch (act) {
+    case BPG_ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            v[i] = v[i] < 0.0f ? 0.0f : v[i];
+        break;
+    case BPG_ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            v[i] = v[i] * ep_sigmoid(v[i]);
+        break;
+    case BPG_ACT_GELU:
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+        break;
+    case BPG_ACT_GELU_TANH:
+        // 0.5 (1 + tanh u) = sigmoid(2 u), u = sqrt(2 / pi) (x + 0.044715 x^3)
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            v[i] = v[i] * ep_sigmoid(1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+        break;
+    default: break;
+    }
+}
+
+} // namespace
+} // namespace bpg

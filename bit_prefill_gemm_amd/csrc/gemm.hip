@@ -37,6 +37,7 @@
 
 #include <type_traits>
 
+#include "epilogue.h"
 #include "internal.h"
 #include "operands.h"
 
@@ -173,7 +174,7 @@ __device__ __forceinline__ void with_count(int n, F &&f)
     }
 }
 
-template <class C, int MODE>
+template <class C, int MODE, bool EP>
 __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem p, int tiles_m,
                                                               int tiles_n, int tm0, int tn0)
 {
@@ -605,6 +606,39 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
             const int t = t0 + tt;
             const int i = t / TN, j = t % TN;
             const int64_t col = col0 + (wn * TN + j) * MF + rc;
+            if constexpr (EP) {
+                const int64_t trow = row0 + (wm * TM + i) * MF;
+                float vr[RG], res[RG];
+                if (p.ep.residual) {
+#pragma unroll
+                    for (int r = 0; r < RG; r++) {
+                        const int rl = M::out_row(g, r);
+                        if (rl < vrows[i])
+                            res[r] = ep_load(p.ep.residual, p.ep.residual_bf16,
+                                             (trow + rl) * p.ep.ldr + col);
+                    }
+                }
+                const float bias = p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col) : 0.0f;
+#pragma unroll
+                for (int r = 0; r < RG; r++) {
+                    float v = red[(((grp * WK + 0) * R + tt) * RG + r) * 64 + lane];
+#pragma unroll
+                    for (int w = 1; w < WK; w++)
+                        v += red[(((grp * WK + w) * R + tt) * RG + r) * 64 + lane];
+                    vr[r] = v * unscale;
+                    if (p.ep.bias)
+                        vr[r] = vr[r] + bias;
+                }
+                ep_activate(p.ep.act, vr);
+#pragma unroll
+                for (int r = 0; r < RG; r++) {
+                    const int rl = M::out_row(g, r);
+                    if (rl < vrows[i])
+                        store_y(p, (trow + rl) * p.ldy + col,
+                                p.ep.residual ? vr[r] + res[r] : vr[r]);
+                }
+                continue;
+            }
 #pragma unroll
             for (int r = 0; r < RG; r++) {
                 float v = red[(((grp * WK + 0) * R + tt) * RG + r) * 64 + lane];
@@ -628,8 +662,15 @@ hipError_t launch_cfg(const GemmProblem &p, int tiles_m, int tiles_n, int tm0, i
 {
     if (grid <= 0)
         return hipSuccess;
-    w4a4_kernel<C, MODE><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(p, tiles_m, tiles_n,
-                                                                            tm0, tn0);
+    if constexpr (MODE == kGemm) {
+        if (p.epilogue) {
+            w4a4_kernel<C, MODE, true><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(
+                p, tiles_m, tiles_n, tm0, tn0);
+            return hipGetLastError();
+        }
+    }
+    w4a4_kernel<C, MODE, false><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(
+        p, tiles_m, tiles_n, tm0, tn0);
     return hipGetLastError();
 }
 

@@ -38,6 +38,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.h"
 #include "internal.h"
 #include "operands.h"
 
@@ -102,7 +103,7 @@ __device__ __forceinline__ void transpose_rows4(uint4 &v)
     v = make_uint4(c[0], c[1], d[0], d[1]);
 }
 
-template <class C>
+template <class C, bool EP>
 __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
 {
     constexpr int TM = C::TM, TN = C::TN, D = C::D, NW = C::NW, NT = C::kThreads;
@@ -351,15 +352,31 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     __syncthreads();
     const float unscale = 1.0f / (float)(1 << C::kShift);
     for (int v = tid; v < R * 64; v += NT) {
+        const int q = v >> 6, ln = v & 63;
+        const int i = q / (TN * 4), j = (q / 4) % TN, r = q % 4;
+        const int m = 16 * i + 4 * (ln >> 4) + r;
+        const int64_t col = col0 + 16 * j + (ln & 15);
+        float res = 0.0f, bias = 0.0f;
+        if constexpr (EP) {
+            if (p.ep.residual && m < rows)
+                res = ep_load(p.ep.residual, p.ep.residual_bf16, (int64_t)m * p.ep.ldr + col);
+            if (p.ep.bias)
+                bias = ep_load(p.ep.bias, p.ep.bias_bf16, col);
+        }
         float s = red[v];
 #pragma unroll
         for (int w = 1; w < NW; w++)
             s += red[w * R * 64 + v];
-        const int q = v >> 6, ln = v & 63;
-        const int i = q / (TN * 4), j = (q / 4) % TN, r = q % 4;
-        const int m = 16 * i + 4 * (ln >> 4) + r;
+        float o[1] = {s * unscale};
+        if constexpr (EP) {
+            if (p.ep.bias)
+                o[0] = o[0] + bias;
+            ep_activate(p.ep.act, o);
+            if (p.ep.residual)
+                o[0] = o[0] + res;
+        }
         if (m < rows)
-            store_y(p, (int64_t)m * p.ldy + col0 + 16 * j + (ln & 15), s * unscale);
+            store_y(p, (int64_t)m * p.ldy + col, o[0]);
     }
 }
 
@@ -376,7 +393,11 @@ template <class C>
 hipError_t launch_cfg(const GemmProblem &p, hipStream_t stream)
 {
     const size_t lds = skinny_lds<C>(p);
-    skinny_kernel<C><<<dim3((unsigned)(p.n / C::kCols)), C::kThreads, lds, stream>>>(p);
+    const dim3 grid((unsigned)(p.n / C::kCols));
+    if (p.epilogue)
+        skinny_kernel<C, true><<<grid, C::kThreads, lds, stream>>>(p);
+    else
+        skinny_kernel<C, false><<<grid, C::kThreads, lds, stream>>>(p);
     return hipGetLastError();
 }
 

@@ -29,6 +29,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.h"
 #include "internal.h"
 #include "operands.h"
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ void strip_tile(int w, int G, int tm, int tn, int a, 
 }
 
 // (the second bound is the minimum number of waves per SIMD)
-template <int BITS>
+template <int BITS, bool EP>
 __global__ __launch_bounds__(StripCfg<BITS>::kThreads, StripCfg<BITS>::kWavesPerSimd) void
 strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
 {
@@ -310,6 +311,34 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     // the wave's tile; the widening factor (256, 8-bit codes 16) is removed here
     const int64_t y0 = (row0 + 4 * hk) * p.ldy + col0 + wave * 32 + c;
     const int lim = last_row + 1 - 4 * hk; // rows of this lane's group that hold data
+    if constexpr (EP) {
+        const int64_t r0 = (row0 + 4 * hk) * p.ep.ldr + col0 + wave * 32 + c;
+        float res[16];
+        if (p.ep.residual) {
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const int ro = 8 * (r >> 2) + (r & 3);
+                if (ro < lim)
+                    res[r] = ep_load(p.ep.residual, p.ep.residual_bf16, r0 + (int64_t)ro * p.ep.ldr);
+            }
+        }
+        const float bias =
+            p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col0 + wave * 32 + c) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+            acc[r] = acc[r] * C::kUnscale;
+            if (p.ep.bias)
+                acc[r] = acc[r] + bias;
+        }
+        ep_activate(p.ep.act, acc);
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+            const int ro = 8 * (r >> 2) + (r & 3);
+            if (ro < lim)
+                store_y(p, y0 + (int64_t)ro * p.ldy, p.ep.residual ? acc[r] + res[r] : acc[r]);
+        }
+        return;
+    }
 #pragma unroll
     for (int r = 0; r < 16; r++) {
         const int ro = 8 * (r >> 2) + (r & 3);
@@ -352,10 +381,15 @@ hipError_t launch_strip(const GemmProblem &p, hipStream_t stream)
         return hipSuccess;
     int a = 1, rg = tm;
     strip_order(p, tm, tn, a, rg);
-    if (p.act_bits == 4)
-        strip_kernel<4><<<dim3((unsigned)grid), StripCfg<4>::kThreads, 0, stream>>>(p, tm, a, rg);
+    const dim3 g((unsigned)grid);
+    if (p.act_bits == 4 && p.epilogue)
+        strip_kernel<4, true><<<g, StripCfg<4>::kThreads, 0, stream>>>(p, tm, a, rg);
+    else if (p.act_bits == 4)
+        strip_kernel<4, false><<<g, StripCfg<4>::kThreads, 0, stream>>>(p, tm, a, rg);
+    else if (p.epilogue)
+        strip_kernel<8, true><<<g, StripCfg<8>::kThreads, 0, stream>>>(p, tm, a, rg);
     else
-        strip_kernel<8><<<dim3((unsigned)grid), StripCfg<8>::kThreads, 0, stream>>>(p, tm, a, rg);
+        strip_kernel<8, false><<<g, StripCfg<8>::kThreads, 0, stream>>>(p, tm, a, rg);
     return hipGetLastError();
 }
 

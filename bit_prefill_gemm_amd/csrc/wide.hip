@@ -29,6 +29,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.h"
 #include "internal.h"
 #include "operands.h"
 
@@ -60,7 +61,7 @@ struct WideCfg {
     static_assert(2 * kStage <= 160 * 1024, "LDS budget");
 };
 
-template <int TN>
+template <int TN, bool EP>
 __global__ __launch_bounds__(512, 1) void wide_kernel(GemmProblem p, int tiles_m)
 {
     typedef WideCfg<TN> C;
@@ -327,6 +328,40 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(GemmProblem p, int tiles_m
             if (j0 + jj >= TN)
                 continue;
             const float *red = jj == 0 ? red0 : red1;
+            if constexpr (EP) {
+                const int64_t col = col0 + (j0 + jj) * 32 + c;
+                float v4[4], res[4];
+                if (p.ep.residual) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int rl = wm * 32 + M::out_row(hk, 4 * wk + e);
+                        if (rl < rows_valid)
+                            res[e] = ep_load(p.ep.residual, p.ep.residual_bf16,
+                                             (row0 + rl) * p.ep.ldr + col);
+                    }
+                }
+                const float bias = p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int r = 4 * wk + e;
+                    float v = red[((wm * 4 + 0) * 16 + r) * 64 + lane];
+#pragma unroll
+                    for (int w = 1; w < 4; w++)
+                        v += red[((wm * 4 + w) * 16 + r) * 64 + lane];
+                    v4[e] = v * (1.0f / 256.0f);
+                    if (p.ep.bias)
+                        v4[e] = v4[e] + bias;
+                }
+                ep_activate(p.ep.act, v4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int rl = wm * 32 + M::out_row(hk, 4 * wk + e);
+                    if (rl < rows_valid)
+                        store_y(p, (row0 + rl) * p.ldy + col,
+                                p.ep.residual ? v4[e] + res[e] : v4[e]);
+                }
+                continue;
+            }
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const int r = 4 * wk + e;
@@ -351,7 +386,10 @@ hipError_t launch_tn(const GemmProblem &p, hipStream_t stream)
     const int64_t grid = (int64_t)tm * tn;
     if (grid <= 0)
         return hipSuccess;
-    wide_kernel<TN><<<dim3((unsigned)grid), 512, 0, stream>>>(p, tm);
+    if (p.epilogue)
+        wide_kernel<TN, true><<<dim3((unsigned)grid), 512, 0, stream>>>(p, tm);
+    else
+        wide_kernel<TN, false><<<dim3((unsigned)grid), 512, 0, stream>>>(p, tm);
     return hipGetLastError();
 }
 

@@ -58,7 +58,8 @@ extern "C" {
 typedef enum {
     BPG_OK = 0,
     BPG_ERR_NULL = 1,   /* a required pointer is NULL */
-    BPG_ERR_SHAPE = 2,  /* a size is negative, K or N not a multiple of 32, ld too small, ... */
+    BPG_ERR_SHAPE = 2,  /* a size is negative, K or N not a multiple of 32, ld too small, a
+                           number outside its range, ... */
     BPG_ERR_ALIGN = 3,  /* a device pointer or leading dimension breaks the alignment rule */
     BPG_ERR_DTYPE = 4,  /* unknown dtype or source kind, or act_bits not 4 or 8 */
     BPG_ERR_STAMP = 5,  /* weight descriptor not made by this library's packers, wrong
@@ -80,8 +81,22 @@ typedef enum {
                                   pack_weights_unrotated only */
 } bpg_src_kind;
 
-/* Activation dtype of quantize_act_h32. */
+/* Activation dtype of quantize_act_h32 (and every float tensor whose type a
+   call names). */
 typedef enum { BPG_X_F32 = 0, BPG_X_BF16 = 1 } bpg_x_dtype;
+
+/* Activation of w4a4_gemm_epilogue. */
+typedef enum {
+    BPG_ACT_NONE = 0,
+    BPG_ACT_RELU = 1,      /* max(t, 0) */
+    BPG_ACT_SILU = 2,      /* t / (1 + e^-t) */
+    BPG_ACT_GELU = 3,      /* t (1 + erf(t / sqrt 2)) / 2 */
+    BPG_ACT_GELU_TANH = 4  /* t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2 */
+} bpg_activation;
+
+/* Scores and group scores of moe_route_topk. */
+typedef enum { BPG_SCORE_SOFTMAX = 0, BPG_SCORE_SIGMOID = 1 } bpg_score;
+typedef enum { BPG_GROUP_MAX = 0, BPG_GROUP_TOP2 = 1 } bpg_group_score;
 
 #define BPG_WEIGHTS_MAGIC 0x57475042u /* "BPGW" little-endian */
 #define BPG_WEIGHTS_VERSION 1u
@@ -233,6 +248,59 @@ bpg_status w4a4_gemm_rot(const void *codes, const float *scales, int act_bits, i
                          int64_t ldy, void *stream);
 
 /*
+ * RMSNorm with the residual's addition, feeding the quantizer, on the GPU
+ * ("509 tokens a second of prompt: the Hadamard route ships", section "The
+ * rotation": the rotation runs inside the step that quantizes activations;
+ * in a pre-norm block what is quantized is the norm of the residual stream.
+ * The pages give no detail of the norm, so the steps are this library's
+ * reading).  Per row of k values:
+ *   h_i = x_i + r_i, one fp32 addition, rounded to the type of the residual
+ *         (the stream); without a residual h is x.  The norm is that of the
+ *         stored value;
+ *   s   = 1 / sqrt(sum_i h_i^2 / k + eps) in fp64, rounded to fp32;
+ *   v_i = (h_i * s) * g_i, two fp32 roundings (g = weight, 1 without one);
+ * then v is rotated over spans of `rotation` = 32, 64 or 128 values (0: not
+ * rotated) and quantized exactly as quantize_act_rot (quantize_act_unrotated)
+ * does with fp32 input.
+ *
+ *   x         device, [m][ldx] of x_dt
+ *   residual  device, [m][ldr] of residual_dt, or NULL (residual_dt, ldr, h
+ *             and ldh are then not used)
+ *   h         device, [m][ldh] of residual_dt, receives the new stream, or
+ *             NULL (not written); may be residual itself (ldh = ldr), must
+ *             not overlap it or x otherwise
+ *   weight    device, [k] of weight_dt, or NULL
+ *   eps       finite and > 0 (else SHAPE)
+ *   codes, scales  as quantize_act_rot writes them
+ * Limits: k <= 65536 and a multiple of 32 and of the span; ldx, ldr and ldh
+ * multiples of 4; pointers 16-byte aligned.  NaN or Inf in a row gives
+ * unspecified codes of that row.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ */
+bpg_status rmsnorm_quantize_act(const void *x, bpg_x_dtype x_dt, int64_t ldx,
+                                const void *residual, bpg_x_dtype residual_dt, int64_t ldr,
+                                void *h, int64_t ldh, const void *weight, bpg_x_dtype weight_dt,
+                                float eps, int64_t m, int64_t k, int act_bits, int rotation,
+                                void *codes, float *scales, void *stream);
+
+/*
+ * The values that codes and scales stand for, on the GPU: the inverse of
+ * quantize_act_h32 / _rot / _unrotated up to their rounding ("509 tokens a
+ * second of prompt: the Hadamard route ships", section "The rotation": the
+ * transform is orthogonal; its matrix is symmetric, so it is its own
+ * inverse).  v = code * scale, one fp32 multiplication, then rotated back
+ * with the butterflies and the factor of quantize_act_rot (rotation 0: not
+ * rotated), rounded once to y's type.
+ *
+ *   codes, scales  device, as the quantizers write them for m rows of k values
+ *   y              device, [m][ldy] of y_dt, ldy >= k, ldy % 4 == 0, overwritten
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ */
+bpg_status dequantize_act(const void *codes, const float *scales, int act_bits, int rotation,
+                          int64_t m, int64_t k, void *y, bpg_x_dtype y_dt, int64_t ldy,
+                          void *stream);
+
+/*
  * Dense W4A4 (or W4A8) product y = x . W^T from codes, on the GPU
  * ("509 tokens a second of prompt: the Hadamard route ships", section
  * "Why prompts are a matrix-unit problem").
@@ -246,6 +314,43 @@ bpg_status w4a4_gemm_rot(const void *codes, const float *scales, int act_bits, i
 bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64_t m,
                      const bpg_weights_desc *w, const void *w_dev, float *y, int64_t ldy,
                      void *stream);
+
+/*
+ * The dense product with bias, activation and residual in its epilogue
+ * ("509 tokens a second of prompt: the Hadamard route ships", section "Why
+ * prompts are a matrix-unit problem": the scales are applied in fp32 after
+ * the integer products; what a block does to the result before it is stored
+ * joins them there).  With t = the fp32 result of w4a4_gemm (w4a4_gemm_rot,
+ * w4a4_gemm_unrotated for rotation 64 / 128, 0):
+ *   y = act(t + bias[column]) + residual[row][column]
+ * each step in fp32 (the exponential, erf and division of an activation
+ * within a few units in the last place), rounded once to y's type.  With no
+ * bias, BPG_ACT_NONE and no residual every element equals w4a4_gemm's (or its
+ * bf16 rounding).
+ *
+ *   rotation  0, 32, 64 or 128: the span of the codes; the image's stamp must
+ *             record the same (else STAMP)
+ *   ep        host, not NULL; read during the call only
+ *   y         device, [m][ldy] of y_dt; fp32: ldy % 4 == 0, bf16: ldy % 8 == 0
+ * Other arguments as w4a4_gemm; the kernel is the one that
+ * w4a4_gemm_kernel_name names.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, STAMP, DEVICE, LAUNCH.
+ */
+typedef struct {
+    const void *bias;         /* device, [n] of bias_dt, aligned to its type; or NULL */
+    const void *residual;     /* device, [m][ldr] of residual_dt, aligned to its type;
+                                 or NULL.  May be y itself (same type, ldr = ldy),
+                                 must not overlap it otherwise */
+    int64_t ldr;              /* >= n; not used without a residual */
+    bpg_x_dtype bias_dt;
+    bpg_x_dtype residual_dt;
+    bpg_activation act;
+} bpg_epilogue;
+
+bpg_status w4a4_gemm_epilogue(const void *codes, const float *scales, int act_bits, int rotation,
+                              int64_t m, const bpg_weights_desc *w, const void *w_dev,
+                              const bpg_epilogue *ep, void *y, bpg_x_dtype y_dt, int64_t ldy,
+                              void *stream);
 
 /*
  * Grouped (MoE) product over ragged expert row ranges, on the GPU
@@ -295,11 +400,43 @@ bpg_status w4a4_grouped_gemm_bf16(const void *codes, const float *scales, int ac
  * covers the expert matmuls; the pages give no detail of the layer around
  * them, so the steps below are this library's reading).  A layer of T tokens,
  * each routed to topk experts (entry t*topk + j), runs as
- *   moe_route_sort -> quantize_act_h32 (T token rows, once)
+ *   moe_route_topk -> moe_route_sort -> quantize_act_h32 or
+ *   rmsnorm_quantize_act (T token rows, once)
  *   -> w4a4_grouped_gemm_gather (gate and up projections, rows gathered by
  *      token) -> swiglu_quantize_h32 -> w4a4_grouped_gemm (down projection)
  *   -> moe_combine.
  *
+ * moe_route_topk: the topk experts of every token and their weights, from a
+ * router's logits.  Per token, over its logits l (a NaN counts as -inf, +inf
+ * as the largest fp32):
+ *   p = softmax(l) or 1 / (1 + e^-l); a row of -inf only has softmax scores 0;
+ *   key = p + bias (the bias moves the choice only; a NaN key counts as -inf);
+ *   with groups > 1, consecutive runs of experts / groups experts form the
+ *   groups; a group's score is its largest key or the sum of its two largest;
+ *   the experts of the topk_groups best groups take part in the choice;
+ *   the topk experts of the largest keys, the largest first;
+ *   weight = p (renormalize: p / the sum of the chosen p, 0 if that sum is 0)
+ *   * scale, rounded to fp32 once.
+ * Scores, keys, group scores and sums are fp64 (softmax without a bias and
+ * with one group compares the logits themselves, which gives the same order);
+ * ties go to the lowest group and the lowest expert.
+ *   logits_dev      device, [tokens][ldl] of dt, aligned to its type, ldl >= experts
+ *   bias_dev        device, fp32 [experts], or NULL
+ *   expert_of_dev   device, int32 [tokens*topk], as moe_route_sort takes it
+ *   weights_dev     device, fp32 [tokens*topk], as moe_combine takes it
+ * Limits: experts <= 512, topk <= 64, groups <= 64 and a divisor of experts,
+ * 1 <= topk_groups <= groups, topk <= topk_groups * (experts / groups),
+ * BPG_GROUP_TOP2 with groups of two experts at least (where groups > 1),
+ * tokens*topk <= 2^20, scale finite.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ */
+bpg_status moe_route_topk(const void *logits_dev, bpg_x_dtype dt, int64_t tokens, int64_t experts,
+                          int64_t ldl, bpg_score score, const float *bias_dev, int64_t groups,
+                          int64_t topk_groups, bpg_group_score group_score, int64_t topk,
+                          int renormalize, float scale, int32_t *expert_of_dev,
+                          float *weights_dev, void *stream);
+
+/*
  * moe_route_sort: sorts the entries by expert, stably (entry order inside an
  * expert), on the GPU (one workgroup per expert, each reading every entry).
  *   expert_of_dev   device, int32 [tokens*topk]; ids outside [0, experts) are

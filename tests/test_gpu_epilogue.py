@@ -1,0 +1,214 @@
+"""The dense product with bias, activation and residual in its epilogue.
+
+Bars: with an empty epilogue every element equals w4a4_gemm's (or its bf16
+rounding) bit for bit, on every kernel a dense product runs; otherwise each
+element lies within the fp32 bound of the product, carried through the
+activation's slope, plus the roundings of the epilogue's own steps, of the
+64-bit formula on the oracle's product.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from bit_prefill_gemm_amd import binding as bb
+from bit_prefill_gemm_amd import synth
+
+from gpu_util import act_to_device, fp32_bound, oracle_codes, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+# m, k, n, bits, kernel: every kernel family, odd rows, K that ends inside a group and a stage
+CASES = [
+    (1, 1024, 96, 4, "weight-stream"), (1, 1056, 64, 8, "weight-stream"),
+    (16, 2080, 160, 4, "weight-stream"), (17, 1024, 128, 8, "weight-stream"),
+    (31, 96, 64, 4, "weight-stream"), (13, 32800, 32, 4, "tiled 16x32"),
+    (9, 32800, 64, 8, "tiled 16x32"),
+    (33, 416, 128, 4, "strip 32x128"), (100, 1056, 256, 8, "strip 32x128"),
+    (512, 544, 5120, 4, "wide 64x160"), (449, 160, 5120, 8, "tiled 64x160"),
+    (96, 1024, 320, 4, "tiled 64x32"), (77, 2080, 1056, 8, "tiled 64x32"),
+    (1000, 96, 4032, 8, "tiled 64x64"),
+]
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_mod()
+    if not t.cuda.is_available():
+        pytest.skip("no GPU")
+    return t
+
+
+def host(t):
+    torch = torch_mod()
+    t = t.cpu().contiguous()
+    return synth.bf16_to_f32(t.view(torch.int16).numpy().view(np.uint16)) if t.dtype == torch.bfloat16 else t.numpy()
+
+
+_made = {}
+
+
+def problem(m, k, n, bits, rotation=32):
+    """Codes, image, and the oracle's product (fp64) with its absolute sum, made once a shape."""
+    torch = torch_mod()
+    key = (m, k, n, bits, rotation)
+    if key not in _made:
+        rng = np.random.default_rng(m + k + n + bits)
+        x = rng.standard_normal((m, k)).astype(np.float32)
+        q, d, _ = oracle.quantize(x, bits)
+        # unit-sized results, so that activations are met where they bend
+        blocks = synth.draw_q4_0(rng, (n,), k, 0.02 / math.sqrt(k), 0.6 / math.sqrt(k))
+        pack = bb.pack_weights_unrotated if rotation == 0 else bb.rotate_pack_weights
+        kind = bb.SRC_Q4_0 if rotation == 0 else bb.SRC_Q4_0_ROTATED
+        W = pack(blocks, kind, n, k).to("cuda")
+        w, dw = oracle.q4_0_decode(blocks, k)
+        codes = torch.from_numpy(oracle_codes(q, bits)).cuda()
+        scales = torch.from_numpy(d).cuda()
+        ref = oracle.gemm_rect(q, d, w, dw, 0, m, 0, n)
+        mag = oracle.gemm_abs_rect(q, d, w, dw, 0, m, 0, n)
+        _made[key] = codes, scales, W, ref, mag
+    return _made[key]
+
+
+def erf64(x):
+    return np.vectorize(math.erf, otypes=[np.float64])(x)
+
+
+def act64(t, act):
+    if act == "relu":
+        return np.maximum(t, 0.0)
+    if act == "silu":
+        return t / (1.0 + np.exp(-t))
+    if act == "gelu":
+        return 0.5 * t * (1.0 + erf64(t / math.sqrt(2.0)))
+    if act == "gelu_tanh":
+        return 0.5 * t * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (t + 0.044715 * t ** 3)))
+    return t
+
+
+def limit(mag, k, t, y, out, act, bias, residual):
+    """The element-wise bound.  t carries the product's fp32 bound and the bias's rounding; an
+    activation's slope is at most 1.13; its own steps (an exponential or erf within 2 ulp, a sum,
+    a quotient, a product, and for the tanh form the argument's four roundings, which enter
+    through |z| sigmoid'(z) <= 0.23) stay below 12 2^-24 |t|; the residual's addition and the
+    output's rounding are half a step each."""
+    u = 2.0 ** -24
+    lim = fp32_bound(mag, k)
+    if bias:
+        lim = lim + u * np.abs(t)
+    if act not in ("none", "relu"):
+        lim = 1.13 * lim + 12 * u * np.abs(t)
+    if residual:
+        lim = lim + u * np.abs(y)
+    lim = lim * (1 + 2.0 ** -16)
+    return lim if out == "fp32" else lim + 2.0 ** -8 * (np.abs(y) + lim)
+
+
+def check(torch, case, act="none", bias=None, residual=None, out="fp32", pads=(0, 0), in_place=False):
+    m, k, n, bits = case[:4]
+    codes, scales, W, ref, mag = problem(m, k, n, bits)
+    assert bb.w4a4_gemm_kernel_name(bits, m, W) == case[4]
+    print("epilogue", case, act, bias, residual, out, flush=True)
+    rng = np.random.default_rng(n + m)
+    types = {"fp32": torch.float32, "bf16": torch.bfloat16}
+    b = r = None
+    if bias:
+        b = torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda().to(types[bias])
+    if residual:
+        r = torch.full((m, n + pads[0]), 7.0, dtype=types[residual], device="cuda")
+        r[:, :n] = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).cuda()
+        r = r[:, :n]
+    t = ref + (0.0 if b is None else host(b).astype(np.float64))
+    y64 = act64(t, act) + (0.0 if r is None else host(r).astype(np.float64))
+    wide = r if in_place else torch.full((m, n + pads[1]), 5.0, dtype=types[out], device="cuda")
+    y = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=b, activation=act, residual=r, y=wide[:, :n])
+    torch.cuda.synchronize()
+    if not in_place:
+        assert (wide[:, n:] == 5.0).all()
+        if r is not None and pads[0]:
+            assert (r.as_strided((m, n + pads[0]), r.stride())[:, n:] == 7.0).all()
+    err = np.abs(host(y).astype(np.float64) - y64)
+    lim = limit(mag, k, t, y64, out, act, b is not None, r is not None)
+    bad = np.argwhere(~(err <= lim))
+    assert bad.size == 0, "%d elements, first %s: %g > %g" % (
+        len(bad), bad[0].tolist(), err[tuple(bad[0])], lim[tuple(bad[0])])
+
+
+@pytest.mark.parametrize("case", CASES, ids=["%dx%dx%d-%d" % c[:4] for c in CASES])
+def test_empty_epilogue_is_the_product(torch, case):
+    m, k, n, bits, kernel = case
+    codes, scales, W, _, _ = problem(m, k, n, bits)
+    assert bb.w4a4_gemm_kernel_name(bits, m, W) == kernel
+    assert torch.equal(bb.w4a4_gemm_epilogue(codes, scales, bits, W), bb.w4a4_gemm(codes, scales, bits, W))
+    assert torch.equal(bb.w4a4_gemm_epilogue(codes, scales, bits, W, dtype=torch.bfloat16),
+                       bb.w4a4_gemm_bf16(codes, scales, bits, W))
+
+
+@pytest.mark.parametrize("case", CASES, ids=["%dx%dx%d-%d" % c[:4] for c in CASES])
+def test_every_step_on_every_kernel(torch, case):
+    check(torch, case, "silu", "fp32", "bf16", "bf16")
+    check(torch, case, "gelu", "bf16", "fp32", "fp32", pads=(3, 16))
+    check(torch, case, "gelu_tanh", "fp32", None, "fp32")
+    check(torch, case, "relu", None, "fp32", "bf16", pads=(5, 8))
+    check(torch, case, "none", "bf16", "bf16", "fp32", pads=(1, 4))
+    # the residual stream updated where it is
+    check(torch, case, "none", None, "bf16", "bf16", in_place=True)
+    check(torch, case, "silu", "fp32", "fp32", "fp32", in_place=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("kind", [None, "fp32", "bf16"])
+def test_activations_and_types(torch, act, kind):
+    for case in (CASES[3], CASES[7]):
+        check(torch, case, act, kind, None, "fp32")
+        check(torch, case, act, None, kind, "bf16")
+
+
+def test_activations_far_out(torch):
+    """Arguments far from zero: the activations reach 0 and x, never NaN, and stay as exact as near zero."""
+    case = CASES[7]
+    m, k, n, bits = case[:4]
+    codes, scales, W, ref, mag = problem(m, k, n, bits)
+    bias = torch.linspace(-200.0, 200.0, n, device="cuda")
+    bias[0], bias[1], bias[2], bias[3] = -3e38, 3e38, -90.0, -104.0
+    t = ref + host(bias).astype(np.float64)
+    for act in ("relu", "silu", "gelu", "gelu_tanh"):
+        y = host(bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=bias, activation=act)).astype(np.float64)
+        with np.errstate(over="ignore", invalid="ignore"):
+            y64 = act64(t, act)
+        y64 = np.where(np.isnan(y64), 0.0, y64)
+        big = np.abs(t) > 1e30
+        lim = limit(mag, k, t, y64, "fp32", act, True, False)
+        assert (np.abs(y - y64)[~big] <= lim[~big]).all(), act
+        assert (np.abs(y - y64)[big] <= 1e-6 * np.abs(t[big])).all(), act
+
+
+def test_unrotated_and_stamps(torch):
+    m, k, n, bits = 5, 256, 64, 4
+    codes, scales, W, ref, mag = problem(m, k, n, bits, rotation=0)
+    y = host(bb.w4a4_gemm_epilogue(codes, scales, bits, W, rotation=0))
+    assert (np.abs(y - ref) <= fp32_bound(mag, k) * (1 + 2.0 ** -20)).all()
+    assert np.array_equal(y, host(bb.w4a4_gemm_unrotated(codes, scales, bits, W)))
+    for rotation in (32, 64, 128):
+        with pytest.raises(bb.BpgError) as e:
+            bb.w4a4_gemm_epilogue(codes, scales, bits, W, rotation=rotation)
+        assert e.value.status == 5
+
+
+def test_rows_behind_stay(torch):
+    """Rows of y and of the residual behind the last token are not touched."""
+    for case in (CASES[2], CASES[7], CASES[9], CASES[12]):
+        m, k, n, bits = case[:4]
+        codes, scales, W, _, _ = problem(m, k, n, bits)
+        y = torch.full((m + 40, n), 9.0, device="cuda")
+        bb.w4a4_gemm_epilogue(codes, scales, bits, W, residual=y[:m], y=y[:m], activation="silu")
+        assert (y[m:] == 9.0).all()
+
+
+def test_no_rows(torch):
+    _, _, W, _, _ = problem(5, 256, 64, 4)
+    y = bb.w4a4_gemm_epilogue(torch.empty(0, 128, dtype=torch.uint8, device="cuda"),
+                              torch.empty(0, 8, device="cuda"), 4, W,
+                              residual=torch.empty(0, 64, device="cuda"), bias=torch.zeros(64, device="cuda"))
+    assert y.shape == (0, 64)
