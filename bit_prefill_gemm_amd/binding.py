@@ -22,9 +22,6 @@ STATUS_NAMES = {0: "BPG_OK", 1: "BPG_ERR_NULL", 2: "BPG_ERR_SHAPE", 3: "BPG_ERR_
 
 SRC_F32, SRC_BF16, SRC_Q4_0_ROTATED, SRC_Q4_0 = 0, 1, 2, 3
 X_F32, X_BF16 = 0, 1
-ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-SCORES = {"softmax": 0, "sigmoid": 1}
-GROUP_SCORES = {"max": 0, "top2": 1}
 
 ENTRY_POINTS = ("bpg_status_str", "rotate_pack_weights_bytes", "rotate_pack_weights",
                 "quantize_act_h32", "w4a4_gemm", "w4a4_grouped_gemm", "w4a4_gemm_blocksums",
@@ -595,72 +592,36 @@ def w4a4_gemm_rot(codes, scales, act_bits: int, rotation: int, w: Weights, y=Non
 
 
 # ------------------------------------------------------------------ between the products
+#
+# These four come between the products of one token, where host time counts:
+# their tensor checks, output allocation and C ABI call are compiled
+# (csrc/native.cpp).
 
-def _empty(stream, shape, dtype, device):
-    """A new output tensor, allocated on the stream that writes it (the allocator may hand out
-    memory that earlier work of that stream still uses)."""
+_native_mod = None
+
+
+def _native():
+    global _native_mod
+    if _native_mod is None:
+        _lib_handle()
+        _torch()  # its libraries are what the extension links to
+        try:
+            from . import _native as mod
+        except ImportError as e:
+            raise RuntimeError("_native.so is not built (run __graft_entry__.build() or python "
+                               "bit_prefill_gemm_amd/build.py); there is no fallback path") from e
+        mod.set_error(BpgError)
+        _native_mod = mod
+    return _native_mod
+
+
+def _on(stream, where, tensor, call, *args):
+    """call(*args) with `stream` current: outputs are then allocated for that stream too."""
     torch = _torch()
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(tensor, torch.Tensor) and tensor.device != stream.device:
+        _fail(where, "the stream is on %s, the tensors on %s" % (stream.device, tensor.device))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _launch(name, stream, dev, *args):
-    """Call entry point `name` on `stream` (the current stream of device `dev` if None), with
-    that device current: the library launches on the current device."""
-    torch = _torch()
-    fn = getattr(_lib_handle(), name)
-    if stream is not None and stream.device.index != dev:
-        _fail(name, "the stream is on device %s, the tensors on %s" % (stream.device.index, dev))
-    handle = _stream_handle(stream, dev)
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    _check(st, name)
-
-
-def _float_code(where, name, dtype):
-    """BPG_X_F32 / BPG_X_BF16 of a torch dtype."""
-    torch = _torch()
-    if dtype == torch.bfloat16:
-        return X_BF16
-    if dtype != torch.float32:
-        _fail(where, "%s has dtype %s, expected torch.float32 or torch.bfloat16" % (name, dtype))
-    return X_F32
-
-
-def _rows_in(where, name, t, shape=None):
-    """A float matrix with unit column stride and rows that do not overlap; returns its dtype code."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
-        _fail(where, "%s must be a 2-D tensor" % name)
-    code = _float_code(where, name, t.dtype)
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        _fail(where, "%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
-    if rows > 0 and cols > 0:
-        s0, s1 = t.stride()
-        if s1 != 1 or (rows > 1 and s0 < cols):
-            _fail(where, "%s must have unit column stride and row stride >= %d" % (name, cols))
-    return code
-
-
-def _row_stride(t, unit):
-    """The leading dimension of a float matrix: that of a single row is free, so the smallest
-    multiple of `unit` elements that holds it."""
-    if t.shape[0] > 1:
-        return t.stride(0)
-    return -(-t.shape[1] // unit) * unit
-
-
-def _check_span(where, rotation, k):
-    if rotation not in (0, 32, 64, 128):
-        _fail(where, "rotation must be 0, 32, 64 or 128, got %r" % (rotation,))
-    if k <= 0 or k % (rotation or 32) != 0:
-        _fail(where, "K = %d is not a positive multiple of %d" % (k, rotation or 32))
+        return call(*args)
 
 
 def rmsnorm_quantize_act(x, residual=None, weight=None, eps: float = 1e-6, act_bits: int = 4,
@@ -669,133 +630,49 @@ def rmsnorm_quantize_act(x, residual=None, weight=None, eps: float = 1e-6, act_b
     or bfloat16, each its own); weight: [K].  Returns (h, codes, scales); h is the new residual
     stream x + residual in the residual's type (it may be given as `residual` itself), or x when
     there is no residual."""
-    torch = _torch()
-    where = "rmsnorm_quantize_act"
-    x_dt = _rows_in(where, "x", x)
-    _check_bits(where, act_bits)
-    m, k = x.shape
-    _check_span(where, rotation, k)
-    r_dt = w_dt = 0
-    if residual is not None:
-        r_dt = _rows_in(where, "residual", residual, (m, k))
-        if h is None:
-            h = _empty(stream, (m, k), dtype=residual.dtype, device=x.device)
-        else:
-            _rows_in(where, "h", h, (m, k))
-            if h.dtype != residual.dtype:
-                _fail(where, "h has dtype %s, the residual %s" % (h.dtype, residual.dtype))
-    elif h is not None:
-        _fail(where, "h needs a residual (without one the stream is x)")
-    if weight is not None:
-        if not isinstance(weight, torch.Tensor):
-            _fail(where, "weight must be a torch tensor")
-        w_dt = _float_code(where, "weight", weight.dtype)
-        _tensor(where, "weight", weight, (weight.dtype,), (k,))
-    if codes is None:
-        codes = _empty(stream, (m, _code_cols(k, act_bits)), dtype=torch.uint8, device=x.device)
-    if scales is None:
-        scales = _empty(stream, (m, k // 32), dtype=torch.float32, device=x.device)
-    _check_codes(where, codes, scales, act_bits, m, k)
-    dev = _same_device(where, x, residual, h, weight, codes, scales)
-    _launch(
-        where, stream, dev, _dptr(x), x_dt, _row_stride(x, 4), _dptr(residual), r_dt,
-        0 if residual is None else _row_stride(residual, 4), _dptr(h),
-        0 if h is None else _row_stride(h, 4), _dptr(weight), w_dt, eps, m, k, act_bits, rotation,
-        _dptr(codes), _dptr(scales))
-    return (x if residual is None else h), codes, scales
+    call = _native().rmsnorm_quantize_act
+    if stream is not None:
+        return _on(stream, "rmsnorm_quantize_act", x, call, x, residual, weight, eps, act_bits,
+                   rotation, h, codes, scales)
+    return call(x, residual, weight, eps, act_bits, rotation, h, codes, scales)
 
 
 def dequantize_act(codes, scales, act_bits: int = 4, rotation: int = 32, y=None, dtype=None,
                    stream=None):
     """The values that codes and scales stand for, rotated back: [rows, K] of `dtype` (float32
     unless y or dtype says bfloat16)."""
-    torch = _torch()
-    where = "dequantize_act"
-    if not isinstance(scales, torch.Tensor) or scales.dim() != 2:
-        _fail(where, "scales must be a 2-D tensor")
-    m, k = scales.shape[0], scales.shape[1] * 32
-    _check_codes(where, codes, scales, act_bits, m, k)
-    _check_span(where, rotation, k)
-    if y is None:
-        y = _empty(stream, (m, k), dtype=dtype or torch.float32, device=codes.device)
-    elif dtype is not None and y.dtype != dtype:
-        _fail(where, "y has dtype %s, expected %s" % (y.dtype, dtype))
-    y_dt = _rows_in(where, "y", y, (m, k))
-    dev = _same_device(where, codes, scales, y)
-    _launch(where, stream, dev, _dptr(codes), _dptr(scales), act_bits, rotation, m, k, _dptr(y),
-            y_dt, _row_stride(y, 4))
-    return y
+    call = _native().dequantize_act
+    if stream is not None:
+        return _on(stream, "dequantize_act", codes, call, codes, scales, act_bits, rotation, y,
+                   dtype)
+    return call(codes, scales, act_bits, rotation, y, dtype)
 
 
 def w4a4_gemm_epilogue(codes, scales, act_bits: int, w: Weights, bias=None,
                        activation: str = "none", residual=None, y=None, dtype=None,
                        rotation: int = 32, stream=None):
     """act(x . W^T + bias) + residual, of `dtype` (float32 unless y or dtype says bfloat16).
-    bias: [N], residual: [M, N] (float32 or bfloat16, each its own; the residual may be y)."""
-    torch = _torch()
-    where = "w4a4_gemm_epilogue"
-    if y is not None and not isinstance(y, torch.Tensor):
-        _fail(where, "y must be a torch tensor")
-    if dtype is None:
-        dtype = torch.float32 if y is None else y.dtype
-    y_dt = _float_code(where, "y", dtype)
-    act = ACTIVATIONS.get(activation)
-    if act is None:
-        _fail(where, "activation must be one of %s, got %r" % (", ".join(ACTIVATIONS), activation))
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
-        _fail(where, "codes must be a 2-D tensor")
-    m, n = codes.shape[0], w.n
-    _check_codes(where, codes, scales, act_bits, m, w.k)
-    _check_image(where, w)
-    if y is None:
-        y = _empty(stream, (m, n), dtype=dtype, device=codes.device)
-    _rows_out(where, "y", y, dtype, m, n)
-    ep = Epilogue(act=act)
-    if bias is not None:
-        if not isinstance(bias, torch.Tensor):
-            _fail(where, "bias must be a torch tensor")
-        ep.bias_dt = _float_code(where, "bias", bias.dtype)
-        _tensor(where, "bias", bias, (bias.dtype,), (n,))
-        ep.bias = bias.data_ptr()
-    if residual is not None:
-        ep.residual_dt = _rows_in(where, "residual", residual, (m, n))
-        ep.residual = residual.data_ptr()
-        ep.ldr = _row_stride(residual, 1)
-    dev = _same_device(where, codes, scales, w.image, y, bias, residual)
-    _launch(where, stream, dev, _dptr(codes), _dptr(scales), act_bits, rotation, m,
-            ctypes.byref(w.desc), _dptr(w.image), ctypes.byref(ep), _dptr(y), y_dt,
-            _row_stride(y, 8))
-    return y
+    activation: none, relu, silu, gelu or gelu_tanh; bias: [N], residual: [M, N] (float32 or
+    bfloat16, each its own; the residual may be y)."""
+    call = _native().w4a4_gemm_epilogue
+    desc = w.desc
+    stamp = ctypes.addressof(desc)
+    if stream is not None:
+        return _on(stream, "w4a4_gemm_epilogue", codes, call, codes, scales, act_bits, stamp,
+                   w.image, bias, activation, residual, y, dtype, rotation)
+    return call(codes, scales, act_bits, stamp, w.image, bias, activation, residual, y, dtype,
+                rotation)
 
 
 def moe_route_topk(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1,
                    topk_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
                    scale: float = 1.0, expert_of=None, weights=None, stream=None):
-    """logits: cuda [tokens, experts] (float32 or bfloat16, unit stride along experts); bias:
-    float32 [experts].  Returns (expert_of int32, weights float32), both [tokens*topk], as
-    moe_route_sort and moe_combine take them."""
-    torch = _torch()
-    where = "moe_route_topk"
-    dt = _rows_in(where, "logits", logits)
-    tokens, experts = logits.shape
-    if score not in SCORES:
-        _fail(where, "score must be softmax or sigmoid, got %r" % (score,))
-    if group_score not in GROUP_SCORES:
-        _fail(where, "group_score must be max or top2, got %r" % (group_score,))
-    if topk < 1:
-        _fail(where, "topk must be positive, got %r" % (topk,))
-    if bias is not None:
-        _tensor(where, "bias", bias, (torch.float32,), (experts,))
-    n = tokens * topk
-    if expert_of is None:
-        expert_of = _empty(stream, n, dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = _empty(stream, n, dtype=torch.float32, device=logits.device)
-    _tensor(where, "expert_of", expert_of, (torch.int32,), (n,))
-    _tensor(where, "weights", weights, (torch.float32,), (n,))
-    dev = _same_device(where, logits, bias, expert_of, weights)
-    _launch(
-        where, stream, dev, _dptr(logits), dt, tokens, experts, _row_stride(logits, 1), SCORES[score], _dptr(bias),
-        groups, topk_groups, GROUP_SCORES[group_score], topk, int(bool(renormalize)), scale,
-        _dptr(expert_of), _dptr(weights))
-    return expert_of, weights
+    """logits: cuda [tokens, experts] (float32 or bfloat16, unit stride along experts); score:
+    softmax or sigmoid; bias: float32 [experts]; group_score: max or top2.  Returns (expert_of
+    int32, weights float32), both [tokens*topk], as moe_route_sort and moe_combine take them."""
+    call = _native().moe_route_topk
+    if stream is not None:
+        return _on(stream, "moe_route_topk", logits, call, logits, topk, score, bias, groups,
+                   topk_groups, group_score, renormalize, scale, expert_of, weights)
+    return call(logits, topk, score, bias, groups, topk_groups, group_score, renormalize, scale,
+                expert_of, weights)

@@ -1,4 +1,5 @@
-"""Build the HIP library libbpg.so in place (gfx950).
+"""Build the HIP library libbpg.so in place (gfx950), and _native.so, the
+compiled Python entry points over it.
 
 Every source is compiled with -ffp-contract=off (the quantizer must not fuse
 its adds and multiplies) and with packed fp32 instructions disabled.
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libbpg.so")
+NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "skinny.hip", "wide.hip", "strip.hip", "grouped.hip", "moe.hip",
            "norm.hip", "route.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -39,13 +42,34 @@ def _run(cmd):
     return err
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _native_commands(obj, out):
+    """Compile and link commands of the Python extension (host code over libbpg.so and torch)."""
+    torch_dir = _torch_dir()
+    compile_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
+                   "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE,
+                   "-isystem", os.path.join(torch_dir, "include"),
+                   "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
+                   "-c", os.path.join(CSRC, "native.cpp"), "-o", obj]
+    link_cmd = ["g++", "-shared", obj, "-o", out, "-L", HERE, "-l:libbpg.so",
+                "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    return compile_cmd, link_cmd
+
+
 def build(verbose: bool = False) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = [os.path.join(objdir, s.replace(".hip", ".o")) for s in SOURCES]
     cmds = [[HIPCC, *FLAGS, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
-    with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
-        outs = list(ex.map(_run, cmds))
+    native_tmp = NATIVE + ".tmp%d" % os.getpid()
+    native_cmd, native_link = _native_commands(os.path.join(objdir, "native.o"), native_tmp)
+    with ThreadPoolExecutor(max_workers=len(cmds) + 1) as ex:
+        outs = list(ex.map(_run, cmds + [native_cmd]))
     if verbose:
         for o in outs:
             if o.strip():
@@ -53,6 +77,8 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
     os.replace(tmp, LIB)
+    _run(native_link)
+    os.replace(native_tmp, NATIVE)
     return LIB
 
 
