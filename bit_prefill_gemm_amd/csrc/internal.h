@@ -53,6 +53,8 @@ struct RouteProblem {
     int experts, topk, groups, kept;
     float scale;
     bool logits_bf16, sigmoid, pair, renormalize;
+    uint32_t size_magic; // set by the launcher: ceil(2^20 / group size),
+    int lanes_shift;     // and log2 of the lanes that share a group
 };
 hipError_t launch_route_topk(const RouteProblem &p, hipStream_t stream);
 

@@ -417,8 +417,9 @@ bpg_status w4a4_grouped_gemm_bf16(const void *codes, const float *scales, int ac
  *   the topk experts of the largest keys, the largest first;
  *   weight = p (renormalize: p / the sum of the chosen p, 0 if that sum is 0)
  *   * scale, rounded to fp32 once.
- * Scores, keys, group scores and sums are fp64 (softmax without a bias and
- * with one group compares the logits themselves, which gives the same order);
+ * Scores, keys, group scores and sums are fp64; both scores are monotone, so
+ * without a bias the logits are compared as keys (a group's sum of two stays
+ * that of its two best experts' scores); a NaN group score counts as -inf;
  * ties go to the lowest group and the lowest expert.
  *   logits_dev      device, [tokens][ldl] of dt, aligned to its type, ldl >= experts
  *   bias_dev        device, fp32 [experts], or NULL

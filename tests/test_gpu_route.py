@@ -43,12 +43,14 @@ def reference(l, topk, score, bias, groups, kept, pair, renorm, scale):
             key = p + bias.astype(np.float64)
             key = np.where(np.isnan(key), -np.inf, key)
         else:
-            key = l[i] if score == "softmax" and groups == 1 else p
+            key = l[i]
         member = np.arange(e)
         if groups > 1:
             size = e // groups
-            by = np.sort(key.reshape(groups, size), axis=1)
-            g = by[:, -1] + by[:, -2] if pair else by[:, -1]
+            by = np.sort((key if bias is not None or not pair else p).reshape(groups, size), axis=1)
+            with np.errstate(invalid="ignore"):
+                g = by[:, -1] + by[:, -2] if pair else by[:, -1]
+            g = np.where(np.isnan(g), -np.inf, g)
             chosen = np.argsort(-g, kind="stable")[:kept]
             member = member[np.isin(member // size, chosen)]
         order = member[np.argsort(-key[member], kind="stable")][:topk]
@@ -165,6 +167,30 @@ def test_infinite_and_far_logits(torch):
     assert (w[0, :2] == 0.5).all()
     check(torch, l, 5, "sigmoid")
     check(torch, l, 5, "softmax", renorm=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_keys_closer_than_fp32_tells(torch, score):
+    """Keys that differ by less than fp32's rounding of the scores: the choice is that of 64 bits."""
+    rng = np.random.default_rng(8)
+    e = 192
+    one = logits(rng, 1, e)[0]
+    p = 1.0 / (1.0 + np.exp(-one.astype(np.float64)))
+    if score == "softmax":
+        p = np.exp(one.astype(np.float64) - one.max())
+        p = p / p.sum()
+    level = (1.0 - p).astype(np.float32)          # every key is 1 within 2^-24
+    l = np.tile(one, (6, 1))
+    l[3:] = logits(rng, 3, e)
+    check(torch, l, 9, score, bias=level)
+    check(torch, l, 9, score, level, 8, 3, True)
+    check(torch, l, 9, score, level, 8, 3, False)
+    steps = (np.arange(e) % 7 * 2.0 ** -24).astype(np.float32)
+    check(torch, np.full((3, e), 0.25), 12, score, bias=steps)
+    # keys of great size and both signs, whose pairs nearly cancel
+    far = np.where(np.arange(e) % 2 == 0, 1e6, -1e6) + np.round(rng.standard_normal(e), 1)
+    check(torch, l, 9, score, bias=far)
+    check(torch, l, 9, score, far, 48, 5, True)
 
 
 def test_no_tokens_and_many(torch):
