@@ -34,6 +34,7 @@ struct NormProblem {
     float *scales;
     int64_t m, k, ldx, ldr, ldh;
     float eps;
+    double inv_k; // set by the launcher: 1 / k
     int act_bits, rot;
     bool x_bf16, residual_bf16, weight_bf16;
 };

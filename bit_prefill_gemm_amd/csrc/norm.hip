@@ -17,8 +17,12 @@
 // one row in 10^8, next to a rounding border) and the codes are those of a
 // plain evaluation, bit for bit.  The fp64 sum is one instruction per value.
 //
-// One workgroup per row (grid-stride), a quad of lanes per 32-block, R blocks
-// per quad held in registers between the sum and the codes.
+// A row belongs to a workgroup, a 32-block to a quad of lanes (lane t holds
+// elements 8t..8t+7: one 16-byte load per 8 bf16 values), R blocks per quad in
+// registers between the sum and the codes.  What bounds it is memory (two
+// reads, a write and the codes) as long as loads are always in flight, so the
+// grid holds just the workgroups that fit the chip; each walks several rows
+// and issues the next row's loads before it reduces the current one.
 //
 // This file must be compiled with -ffp-contract=off (see quantize.hip).
 #include <hip/hip_runtime.h>
@@ -33,6 +37,8 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+// 16 bytes of rows that are 8-byte aligned (bf16, leading dimension a multiple of 4)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(8)));
 
 // two fp32 -> bf16 bits, round to nearest even (NaN stays NaN)
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
@@ -41,49 +47,189 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
 }
 
-// store the lane's 8 values of a block and return what was stored
-__device__ __forceinline__ void store8(float *dst, int t, float (&v)[8])
-{
-    *reinterpret_cast<float4 *>(dst + 4 * t) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(dst + 16 + 4 * t) = make_float4(v[4], v[5], v[6], v[7]);
-}
+// The lane's 8 values of a block as they sit in memory, T = float or uint16_t
+// (bf16 bits).
+template <typename T> struct Raw;
 
-__device__ __forceinline__ void store8(uint16_t *dst, int t, float (&v)[8])
-{
-    const uint2 lo = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
-    const uint2 hi = make_uint2(bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
-    *reinterpret_cast<uint2 *>(dst + 4 * t) = lo;
-    *reinterpret_cast<uint2 *>(dst + 16 + 4 * t) = hi;
-}
+template <> struct Raw<uint16_t> {
+    u32x4 w;
+    __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
+    __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<u32x4 *>(p) = w; }
+    __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ float at(int i) const
+    {
+        return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    }
+    __device__ __forceinline__ void round(const float (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    }
+};
 
-__device__ __forceinline__ void round_to(const float *, float (&)[8]) {}
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void store(float *p) const
+    {
+        *reinterpret_cast<float4 *>(p) = a;
+        *reinterpret_cast<float4 *>(p + 4) = b;
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float at(int i) const
+    {
+        return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w
+             : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+    }
+    __device__ __forceinline__ void round(const float (&v)[8])
+    {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
 
-__device__ __forceinline__ void round_to(const uint16_t *, float (&v)[8])
+constexpr int kRowRor8 = 0x128; // DPP row_ror:8: lane ^ 8 inside 16 lanes
+
+// The rotation of quantize.hip with lane t of a quad holding elements
+// 8t..8t+7: h = 1, 2, 4 inside the lane, 8 and 16 inside the quad (the lane
+// with the bit clear is lower), 32 and 64 across the quads of a longer span.
+template <int ROT>
+__device__ __forceinline__ void rotate_lanes(float (&v)[8], int lane)
 {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const uint32_t p = bf16_pair(v[i], v[i + 1]);
-        v[i] = bf16_to_f32(p & 0xFFFFu);
-        v[i + 1] = bf16_to_f32(p >> 16);
-    }
+    for (int h = 1; h < 8; h *= 2)
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (!(i & h)) {
+                const float a = v[i], b = v[i + h];
+                v[i] = a + b;
+                v[i + h] = a - b;
+            }
+    cross_stage<kQuadXor1>(v, (lane & 1) != 0);
+    cross_stage<kQuadXor2>(v, (lane & 2) != 0);
+    if constexpr (ROT >= 64)
+        cross_quad_stage<kSwzXor4>(v, (lane & 4) != 0);
+    if constexpr (ROT >= 128)
+        cross_stage<kRowRor8>(v, (lane & 8) != 0);
+    const float c = ROT == 64 ? 0.125f : __uint_as_float(ROT == 128 ? 0x3DB504F3u : 0x3E3504F3u);
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        v[i] = v[i] * c;
 }
 
 template <int R>
-__device__ __forceinline__ void rotate_rounds(float (&v)[R][8], int rot, int t, int lane)
+__device__ __forceinline__ void rotate_rounds(float (&v)[R][8], int rot, int lane)
 {
     if (rot == 32) {
 #pragma unroll
         for (int r = 0; r < R; r++)
-            rotate_p<32>(v[r], t, lane);
+            rotate_lanes<32>(v[r], lane);
     } else if (rot == 64) {
 #pragma unroll
         for (int r = 0; r < R; r++)
-            rotate_p<64>(v[r], t, lane);
+            rotate_lanes<64>(v[r], lane);
     } else if (rot == 128) {
 #pragma unroll
         for (int r = 0; r < R; r++)
-            rotate_p<128>(v[r], t, lane);
+            rotate_lanes<128>(v[r], lane);
     }
+}
+
+// low bytes of a, b, c, d, first to last
+__device__ __forceinline__ uint32_t low_bytes(float a, float b, float c, float d)
+{
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d), __float_as_uint(c), 0x04000c0cu);
+    return lo | hi;
+}
+
+// Scale and codes of one block per quad, as quantize.hip defines them; the
+// lane's part of the codes: 8 bytes, for 4-bit codes in lanes t = 0, 1 only
+// (bytes 8t..8t+7 of the block).
+template <int BITS>
+__device__ __forceinline__ uint2 quantize_lanes(const float (&v)[8], float &d)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        amax = fmaxf(amax, fabsf(v[i]));
+    amax = fmaxf(amax, quad_swap<kQuadXor1>(amax));
+    amax = fmaxf(amax, quad_swap<kQuadXor2>(amax));
+    constexpr float kQmax = BITS == 4 ? 7.0f : 127.0f;
+    constexpr float kQmin = BITS == 4 ? -8.0f : -127.0f;
+    d = amax / kQmax;
+    // rint(v / d), taken as v * rcp(d) with one check per wave whether any
+    // value lies within 1e-4 of a rounding midpoint (the product is within
+    // 2.3e-5 of the quotient, |v / d| <= 127); then, or where d is too small for
+    // the reciprocal, the IEEE quotient decides.  Adding 1.5 2^23 rounds to the
+    // nearest integer (ties to even) and leaves it in the low bits.
+    constexpr float kMagic = 12582912.0f;
+    const float rd = d != 0.0f ? __builtin_amdgcn_rcpf(d) : 0.0f;
+    float y[8];
+    float off = d != 0.0f && !(d >= 0x1p-100f) ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float q = v[i] * rd;
+        y[i] = q + kMagic;
+        off = fmaxf(off, fabsf(q - (y[i] - kMagic)));
+    }
+    if (__builtin_amdgcn_ballot_w64(off > 0.4999f) != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float q = d != 0.0f ? v[i] / d : 0.0f;
+            y[i] = fminf(fmaxf(q, kQmin), kQmax) + kMagic;
+        }
+    }
+    uint2 w = make_uint2(low_bytes(y[0], y[1], y[2], y[3]), low_bytes(y[4], y[5], y[6], y[7]));
+    if constexpr (BITS == 4) {
+        // byte j = code j | code j + 16 << 4: the upper half of the block is with lane t ^ 2
+        w.x &= 0x0F0F0F0Fu;
+        w.y &= 0x0F0F0F0Fu;
+        w.x |= (uint32_t)__builtin_amdgcn_mov_dpp((int)w.x, kQuadXor2, 0xF, 0xF, true) << 4;
+        w.y |= (uint32_t)__builtin_amdgcn_mov_dpp((int)w.y, kQuadXor2, 0xF, 0xF, true) << 4;
+    }
+    return w;
+}
+
+// Sum over a row of 16 lanes, in lane 15 (row_shr steps), then over the rows
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+__device__ __forceinline__ double row16_sum(double v)
+{
+    v += dpp_f64<0x111, 0xF>(v);
+    v += dpp_f64<0x112, 0xF>(v);
+    v += dpp_f64<0x114, 0xF>(v);
+    v += dpp_f64<0x118, 0xF>(v);
+    return v;
+}
+
+__device__ __forceinline__ double lane_of(double v, int lane)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// 1 / sqrt(a), a > 0 normal: the hardware's estimate (2^-24) and one step of
+// third order, within a few units of the 53rd bit
+__device__ __forceinline__ double rsqrt_f64(double a)
+{
+    const double y = __builtin_amdgcn_rsq(a);
+    const double e = __builtin_fma(-a * y, y, 1.0);
+    return __builtin_fma(y * e, __builtin_fma(0.375, e, 0.5), y);
 }
 
 // Tx: type of x, Tr: type of the residual stream (float, or uint16_t = bf16
@@ -91,6 +237,7 @@ __device__ __forceinline__ void rotate_rounds(float (&v)[R][8], int rot, int t, 
 template <typename Tx, typename Tr, int BITS, int R>
 __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
 {
+    // two buffers: a wave may be one row ahead of the slowest reader
     __shared__ double partial[2][16];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -99,99 +246,147 @@ __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
     const int waves = blockDim.x >> 6;
     const int quads = blockDim.x >> 2, qd = tid >> 2;
     const int nb = (int)(p.k / 32); // the host limits k to 2^16
+    const Tx *const x = static_cast<const Tx *>(p.x);
+    const Tr *const res = static_cast<const Tr *>(p.residual);
+    if (waves > 1 && tid < 32)
+        partial[tid >> 4][tid & 15] = 0.0; // the waves that do not exist
+
+    // The lane's part of block qd + r quads; quads past the row's end repeat
+    // its last span's place in it and store nothing.
+    int at[R];
+    bool live[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int b = qd + r * quads;
+        live[r] = b < nb;
+        at[r] = (live[r] ? b : 0) * 32 + 8 * t;
+    }
+    // few blocks per lane: the next row's values are loaded a row ahead
+    constexpr bool ahead = R <= 2;
+    Raw<Tx> rx[ahead ? R : 1];
+    Raw<Tr> rr[ahead ? R : 1];
+    auto load_row = [&](int64_t row) {
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            rx[r].load(x + row * p.ldx + at[r]);
+        if (res) {
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                rr[r].load(res + row * p.ldr + at[r]);
+        }
+    };
+    auto load_weight = [&](int r, float (&g)[8]) {
+        if (!p.weight) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                g[i] = 1.0f;
+        } else if (p.weight_bf16) {
+            Raw<uint16_t> w;
+            w.load(static_cast<const uint16_t *>(p.weight) + at[r]);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                g[i] = w.at(i);
+        } else {
+            Raw<float> w;
+            w.load(static_cast<const float *>(p.weight) + at[r]);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                g[i] = w.at(i);
+        }
+    };
+    // and the weight stays in registers for all rows
+    constexpr bool keep = R <= 2;
+    float g[keep ? R : 1][8];
+    if constexpr (ahead)
+        load_row(blockIdx.x);
+    if constexpr (keep) {
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            load_weight(r, g[r]);
+    }
+    if (waves > 1)
+        __syncthreads(); // the zeros
 
     int parity = 0;
     for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, parity ^= 1) {
-        const Tx *x = static_cast<const Tx *>(p.x) + row * p.ldx;
-        const Tr *res = static_cast<const Tr *>(p.residual) + row * p.ldr;
-        float v[R][8], g[R][8];
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            const int b = qd + r * quads;
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                v[r][i] = 0.0f;
-            if (b < nb)
-                load8(x + b * 32, t, v[r]);
-        }
-        if (p.residual) {
-            float a[R][8];
-#pragma unroll
-            for (int r = 0; r < R; r++) {
-                const int b = qd + r * quads;
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    a[r][i] = 0.0f;
-                if (b < nb)
-                    load8(res + b * 32, t, a[r]);
-            }
-#pragma unroll
-            for (int r = 0; r < R; r++) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    v[r][i] = v[r][i] + a[r][i];
-                round_to(res, v[r]);
-            }
-            if (p.h) {
-                Tr *h = static_cast<Tr *>(p.h) + row * p.ldh;
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                    const int b = qd + r * quads;
-                    if (b < nb)
-                        store8(h + b * 32, t, v[r]);
-                }
-            }
-        }
-        // the norm's weight (1 where there is none)
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            const int b = qd + r * quads;
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                g[r][i] = 1.0f;
-            if (p.weight && b < nb) {
-                if (p.weight_bf16)
-                    load8(static_cast<const uint16_t *>(p.weight) + b * 32, t, g[r]);
-                else
-                    load8(static_cast<const float *>(p.weight) + b * 32, t, g[r]);
-            }
-        }
-
-        // the sum of squares: lane, wave, workgroup, each in a fixed order
+        float v[R][8];
         double ss = 0.0;
 #pragma unroll
-        for (int r = 0; r < R; r++)
+        for (int r = 0; r < R; r++) {
+            const int q = ahead ? r : 0;
+            if constexpr (!ahead) {
+                rx[0].load(x + row * p.ldx + at[r]);
+                if (res)
+                    rr[0].load(res + row * p.ldr + at[r]);
+            }
+            if (res) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[r][i] = rx[q].at(i) + rr[q].at(i);
+                Raw<Tr> h;
+                h.round(v[r]);
+                if (p.h && live[r])
+                    h.store(static_cast<Tr *>(p.h) + row * p.ldh + at[r]);
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[r][i] = h.at(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[r][i] = rx[q].at(i);
+            }
+            double sb = 0.0;
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                ss = __builtin_fma((double)v[r][i], (double)v[r][i], ss);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            ss += __shfl_xor(ss, d);
+                sb = __builtin_fma((double)v[r][i], (double)v[r][i], sb);
+            ss += live[r] ? sb : 0.0;
+        }
+        if constexpr (ahead) {
+            if (row + gridDim.x < p.m)
+                load_row(row + gridDim.x);
+        }
+
+        // the sum: lanes, waves, each in a fixed order
+        ss = row16_sum(ss);
+        ss += dpp_f64<0x142, 0xA>(ss);
+        ss += dpp_f64<0x143, 0xC>(ss);
         if (waves > 1) {
-            // (two buffers: a wave may be one row ahead of the slowest reader)
-            if (lane == 0)
+            if (lane == 63)
                 partial[parity][wave] = ss;
             __syncthreads();
-            ss = 0.0;
-            for (int w = 0; w < waves; w++)
-                ss += partial[parity][w];
+            ss = lane_of(row16_sum(partial[parity][lane & 15]), 15);
+        } else {
+            ss = lane_of(ss, 63);
         }
-        const float s = (float)(1.0 / sqrt(ss / (double)p.k + (double)p.eps));
+        const float s = (float)rsqrt_f64(__builtin_fma(ss, p.inv_k, (double)p.eps));
 
 #pragma unroll
-        for (int r = 0; r < R; r++)
+        for (int r = 0; r < R; r++) {
+            if constexpr (!keep)
+                load_weight(r, g[0]);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 v[r][i] = v[r][i] * s;
-                v[r][i] = v[r][i] * g[r][i];
+                v[r][i] = v[r][i] * g[keep ? r : 0][i];
             }
-        rotate_rounds(v, p.rot, t, lane);
+        }
+        rotate_rounds(v, p.rot, lane);
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            const int b = qd + r * quads;
-            if (b < nb)
-                quantize_block<BITS>(v[r], t, 0, row, b, p.k, nb, static_cast<uint8_t *>(p.codes),
-                                     p.scales);
+            float d;
+            const uint2 w = quantize_lanes<BITS>(v[r], d);
+            if (!live[r])
+                continue;
+            const int64_t b = row * nb + qd + r * quads;
+            uint8_t *const codes = static_cast<uint8_t *>(p.codes);
+            if constexpr (BITS == 4) {
+                if (t < 2)
+                    *reinterpret_cast<uint2 *>(codes + b * 16 + 8 * t) = w;
+            } else {
+                *reinterpret_cast<uint2 *>(codes + b * 32 + 8 * t) = w;
+            }
+            if (t == 0)
+                p.scales[b] = d;
         }
     }
 }
@@ -214,41 +409,58 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t *__restri
         const float d = scales[blk];
         float v[1][8];
         if constexpr (BITS == 4) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + blk * 16 + 4 * t);
+            // bytes 8 (t & 1) .. + 7 of the block: elements 8t.. in the low nibbles for t < 2,
+            // in the high ones for t = 2, 3
+            const uint2 c = *reinterpret_cast<const uint2 *>(codes + blk * 16 + 8 * (t & 1));
+            const int up = t < 2 ? 4 : 0;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                v[0][i] = (float)((int)(w << (28 - 8 * i)) >> 28) * d;
-                v[0][i + 4] = (float)((int)(w << (24 - 8 * i)) >> 28) * d;
+                v[0][i] = (float)((int)((c.x << up) << (24 - 8 * i)) >> 28) * d;
+                v[0][i + 4] = (float)((int)((c.y << up) << (24 - 8 * i)) >> 28) * d;
             }
         } else {
-            const uint32_t lo = *reinterpret_cast<const uint32_t *>(codes + blk * 32 + 4 * t);
-            const uint32_t hi = *reinterpret_cast<const uint32_t *>(codes + blk * 32 + 16 + 4 * t);
+            const uint2 c = *reinterpret_cast<const uint2 *>(codes + blk * 32 + 8 * t);
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                v[0][i] = (float)((int)(lo << (24 - 8 * i)) >> 24) * d;
-                v[0][i + 4] = (float)((int)(hi << (24 - 8 * i)) >> 24) * d;
+                v[0][i] = (float)((int)(c.x << (24 - 8 * i)) >> 24) * d;
+                v[0][i + 4] = (float)((int)(c.y << (24 - 8 * i)) >> 24) * d;
             }
         }
-        rotate_rounds(v, rot, t, lane);
-        store8(y + row * ldy + b * 32, t, v[0]);
+        rotate_rounds(v, rot, lane);
+        Raw<Ty> out;
+        out.round(v[0]);
+        out.store(y + row * ldy + b * 32 + 8 * t);
     }
 }
+
+constexpr int kCUs = 256;
 
 template <typename Tx, typename Tr, int BITS>
 hipError_t launch_norm_rounds(const NormProblem &p, hipStream_t stream)
 {
     const int nb = (int)(p.k / 32);
-    const int64_t rows = p.m < ((int64_t)1 << 20) ? p.m : (int64_t)1 << 20;
-    const dim3 grid((unsigned)rows);
-    auto threads = [&](int rounds) { return dim3((unsigned)(64 * ((nb + 16 * rounds - 1) / (16 * rounds)))); };
-    if (nb <= 256)
-        norm_quantize_kernel<Tx, Tr, BITS, 1><<<grid, threads(1), 0, stream>>>(p);
+    // per_cu: waves that a CU holds of the kernel (by its registers); the grid
+    // is no more workgroups than fit at once
+    auto launch = [&](auto kernel, int rounds, int per_cu) {
+        const int waves = (nb + 16 * rounds - 1) / (16 * rounds);
+        const int64_t most = (int64_t)kCUs * (per_cu / waves > 0 ? per_cu / waves : 1);
+        const dim3 grid((unsigned)(p.m < most ? p.m : most));
+        kernel<<<grid, dim3((unsigned)(64 * waves)), 0, stream>>>(p);
+    };
+    // One block per quad while every row has a workgroup at once (the shortest
+    // chain from the loads to the stores); with more rows than that, two: half
+    // the reductions and barriers a row.
+    const bool once = p.m <= (int64_t)kCUs * (32 / ((nb + 15) / 16 < 32 ? (nb + 15) / 16 : 32));
+    if (nb <= 256 && (once || nb < 32))
+        launch(norm_quantize_kernel<Tx, Tr, BITS, 1>, 1, 32);
     else if (nb <= 512)
-        norm_quantize_kernel<Tx, Tr, BITS, 2><<<grid, threads(2), 0, stream>>>(p);
+        launch(norm_quantize_kernel<Tx, Tr, BITS, 2>, 2, 20);
+    else if (nb <= 768)
+        launch(norm_quantize_kernel<Tx, Tr, BITS, 3>, 3, 16);
     else if (nb <= 1024)
-        norm_quantize_kernel<Tx, Tr, BITS, 4><<<grid, threads(4), 0, stream>>>(p);
+        launch(norm_quantize_kernel<Tx, Tr, BITS, 4>, 4, 16);
     else
-        norm_quantize_kernel<Tx, Tr, BITS, 8><<<grid, threads(8), 0, stream>>>(p);
+        launch(norm_quantize_kernel<Tx, Tr, BITS, 8>, 8, 16);
     return hipGetLastError();
 }
 
@@ -261,10 +473,12 @@ hipError_t launch_norm_types(const NormProblem &p, hipStream_t stream)
 
 } // namespace
 
-hipError_t launch_norm_quantize(const NormProblem &p, hipStream_t stream)
+hipError_t launch_norm_quantize(const NormProblem &problem, hipStream_t stream)
 {
-    if (p.m == 0)
+    if (problem.m == 0)
         return hipSuccess;
+    NormProblem p = problem;
+    p.inv_k = 1.0 / (double)p.k;
     if (p.x_bf16)
         return p.residual_bf16 ? launch_norm_types<uint16_t, uint16_t>(p, stream)
                                : launch_norm_types<uint16_t, float>(p, stream);
