@@ -30,7 +30,7 @@ ENTRY_POINTS = ("bpg_status_str", "rotate_pack_weights_bytes", "rotate_pack_weig
                 "rotate_pack_weights_rot", "quantize_act_rot", "w4a4_gemm_rot",
                 "w4a4_gemm_bf16", "w4a4_grouped_gemm_bf16", "w4a4_gemm_kernel_name",
                 "w4a4_grouped_gemm_kernel_name", "rmsnorm_quantize_act", "dequantize_act",
-                "w4a4_gemm_epilogue", "moe_route_topk")
+                "w4a4_gemm_epilogue", "w4a4_gemm_epilogue_kernel_name", "moe_route_topk")
 
 
 class WeightsDesc(ctypes.Structure):
@@ -110,8 +110,10 @@ def _lib_handle():
     lib.w4a4_gemm_blocksums.argtypes = [_vp, _vp, ctypes.c_int, _i64,
                                         ctypes.POINTER(WeightsDesc), _vp, _i64, _i64, _i64, _i64,
                                         _i64, _vp, _vp]
-    lib.w4a4_gemm_kernel_name.restype = ctypes.c_char_p
-    lib.w4a4_gemm_kernel_name.argtypes = [ctypes.c_int, _i64, ctypes.POINTER(WeightsDesc)]
+    for name in ("w4a4_gemm_kernel_name", "w4a4_gemm_epilogue_kernel_name"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_char_p
+        fn.argtypes = [ctypes.c_int, _i64, ctypes.POINTER(WeightsDesc)]
     lib.w4a4_grouped_gemm_kernel_name.restype = ctypes.c_char_p
     lib.w4a4_grouped_gemm_kernel_name.argtypes = [ctypes.c_int, _i64, _i64,
                                                   ctypes.POINTER(WeightsDesc)]
@@ -447,6 +449,14 @@ def w4a4_gemm_kernel_name(act_bits: int, m: int, w: Weights) -> str:
     r = _lib_handle().w4a4_gemm_kernel_name(act_bits, m, ctypes.byref(w.desc))
     if r is None:
         raise ValueError("w4a4_gemm_kernel_name: invalid act_bits, m or stamp")
+    return r.decode()
+
+
+def w4a4_gemm_epilogue_kernel_name(act_bits: int, m: int, w: Weights) -> str:
+    """The kernel w4a4_gemm_epilogue runs for m rows of act_bits codes against w (host only)."""
+    r = _lib_handle().w4a4_gemm_epilogue_kernel_name(act_bits, m, ctypes.byref(w.desc))
+    if r is None:
+        raise ValueError("w4a4_gemm_epilogue_kernel_name: invalid act_bits, m or stamp")
     return r.decode()
 
 

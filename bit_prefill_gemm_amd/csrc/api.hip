@@ -380,6 +380,23 @@ bpg_status gemm_checked(const void *codes, const float *scales, int act_bits, in
     return launch_status(bpg::launch_gemm(p, static_cast<hipStream_t>(stream)));
 }
 
+// the kernel of a dense product, with or without an epilogue
+const char *dense_kernel_name(int act_bits, int64_t m, const bpg_weights_desc *w, bool epilogue)
+{
+    if (!w || (act_bits != 4 && act_bits != 8) || m < 0 || m > ((int64_t)1 << 31) - 1)
+        return nullptr;
+    if (check_stamp(w, w->rotation) != BPG_OK || w->num_experts != 1)
+        return nullptr;
+    bpg::GemmProblem p{};
+    p.rows = m;
+    p.n = w->n;
+    p.k = w->k;
+    p.experts = 1;
+    p.act_bits = act_bits;
+    p.epilogue = epilogue;
+    return bpg::kernel_name(bpg::plan_gemm(p));
+}
+
 } // namespace
 
 extern "C" {
@@ -541,17 +558,12 @@ bpg_status quantize_act_rot(const void *x, bpg_x_dtype dt, int64_t m, int64_t k,
 
 const char *w4a4_gemm_kernel_name(int act_bits, int64_t m, const bpg_weights_desc *w)
 {
-    if (!w || (act_bits != 4 && act_bits != 8) || m < 0 || m > ((int64_t)1 << 31) - 1)
-        return nullptr;
-    if (check_stamp(w, w->rotation) != BPG_OK || w->num_experts != 1)
-        return nullptr;
-    bpg::GemmProblem p{};
-    p.rows = m;
-    p.n = w->n;
-    p.k = w->k;
-    p.experts = 1;
-    p.act_bits = act_bits;
-    return bpg::kernel_name(bpg::plan_gemm(p));
+    return dense_kernel_name(act_bits, m, w, false);
+}
+
+const char *w4a4_gemm_epilogue_kernel_name(int act_bits, int64_t m, const bpg_weights_desc *w)
+{
+    return dense_kernel_name(act_bits, m, w, true);
 }
 
 const char *w4a4_grouped_gemm_kernel_name(int act_bits, int64_t total_rows, int64_t src_rows,

@@ -592,6 +592,24 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
     float *red = reinterpret_cast<float *>(lds);
     constexpr int R = C::kRedTiles;
     for (int t0 = 0; t0 < C::kTiles; t0 += R) {
+        // the residual values of the results that this wave sums
+        constexpr int kOwn = EP ? (R + WK - 1) / WK : 1;
+        uint32_t res[kOwn][RG];
+        if constexpr (EP) {
+            if (p.ep.residual) {
+#pragma unroll
+                for (int o = 0; o < kOwn; o++) {
+                    const int t = min(t0 + wk + o * WK, C::kTiles - 1);
+                    const int i = t / TN, j = t % TN;
+                    const int64_t r0 = row0 * p.ep.ldr + col0 + (wn * TN + j) * MF + rc;
+#pragma unroll
+                    for (int r = 0; r < RG; r++) {
+                        const int rl = min((wm * TM + i) * MF + M::out_row(g, r), last_row);
+                        res[o][r] = ep_raw(p.ep, r0 + (int64_t)rl * p.ep.ldr);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int t = 0; t < C::kTiles; t++) {
             if (t < t0 || t >= t0 + R)
@@ -602,22 +620,17 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
                 red[(((grp * WK + wk) * R + (t - t0)) * RG + r) * 64 + lane] = acc[i][j][r];
         }
         __syncthreads();
-        for (int tt = wk; tt < R && t0 + tt < C::kTiles; tt += WK) {
+#pragma unroll
+        for (int o = 0; o < (R + WK - 1) / WK; o++) {
+            const int tt = wk + o * WK;
+            if (tt >= R || t0 + tt >= C::kTiles)
+                break;
             const int t = t0 + tt;
             const int i = t / TN, j = t % TN;
             const int64_t col = col0 + (wn * TN + j) * MF + rc;
             if constexpr (EP) {
                 const int64_t trow = row0 + (wm * TM + i) * MF;
-                float vr[RG], res[RG];
-                if (p.ep.residual) {
-#pragma unroll
-                    for (int r = 0; r < RG; r++) {
-                        const int rl = M::out_row(g, r);
-                        if (rl < vrows[i])
-                            res[r] = ep_load(p.ep.residual, p.ep.residual_bf16,
-                                             (trow + rl) * p.ep.ldr + col);
-                    }
-                }
+                float vr[RG];
                 const float bias = p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col) : 0.0f;
 #pragma unroll
                 for (int r = 0; r < RG; r++) {
@@ -635,7 +648,7 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
                     const int rl = M::out_row(g, r);
                     if (rl < vrows[i])
                         store_y(p, (trow + rl) * p.ldy + col,
-                                p.ep.residual ? vr[r] + res[r] : vr[r]);
+                                p.ep.residual ? vr[r] + ep_value(p.ep, res[EP ? o : 0][r]) : vr[r]);
                 }
                 continue;
             }
@@ -819,6 +832,8 @@ int plan_gemm(const GemmProblem &p)
 {
     if (p.rows == 0)
         return kNoKernel;
+    if (chunks_fit(p))
+        return kChunks;
     if (skinny_fits(p))
         return kSkinny;
     return p.act_bits == 4 ? plan_dense_bits<4>(p) : plan_dense_bits<8>(p);
@@ -837,6 +852,7 @@ const char *kernel_name(int kernel)
 {
     switch (kernel) {
     case kSkinny: return "weight-stream";
+    case kChunks: return "weight-stream chunks";
     case kWide: return "wide 64x160";
     case kStrip: return "strip 32x128";
     case kTiled64x160: return "tiled 64x160";
@@ -860,6 +876,8 @@ hipError_t launch_gemm(const GemmProblem &p, hipStream_t stream)
         return hipSuccess;
     if (kernel == kSkinny)
         return launch_skinny(p, stream);
+    if (kernel == kChunks)
+        return launch_chunks(p, stream);
     return p.act_bits == 4 ? launch_dense_bits<4>(kernel, p, stream)
                            : launch_dense_bits<8>(kernel, p, stream);
 }

@@ -101,6 +101,7 @@ struct GemmProblem {
 enum Kernel {
     kNoKernel = 0,
     kSkinny,       // weight-stream kernel, M <= 32 (skinny.hip)
+    kChunks,       // the same over chunks of 16 rows, with an epilogue only
     kWide,         // 64 x 160 direct-load tiles, 4-bit (wide.hip)
     kStrip,        // 32 x 128 strips (strip.hip)
     kTiled64x160,  // tiled kernel shapes (gemm.hip)
@@ -123,6 +124,9 @@ hipError_t launch_gemm(const GemmProblem &p, hipStream_t stream);
 // skinny_fits(p).
 bool skinny_fits(const GemmProblem &p);
 hipError_t launch_skinny(const GemmProblem &p, hipStream_t stream);
+// The same over chunks of 16 rows: usable when chunks_fit(p).
+bool chunks_fit(const GemmProblem &p);
+hipError_t launch_chunks(const GemmProblem &p, hipStream_t stream);
 // The wide-tile kernel (4-bit activations, dense, many rows): 64 x 160
 // tiles; usable when wide_fits(p).
 bool wide_fits(const GemmProblem &p);

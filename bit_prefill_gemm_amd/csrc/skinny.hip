@@ -117,8 +117,22 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int B = (int)(p.k / 32); // the host limits K
     const int NG = (B + 3) / 4;    // groups of four blocks
-    const int rows = (int)p.rows;  // 1 .. kRows
-    const int64_t tile = blockIdx.x;
+    // this workgroup's column tile and chunk of rows.  Without an epilogue there
+    // is one chunk; with several, the chunks of a tile follow one another on one
+    // XCD (workgroups go to the eight round robin), so they share its L2
+    // (32 x 16384 x 32768, 302 MB of weights: 107 us; 112 in tile order across
+    // the XCDs, 126 chunk by chunk).
+    int64_t tile = blockIdx.x, row0 = 0;
+    if constexpr (EP) {
+        const int chunks = (int)((p.rows + kRows - 1) / kRows);
+        if (chunks > 1) {
+            const int x = blockIdx.x % 8, each = gridDim.x / 8, more = gridDim.x % 8;
+            const int at = x * each + (x < more ? x : more) + blockIdx.x / 8;
+            tile = at / chunks;
+            row0 = (int64_t)(at % chunks) * kRows;
+        }
+    }
+    const int rows = (int)(p.rows - row0 < kRows ? p.rows - row0 : kRows);
     const int64_t col0 = tile * C::kCols;
 
     float *Da = lds;
@@ -135,7 +149,8 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     const int g0 = (int)((int64_t)wave * NG / NW);
     const int g1 = (int)((int64_t)(wave + 1) * NG / NW);
     const int64_t arow = p.k * kAB / 32;
-    const gptr a_base = uniform_ptr(p.codes);
+    const gptr a_base = uniform_ptr(p.codes + row0 * arow);
+    const float *const da_base = p.scales + row0 * B;
     const gptr w_base = uniform_ptr(p.wcodes + (col0 / 32) * NG * 2304);
     uint32_t va[TM], vw[TN];
     // the group's scales: 16 bytes at [c16 = c] = column c's and column
@@ -269,7 +284,7 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     auto da_load = [&](int b) {
 #pragma unroll
         for (int m = 0; m < kRows; m++)
-            dv[m] = b < B && m < rows ? p.scales[(int64_t)m * B + b] : 0.0f;
+            dv[m] = b < B && m < rows ? da_base[(int64_t)m * B + b] : 0.0f;
     };
     auto da_store = [&](int b) {
         if (b < da_cols)
@@ -293,6 +308,21 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
             for (int m = 0; m < kRows; m++)
                 *reinterpret_cast<uint4 *>(act_lds + m * a_stride + ch * 16) = av[m];
     };
+    // the residual values of the results that this thread stores (loaded first:
+    // at the end a workgroup would wait for them with nothing left to do)
+    constexpr int kOwn = (R * 64 + NT - 1) / NT;
+    uint32_t res[EP ? kOwn : 1];
+    if constexpr (EP) {
+        if (p.ep.residual) {
+#pragma unroll
+            for (int o = 0; o < kOwn; o++) {
+                const int v = min(tid + o * NT, R * 64 - 1);
+                const int q = v >> 6, ln = v & 63;
+                const int m = min(16 * (q / (TN * 4)) + 4 * (ln >> 4) + q % 4, rows - 1);
+                res[o] = ep_raw(p.ep, (row0 + m) * p.ep.ldr + col0 + 16 * ((q / 4) % TN) + (ln & 15));
+            }
+        }
+    }
     da_load(tid);
     if constexpr (C::AL)
         act_load(tid);
@@ -351,15 +381,17 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
                 red[(wave * R + (i * TN + j) * 4 + r) * 64 + lane] = acc[i][j][r];
     __syncthreads();
     const float unscale = 1.0f / (float)(1 << C::kShift);
-    for (int v = tid; v < R * 64; v += NT) {
+#pragma unroll
+    for (int o = 0; o < kOwn; o++) {
+        const int v = tid + o * NT;
+        if (v >= R * 64)
+            break;
         const int q = v >> 6, ln = v & 63;
         const int i = q / (TN * 4), j = (q / 4) % TN, r = q % 4;
         const int m = 16 * i + 4 * (ln >> 4) + r;
         const int64_t col = col0 + 16 * j + (ln & 15);
-        float res = 0.0f, bias = 0.0f;
+        float bias = 0.0f;
         if constexpr (EP) {
-            if (p.ep.residual && m < rows)
-                res = ep_load(p.ep.residual, p.ep.residual_bf16, (int64_t)m * p.ep.ldr + col);
             if (p.ep.bias)
                 bias = ep_load(p.ep.bias, p.ep.bias_bf16, col);
         }
@@ -367,16 +399,16 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
 #pragma unroll
         for (int w = 1; w < NW; w++)
             s += red[w * R * 64 + v];
-        float o[1] = {s * unscale};
+        float out[1] = {s * unscale};
         if constexpr (EP) {
             if (p.ep.bias)
-                o[0] = o[0] + bias;
-            ep_activate(p.ep.act, o);
+                out[0] = out[0] + bias;
+            ep_activate(p.ep.act, out);
             if (p.ep.residual)
-                o[0] = o[0] + res;
+                out[0] = out[0] + ep_value(p.ep, res[EP ? o : 0]);
         }
         if (m < rows)
-            store_y(p, (int64_t)m * p.ldy + col, o[0]);
+            store_y(p, (row0 + m) * p.ldy + col, out[0]);
     }
 }
 
@@ -393,7 +425,8 @@ template <class C>
 hipError_t launch_cfg(const GemmProblem &p, hipStream_t stream)
 {
     const size_t lds = skinny_lds<C>(p);
-    const dim3 grid((unsigned)(p.n / C::kCols));
+    const int64_t chunks = (p.rows + C::kRows - 1) / C::kRows;
+    const dim3 grid((unsigned)(p.n / C::kCols * chunks));
     if (p.epilogue)
         skinny_kernel<C, true><<<grid, C::kThreads, lds, stream>>>(p);
     else
@@ -440,7 +473,8 @@ hipError_t launch_al(const GemmProblem &p, int nw, hipStream_t stream)
 template <int BITS, int TM, int TN>
 hipError_t launch_tn(const GemmProblem &p, hipStream_t stream)
 {
-    const int64_t tiles = p.n / (16 * TN), NG = (p.k / 32 + 3) / 4;
+    const int64_t chunks = (p.rows + 16 * TM - 1) / (16 * TM);
+    const int64_t tiles = p.n / (16 * TN) * chunks, NG = (p.k / 32 + 3) / 4;
     // (two row tiles need more registers: at most 8 waves)
     constexpr int nw_max = TM == 1 ? 16 : 8;
     int nw = 4;
@@ -469,6 +503,30 @@ bool skinny_fits(const GemmProblem &p)
     // the transposed scales (whole groups of four blocks) must fit the 64 KB
     // of dynamic LDS
     return (p.k / 32 + 3) / 4 * 4 * rows_cov * 4 <= 65536;
+}
+
+// With an epilogue the kernel also runs more rows, in chunks of 16:
+// every chunk streams the weights again, from L2 but for the first, and its
+// workgroups' waves split K, so the time of a product with few output tiles is
+// that of a wave's share of K instead of the whole of K in series.  T = chunks
+// x 32-column tiles workgroups; taken up to T = 1024, from K = 2048 on up to
+// T = 2048.  Measured (us, 4-bit, M x K x N, this kernel against the one that
+// w4a4_gemm runs): 77 x 2080 x 1056 6.1 / 11.7 (tiled), 96 x 5120 x 1056
+// 8.1 / 20.7 (tiled), 128 x 5120 x 5120 21.2 / 35.3 (strip), 512 x 17408 x 640
+// 38 / 105 (strip), 17 x 2048 x 5120 6.7 / 8.3 and 32 x 5120 x 17408
+// 21.0 / 22.4 (one chunk of 32 rows); just past the bounds, 256 x 512 x 5120
+// (T = 2560) 12.4 / 9.8, 64 x 2048 x 17408 (T = 2176) 17.5 / 19.9 and
+// 96 x 5120 x 17408 (T = 3264) 49.7 / 40.3.
+bool chunks_fit(const GemmProblem &p)
+{
+    const int64_t t = (p.rows + 15) / 16 * (p.n / 32);
+    return p.epilogue && p.rows > 16 && (p.k / 32 + 3) / 4 * 4 * 16 * 4 <= 65536 &&
+           t <= (p.k >= 2048 ? 2048 : 1024);
+}
+
+hipError_t launch_chunks(const GemmProblem &p, hipStream_t stream)
+{
+    return p.act_bits == 4 ? launch_tm<4, 1>(p, stream) : launch_tm<8, 1>(p, stream);
 }
 
 hipError_t launch_skinny(const GemmProblem &p, hipStream_t stream)

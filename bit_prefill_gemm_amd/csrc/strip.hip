@@ -199,6 +199,19 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
 #pragma unroll
     for (int r = 0; r < 16; r++)
         acc[r] = 0.0f;
+    // the residual values of the lane's results: loaded behind the first
+    // stage's operands, so that nothing waits for them at the end (4-bit codes;
+    // with 8-bit ones the 16 registers would cost the fourth workgroup of a CU,
+    // 271 against 260 us at 1024 x 5120 x 17408, and they are loaded at the end)
+    uint32_t res[EP ? 16 : 1];
+    auto load_residual = [&] {
+        const int64_t r0 = row0 * p.ep.ldr + col0 + wave * 32 + c;
+#pragma unroll
+        for (int r = 0; r < 16; r++) {
+            const int rl = min(4 * hk + 8 * (r >> 2) + (r & 3), last_row);
+            res[EP ? r : 0] = ep_raw(p.ep, r0 + (int64_t)rl * p.ep.ldr);
+        }
+    };
     Acc magic;
 #pragma unroll
     for (int r = 0; r < 16; r++)
@@ -291,6 +304,10 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     constexpr int kWaitLoads = 0x0F70;
 
     issue(buf0, 0);
+    if constexpr (EP && BITS == 4) {
+        if (p.ep.residual)
+            load_residual();
+    }
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     __syncthreads();
     for (int st = 0; st < nst; st += 2) {
@@ -312,16 +329,8 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     const int64_t y0 = (row0 + 4 * hk) * p.ldy + col0 + wave * 32 + c;
     const int lim = last_row + 1 - 4 * hk; // rows of this lane's group that hold data
     if constexpr (EP) {
-        const int64_t r0 = (row0 + 4 * hk) * p.ep.ldr + col0 + wave * 32 + c;
-        float res[16];
-        if (p.ep.residual) {
-#pragma unroll
-            for (int r = 0; r < 16; r++) {
-                const int ro = 8 * (r >> 2) + (r & 3);
-                if (ro < lim)
-                    res[r] = ep_load(p.ep.residual, p.ep.residual_bf16, r0 + (int64_t)ro * p.ep.ldr);
-            }
-        }
+        if (BITS == 8 && p.ep.residual)
+            load_residual();
         const float bias =
             p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col0 + wave * 32 + c) : 0.0f;
 #pragma unroll
@@ -335,7 +344,7 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
         for (int r = 0; r < 16; r++) {
             const int ro = 8 * (r >> 2) + (r & 3);
             if (ro < lim)
-                store_y(p, y0 + (int64_t)ro * p.ldy, p.ep.residual ? acc[r] + res[r] : acc[r]);
+                store_y(p, y0 + (int64_t)ro * p.ldy, p.ep.residual ? acc[r] + ep_value(p.ep, res[r]) : acc[r]);
         }
         return;
     }

@@ -313,6 +313,20 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(GemmProblem p, int tiles_m
     float *red0 = reinterpret_cast<float *>(w_lds0);
     float *red1 = reinterpret_cast<float *>(w_lds1);
     const int rows_valid = last_row + 1;
+    // the residual values of the results that this wave sums
+    uint32_t res[EP ? TN : 1][4];
+    if constexpr (EP) {
+        if (p.ep.residual) {
+            const int64_t r0 = row0 * p.ep.ldr + col0 + c;
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int rl = min(wm * 32 + M::out_row(hk, 4 * wk + e), last_row);
+                    res[j][e] = ep_raw(p.ep, r0 + (int64_t)rl * p.ep.ldr + j * 32);
+                }
+        }
+    }
 #pragma unroll
     for (int j0 = 0; j0 < TN; j0 += 2) {
 #pragma unroll
@@ -330,16 +344,7 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(GemmProblem p, int tiles_m
             const float *red = jj == 0 ? red0 : red1;
             if constexpr (EP) {
                 const int64_t col = col0 + (j0 + jj) * 32 + c;
-                float v4[4], res[4];
-                if (p.ep.residual) {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int rl = wm * 32 + M::out_row(hk, 4 * wk + e);
-                        if (rl < rows_valid)
-                            res[e] = ep_load(p.ep.residual, p.ep.residual_bf16,
-                                             (row0 + rl) * p.ep.ldr + col);
-                    }
-                }
+                float v4[4];
                 const float bias = p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col) : 0.0f;
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
@@ -358,7 +363,7 @@ __global__ __launch_bounds__(512, 1) void wide_kernel(GemmProblem p, int tiles_m
                     const int rl = wm * 32 + M::out_row(hk, 4 * wk + e);
                     if (rl < rows_valid)
                         store_y(p, (row0 + rl) * p.ldy + col,
-                                p.ep.residual ? v4[e] + res[e] : v4[e]);
+                                p.ep.residual ? v4[e] + ep_value(p.ep, res[j0 + jj][e]) : v4[e]);
                 }
                 continue;
             }

@@ -323,17 +323,20 @@ bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64
  * joins them there).  With t = the fp32 result of w4a4_gemm (w4a4_gemm_rot,
  * w4a4_gemm_unrotated for rotation 64 / 128, 0):
  *   y = act(t + bias[column]) + residual[row][column]
- * each step in fp32 (the exponential, erf and division of an activation
- * within a few units in the last place), rounded once to y's type.  With no
- * bias, BPG_ACT_NONE and no residual every element equals w4a4_gemm's (or its
- * bf16 rounding).
+ * each step in fp32 (the exponential, erf and reciprocal of an activation
+ * within a few units in the last place), rounded once to y's type.  Where both
+ * run the same kernel (see the routing queries below), with no bias,
+ * BPG_ACT_NONE and no residual every element equals w4a4_gemm's (or its bf16
+ * rounding).
  *
  *   rotation  0, 32, 64 or 128: the span of the codes; the image's stamp must
  *             record the same (else STAMP)
  *   ep        host, not NULL; read during the call only
  *   y         device, [m][ldy] of y_dt; fp32: ldy % 4 == 0, bf16: ldy % 8 == 0
- * Other arguments as w4a4_gemm; the kernel is the one that
- * w4a4_gemm_kernel_name names.
+ * Other arguments as w4a4_gemm.  The kernel is the one that
+ * w4a4_gemm_epilogue_kernel_name names; with more than 16 rows and few output
+ * tiles it is another one than w4a4_gemm's, which adds the blocks' sums in
+ * another (fixed) order.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, STAMP, DEVICE, LAUNCH.
  */
 typedef struct {
@@ -525,7 +528,8 @@ bpg_status w4a4_gemm_blocksums(const void *codes, const float *scales, int act_b
 /*
  * Routing queries, host only (no GPU call): the name of the kernel that
  * w4a4_gemm (and its _bf16, _unrotated and _rot forms) with these arguments
- * launches, and the same for w4a4_grouped_gemm (src_rows = 0) or
+ * launches, the same for w4a4_gemm_epilogue (which also has "weight-stream
+ * chunks"), and the same for w4a4_grouped_gemm (src_rows = 0) or
  * w4a4_grouped_gemm_gather (src_rows = the activation rows it reads).  The
  * kernel is chosen from the shape and the code width alone, so the answer is
  * what the product call runs: "weight-stream", "wide 64x160",
@@ -534,6 +538,7 @@ bpg_status w4a4_gemm_blocksums(const void *codes, const float *scales, int act_b
  * strings; the caller frees nothing).
  */
 const char *w4a4_gemm_kernel_name(int act_bits, int64_t m, const bpg_weights_desc *w);
+const char *w4a4_gemm_epilogue_kernel_name(int act_bits, int64_t m, const bpg_weights_desc *w);
 const char *w4a4_grouped_gemm_kernel_name(int act_bits, int64_t total_rows, int64_t src_rows,
                                           const bpg_weights_desc *w);
 
