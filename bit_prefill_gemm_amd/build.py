@@ -57,7 +57,7 @@ def _native_commands(obj, out):
                    "-c", os.path.join(CSRC, "native.cpp"), "-o", obj]
     link_cmd = ["g++", "-shared", obj, "-o", out, "-L", HERE, "-l:libbpg.so",
                 "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
-                "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+                "-ltorch_hip", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
     return compile_cmd, link_cmd
 
 

@@ -15,6 +15,7 @@
 // reported the same way with or without a GPU.
 #include <torch/csrc/python_headers.h>
 
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -219,8 +220,11 @@ c10::Device one_device(const char *where, std::initializer_list<const at::Tensor
     return first;
 }
 
+// a new tensor beside `like`; for a cuda one without at::empty's dispatch
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like)
 {
+    if (like.is_cuda())
+        return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
     return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
