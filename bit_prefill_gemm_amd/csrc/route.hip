@@ -304,7 +304,13 @@ __device__ __forceinline__ bool take_fast(const RouteProblem &p, uint32_t (&key)
     const int e = lane < taken ? expert() : 0;
     double k = (double)ls[e];
     if (approximate) {
-        const double s = p.sigmoid ? sigmoid_f64(ls[e]) : exp_f64(ls[e], top) / exp_sum<NE>(l, top);
+        double s;
+        if (p.sigmoid) {
+            s = sigmoid_f64(ls[e]);
+        } else {
+            const double sum = exp_sum<NE>(l, top); // 0 where every logit is -inf
+            s = sum > 0.0 ? exp_f64(ls[e], top) / sum : 0.0;
+        }
         k = fmax(s + (double)p.bias[e], -INFINITY);
     }
     int rank = 0;

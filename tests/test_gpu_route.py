@@ -145,6 +145,16 @@ def test_masked_logits(torch, score):
         check(torch, l, 8, score, renorm=False)
         check(torch, l, 8, score, bias=0.1 * rng.standard_normal(96))
         check(torch, l, 8, score, None, 8, 3, True)
+    # rows without an open expert and keys that tie or nearly do
+    for e in (40, 70):
+        l = np.full((3, e), -np.inf)
+        l[2, ::3] = 1.0
+        steps = np.float32(0.5) + (np.arange(e) % 5 * 2.0 ** -24).astype(np.float32)
+        check(torch, l, 6, score, bias=steps)
+        check(torch, l, 6, score, bias=np.zeros(e))
+        check(torch, l, 6, score)
+        check(torch, l, 4, score, steps, 10, 2, True)
+        check(torch, l, 4, score, steps, 5, 3, False)
     # experts that are switched off by their bias, for everybody
     b = np.zeros(96)
     b[rng.random(96) < 0.5] = -np.inf
