@@ -620,15 +620,15 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
                 red[(((grp * WK + wk) * R + (t - t0)) * RG + r) * 64 + lane] = acc[i][j][r];
         }
         __syncthreads();
+        if constexpr (EP) {
 #pragma unroll
-        for (int o = 0; o < (R + WK - 1) / WK; o++) {
-            const int tt = wk + o * WK;
-            if (tt >= R || t0 + tt >= C::kTiles)
-                break;
-            const int t = t0 + tt;
-            const int i = t / TN, j = t % TN;
-            const int64_t col = col0 + (wn * TN + j) * MF + rc;
-            if constexpr (EP) {
+            for (int o = 0; o < kOwn; o++) {
+                const int tt = wk + o * WK;
+                if (tt >= R || t0 + tt >= C::kTiles)
+                    break;
+                const int t = t0 + tt;
+                const int i = t / TN, j = t % TN;
+                const int64_t col = col0 + (wn * TN + j) * MF + rc;
                 const int64_t trow = row0 + (wm * TM + i) * MF;
                 float vr[RG];
                 const float bias = p.ep.bias ? ep_load(p.ep.bias, p.ep.bias_bf16, col) : 0.0f;
@@ -648,19 +648,24 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
                     const int rl = M::out_row(g, r);
                     if (rl < vrows[i])
                         store_y(p, (trow + rl) * p.ldy + col,
-                                p.ep.residual ? vr[r] + ep_value(p.ep, res[EP ? o : 0][r]) : vr[r]);
+                                p.ep.residual ? vr[r] + ep_value(p.ep, res[o][r]) : vr[r]);
                 }
-                continue;
             }
+        } else {
+            for (int tt = wk; tt < R && t0 + tt < C::kTiles; tt += WK) {
+                const int t = t0 + tt;
+                const int i = t / TN, j = t % TN;
+                const int64_t col = col0 + (wn * TN + j) * MF + rc;
 #pragma unroll
-            for (int r = 0; r < RG; r++) {
-                float v = red[(((grp * WK + 0) * R + tt) * RG + r) * 64 + lane];
+                for (int r = 0; r < RG; r++) {
+                    float v = red[(((grp * WK + 0) * R + tt) * RG + r) * 64 + lane];
 #pragma unroll
-                for (int w = 1; w < WK; w++)
-                    v += red[(((grp * WK + w) * R + tt) * RG + r) * 64 + lane];
-                const int rl = M::out_row(g, r);
-                if (rl < vrows[i])
-                    store_y(p, (row0 + (wm * TM + i) * MF + rl) * p.ldy + col, v * unscale);
+                    for (int w = 1; w < WK; w++)
+                        v += red[(((grp * WK + w) * R + tt) * RG + r) * 64 + lane];
+                    const int rl = M::out_row(g, r);
+                    if (rl < vrows[i])
+                        store_y(p, (row0 + (wm * TM + i) * MF + rl) * p.ldy + col, v * unscale);
+                }
             }
         }
         __syncthreads();
