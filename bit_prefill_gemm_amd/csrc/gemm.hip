@@ -674,29 +674,22 @@ __global__ __launch_bounds__(C::kThreads, C::kOcc) void w4a4_kernel(GemmProblem 
 
 // ---------------------------------------------------------------- launchers
 
-template <class C, int MODE>
+template <class C, int MODE, bool EP = false>
 hipError_t launch_cfg(const GemmProblem &p, int tiles_m, int tiles_n, int tm0, int tn0,
                       int64_t grid, hipStream_t stream)
 {
     if (grid <= 0)
         return hipSuccess;
-    if constexpr (MODE == kGemm) {
-        if (p.epilogue) {
-            w4a4_kernel<C, MODE, true><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(
-                p, tiles_m, tiles_n, tm0, tn0);
-            return hipGetLastError();
-        }
-    }
-    w4a4_kernel<C, MODE, false><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(
+    w4a4_kernel<C, MODE, EP><<<dim3((unsigned)grid), C::kThreads, 0, stream>>>(
         p, tiles_m, tiles_n, tm0, tn0);
     return hipGetLastError();
 }
 
-template <class C>
+template <class C, bool EP = false>
 hipError_t launch_dense_cfg(const GemmProblem &p, hipStream_t stream)
 {
     const int tm = (int)((p.rows + C::BM - 1) / C::BM), tn = (int)(p.n / C::BN);
-    return launch_cfg<C, kGemm>(p, tm, tn, 0, 0, (int64_t)tm * tn, stream);
+    return launch_cfg<C, kGemm, EP>(p, tm, tn, 0, 0, (int64_t)tm * tn, stream);
 }
 
 // Dense tile shapes.  The wide shapes run one 8-wave workgroup per CU whose
@@ -788,6 +781,49 @@ hipError_t launch_dense_bits(int kernel, const GemmProblem &p, hipStream_t strea
     }
 }
 
+// The kernel of a product with an epilogue that the weight-stream kernel does
+// not run.  Its results need not equal w4a4_gemm's to the last bit, so the
+// strips also serve widths that are no multiple of 128 (the last strip's
+// missing tiles idle), and the rules go by the time alone.  Measured, us,
+// M x K x N, strips (S = row tiles x strips) against
+//   - 64 x 32 tiles, 4-bit: 1024 x 2080 x 1056 (S = 288) 20.8 / 17.8,
+//     64 x 5120 x 17376 (272) 38.9 / 35.4, 96 x 5120 x 17376 (408) 39.4 / 55.9,
+//     512 x 5120 x 4128 (528) 48.0 / 56.1; 8-bit: 512 x 512 x 1056 (144)
+//     8.6 / 7.9, 256 x 512 x 4128 (264) 9.5 / 12.0, 1024 x 5120 x 17376 (4352)
+//     268 / 469;
+//   - 64 x 160 tiles, 4-bit (wide): 1024 x 256 x 5120 16.0 / 22.7,
+//     1024 x 512 x 5120 20.0 / 23.1, 512 x 1024 x 5120 17.3 / 16.0,
+//     512 x 5120 x 5120 51.2 / 43.2; 8-bit (tiled): 512 x 512 x 5120
+//     12.4 / 14.5, 512 x 2048 x 5120 26.0 / 26.4, 512 x 17408 x 5120 157 / 146.
+template <int BITS>
+int plan_epilogue_bits(const GemmProblem &p)
+{
+    const int dense = plan_dense_bits<BITS>(p);
+    if (dense == kTiled16x64 || dense == kTiled16x32)
+        return dense; // 16 rows, K past the weight-stream kernel's LDS
+    if (BITS == 4 ? dense == kWide && p.k >= 1024 : dense == kTiled64x160 && p.k >= 4096)
+        return dense;
+    const int64_t strips = (p.rows + 31) / 32 * ((p.n + 127) / 128);
+    return strip_fits(p) && strips > (BITS == 4 ? 300 : 200) ? kStrip : kTiled64x32;
+}
+
+template <int BITS>
+hipError_t launch_epilogue_bits(int kernel, const GemmProblem &p, hipStream_t stream)
+{
+    using T = Tiles<BITS>;
+    switch (kernel) {
+    case kStrip: return launch_strip(p, stream);
+    case kTiled16x64: return launch_dense_cfg<typename T::T16x64, true>(p, stream);
+    case kTiled16x32: return launch_dense_cfg<typename T::T16x32, true>(p, stream);
+    case kTiled64x32: return launch_dense_cfg<typename T::T64x32, true>(p, stream);
+    default:
+        if constexpr (BITS == 4)
+            return launch_wide(p, stream);
+        else
+            return launch_dense_cfg<typename T::W64x160, true>(p, stream);
+    }
+}
+
 // Grouped: 32-row slots (row tiles past an expert's rows are skipped) and
 // 128, 64 or 32 columns per workgroup: four waves of 32 x 32, each over the
 // whole of K (an expert's K is short, so splitting it across waves would leave
@@ -841,6 +877,8 @@ int plan_gemm(const GemmProblem &p)
         return kChunks;
     if (skinny_fits(p))
         return kSkinny;
+    if (p.epilogue)
+        return p.act_bits == 4 ? plan_epilogue_bits<4>(p) : plan_epilogue_bits<8>(p);
     return p.act_bits == 4 ? plan_dense_bits<4>(p) : plan_dense_bits<8>(p);
 }
 
@@ -883,6 +921,9 @@ hipError_t launch_gemm(const GemmProblem &p, hipStream_t stream)
         return launch_skinny(p, stream);
     if (kernel == kChunks)
         return launch_chunks(p, stream);
+    if (p.epilogue)
+        return p.act_bits == 4 ? launch_epilogue_bits<4>(kernel, p, stream)
+                               : launch_epilogue_bits<8>(kernel, p, stream);
     return p.act_bits == 4 ? launch_dense_bits<4>(kernel, p, stream)
                            : launch_dense_bits<8>(kernel, p, stream);
 }

@@ -123,11 +123,15 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     const int64_t arow = p.k / 32 * C::kAB;
 
     int rt, ct;
-    strip_tile(blockIdx.x, gridDim.x, tiles_m, (int)(p.n / C::BN), parts_m, row_group, rt, ct);
+    strip_tile(blockIdx.x, gridDim.x, tiles_m, (int)((p.n + C::BN - 1) / C::BN), parts_m, row_group,
+               rt, ct);
     const int64_t row0 = (int64_t)rt * C::BM;
     const int64_t col0 = (int64_t)ct * C::BN;
     const int64_t rem = p.rows - 1 - row0;
     const int last_row = rem < C::BM - 1 ? (int)rem : C::BM - 1; // >= 0
+    // With an epilogue the last strip may hold fewer than TN tiles; the waves
+    // of the others repeat its last tile and store nothing.
+    const int last_tile = EP ? (int)min((p.n - col0) / 32, (int64_t)TN) - 1 : TN - 1;
 
     // ---- direct-load sources of this lane, relative to the stage (every
     //      offset stays under 2^31 for K <= 2^22)
@@ -142,7 +146,7 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     for (int u = 0; u < C::kWPerWave; u++) {
         const int i = wave + TN * u;
         const int b = 1024 * (i < C::kWLoads ? i : 0) + 16 * lane;
-        const int t = b / C::kWTile;
+        const int t = min(b / C::kWTile, last_tile);
         const int r = b % C::kWTile;
         const int gg = r / C::kGroupBytes;
         woff[u] = (uint32_t)((t * NG + gg) * C::kGroupBytes + r % C::kGroupBytes);
@@ -205,7 +209,7 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     // 271 against 260 us at 1024 x 5120 x 17408, and they are loaded at the end)
     uint32_t res[EP ? 16 : 1];
     auto load_residual = [&] {
-        const int64_t r0 = row0 * p.ep.ldr + col0 + wave * 32 + c;
+        const int64_t r0 = row0 * p.ep.ldr + col0 + min(wave, last_tile) * 32 + c;
 #pragma unroll
         for (int r = 0; r < 16; r++) {
             const int rl = min(4 * hk + 8 * (r >> 2) + (r & 3), last_row);
@@ -329,6 +333,8 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     const int64_t y0 = (row0 + 4 * hk) * p.ldy + col0 + wave * 32 + c;
     const int lim = last_row + 1 - 4 * hk; // rows of this lane's group that hold data
     if constexpr (EP) {
+        if (wave > last_tile)
+            return; // no barrier follows
         if (BITS == 8 && p.ep.residual)
             load_residual();
         const float bias =
@@ -360,8 +366,9 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
 
 bool strip_fits(const GemmProblem &p)
 {
-    return (p.act_bits == 4 || p.act_bits == 8) && p.experts == 1 && p.n % 128 == 0 &&
-           p.rows > 0 && (p.rows + 31) / 32 * (p.n / 128) < (int64_t)1 << 31;
+    return (p.act_bits == 4 || p.act_bits == 8) && p.experts == 1 &&
+           (p.n % 128 == 0 || p.epilogue) && p.rows > 0 &&
+           (p.rows + 31) / 32 * ((p.n + 127) / 128) < (int64_t)1 << 31;
 }
 
 // The XCD rectangles of strip_tile: the fewest row parts a (1, 2, 4, 8)
@@ -384,7 +391,7 @@ void strip_order(const GemmProblem &p, int tm, int tn, int &a, int &rg)
 
 hipError_t launch_strip(const GemmProblem &p, hipStream_t stream)
 {
-    const int tm = (int)((p.rows + 31) / 32), tn = (int)(p.n / 128);
+    const int tm = (int)((p.rows + 31) / 32), tn = (int)((p.n + 127) / 128);
     const int64_t grid = (int64_t)tm * tn;
     if (grid <= 0)
         return hipSuccess;

@@ -27,15 +27,17 @@ CASES = [
     (16, 2080, 160, 4, "weight-stream"), (9, 8192, 64, 8, "weight-stream"),
     (13, 32800, 32, 4, "tiled 16x32"), (9, 32800, 64, 8, "tiled 16x32"),
     (1025, 96, 2176, 4, "strip 32x128"), (1030, 160, 2176, 8, "strip 32x128"),
-    (512, 544, 5120, 4, "wide 64x160"), (449, 160, 5120, 8, "tiled 64x160"),
-    (1025, 96, 576, 4, "tiled 64x32"), (1041, 2080, 1056, 8, "tiled 64x32"),
-    (1000, 96, 4032, 8, "tiled 64x64"),
+    # strips over widths that leave one, two and three of the last strip's tiles
+    (640, 416, 2080, 4, "strip 32x128"), (601, 1056, 2112, 8, "strip 32x128"), (650, 96, 2144, 4, "strip 32x128"),
+    (512, 1056, 5120, 4, "wide 64x160"), (512, 544, 5120, 4, "strip 32x128"),
+    (449, 4128, 5120, 8, "tiled 64x160"), (1025, 96, 576, 4, "tiled 64x32"),
+    (1041, 2080, 1056, 4, "tiled 64x32"), (520, 96, 1056, 8, "tiled 64x32"),
     (17, 1024, 128, 8, "weight-stream chunks"), (31, 96, 64, 4, "weight-stream chunks"),
     (33, 416, 128, 4, "weight-stream chunks"), (100, 1056, 256, 8, "weight-stream chunks"),
     (77, 2080, 1056, 8, "weight-stream chunks"), (300, 32, 96, 4, "weight-stream chunks"),
     (40, 6560, 64, 4, "weight-stream chunks"), (50, 4000, 32, 8, "weight-stream chunks"),
-    (1024, 64, 512, 4, "weight-stream chunks"), (1025, 64, 512, 4, "strip 32x128"),
-    (512, 2048, 2048, 4, "weight-stream chunks"), (513, 2048, 2048, 8, "strip 32x128"),
+    (1024, 64, 512, 4, "weight-stream chunks"), (1025, 64, 512, 4, "tiled 64x32"),
+    (512, 2048, 2048, 4, "weight-stream chunks"), (513, 2048, 2048, 4, "tiled 64x32"),
     (20, 32768, 32, 4, "weight-stream chunks"), (20, 32800, 32, 4, "tiled 64x32"),
 ]
 
@@ -151,8 +153,6 @@ def test_empty_epilogue_is_the_product(torch, case):
     y = bb.w4a4_gemm_epilogue(codes, scales, bits, W)
     if bb.w4a4_gemm_kernel_name(bits, m, W) == kernel:
         assert torch.equal(y, bb.w4a4_gemm(codes, scales, bits, W))
-    else:
-        assert kernel == "weight-stream chunks"
     # bf16 output is the fp32 result rounded, and every run gives the same bits
     assert torch.equal(bb.w4a4_gemm_epilogue(codes, scales, bits, W, dtype=torch.bfloat16), y.bfloat16())
     assert torch.equal(bb.w4a4_gemm_epilogue(codes, scales, bits, W), y)
@@ -173,14 +173,14 @@ def test_every_step_on_every_kernel(torch, case):
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("kind", [None, "fp32", "bf16"])
 def test_activations_and_types(torch, act, kind):
-    for case in (CASES[13], CASES[22]):
+    for case in ((17, 1024, 128, 8, "weight-stream chunks"), (650, 96, 2144, 4, "strip 32x128")):
         check(torch, case, act, kind, None, "fp32")
         check(torch, case, act, None, kind, "bf16")
 
 
 def test_activations_far_out(torch):
     """Arguments far from zero: the activations reach 0 and x, never NaN, and stay as exact as near zero."""
-    case = CASES[15]
+    case = (33, 416, 128, 4, "weight-stream chunks")
     m, k, n, bits = case[:4]
     codes, scales, W, ref, mag = problem(m, k, n, bits)
     bias = torch.linspace(-200.0, 200.0, n, device="cuda")
@@ -195,6 +195,38 @@ def test_activations_far_out(torch):
         lim = limit(mag, k, t, y64, "fp32", act, True, False)
         assert (np.abs(y - y64)[~big] <= lim[~big]).all(), act
         assert (np.abs(y - y64)[big] <= 1e-6 * np.abs(t[big])).all(), act
+
+
+def random_weights(torch, n, k, seed):
+    """An image of random codes and scales, made on the GPU (its layout is the packer's)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    groups = (k // 32 + 3) // 4
+    img = torch.randint(0, 256, (n // 32 * groups, 2304), dtype=torch.uint8, device="cuda", generator=g)
+    scale = (0.002 + 0.018 * torch.rand(n // 32 * groups, 128, device="cuda", generator=g)).half()
+    img[:, 2048:] = scale.view(torch.uint8)
+    d = bb.WeightsDesc(0x57475042, 1, 32, 3, n, k, 1, img.numel(), 2048)
+    return bb.Weights(d, img.view(-1))
+
+
+@pytest.mark.parametrize("m,k,n,bits,kernel", [(9, 32896, 16448, 4, "tiled 16x64"), (3, 32896, 16448, 8, "tiled 16x64"),
+                                               (25, 512, 16640, 4, "weight-stream"), (32, 1024, 16640, 8, "weight-stream"),
+                                               (500, 1024, 5120, 4, "wide 64x160")])
+def test_steps_on_the_products_own_result(torch, m, k, n, bits, kernel):
+    """Where both entry points run the same kernel, bias, relu and residual are single fp32
+    operations on w4a4_gemm's result: equal bit for bit."""
+    W = random_weights(torch, n, k, m)
+    assert bb.w4a4_gemm_epilogue_kernel_name(bits, m, W) == kernel == bb.w4a4_gemm_kernel_name(bits, m, W)
+    print("own result", m, k, n, bits, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m + 1)
+    x = torch.randn(m, k, device="cuda", generator=g)
+    codes, scales = bb.quantize_act_h32(x, bits)
+    t = bb.w4a4_gemm(codes, scales, bits, W)
+    bias = torch.randn(n, device="cuda", generator=g)
+    res = torch.randn(m, n, device="cuda", generator=g).bfloat16()
+    y = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=bias, activation="relu", residual=res)
+    assert torch.equal(y, torch.relu(t + bias) + res.float())
+    y = bb.w4a4_gemm_epilogue(codes, scales, bits, W, residual=res, dtype=torch.bfloat16)
+    assert torch.equal(y, (t + res.float()).bfloat16())
 
 
 def test_unrotated_and_stamps(torch):
