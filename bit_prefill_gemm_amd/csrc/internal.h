@@ -101,7 +101,8 @@ struct GemmProblem {
 enum Kernel {
     kNoKernel = 0,
     kSkinny,       // weight-stream kernel, M <= 32 (skinny.hip)
-    kChunks,       // the same over chunks of 16 rows, with an epilogue only
+    kChunks,       // the same over chunks of 16 rows and tiles of 16 or 32 columns,
+                   // with an epilogue only
     kWide,         // 64 x 160 direct-load tiles, 4-bit (wide.hip)
     kStrip,        // 32 x 128 strips (strip.hip)
     kTiled64x160,  // tiled kernel shapes (gemm.hip)

@@ -50,7 +50,7 @@ template <int BITS_, int TM_, int NW_, int TN_, int D_, bool AL_>
 struct SkCfg {
     static constexpr int BITS = BITS_, TM = TM_, NW = NW_;
     static constexpr int TN = TN_;                    // 16-column tiles per workgroup: one image tile
-    static_assert(TN == 2, "one 32-column image tile per workgroup");
+    static_assert(TN == 1 || TN == 2, "half an image tile per workgroup, or one");
     static constexpr int kCols = 16 * TN;
     // groups of four blocks in flight per wave: one when a wave walks many
     // groups and reads its activation rows from L2, two otherwise.  Deeper
@@ -134,6 +134,7 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     }
     const int rows = (int)(p.rows - row0 < kRows ? p.rows - row0 : kRows);
     const int64_t col0 = tile * C::kCols;
+    const int half = TN == 1 ? (int)(tile & 1) : 0;
 
     float *Da = lds;
     // staged activation rows (AL): row m at act_lds + m * a_stride bytes
@@ -163,8 +164,8 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
     }
 #pragma unroll
     for (int j = 0; j < TN; j++) {
-        // 16-column tile j is half j of the image tile
-        vw[j] = (uint32_t)((g * 32 + 16 * j + c) * 16);
+        // 16-column tile j is half j (TN = 1: `half`) of the image tile
+        vw[j] = (uint32_t)((g * 32 + 16 * (j + half) + c) * 16);
     }
 
     // ring of D groups of operands in registers
@@ -252,7 +253,8 @@ __global__ __launch_bounds__(C::kThreads) void skinny_kernel(GemmProblem p)
                 da[i] = *reinterpret_cast<const float4 *>(Da + b * kRows + 16 * i + 4 * g);
 #pragma unroll
             for (int j = 0; j < TN; j++) {
-                const uint32_t hp = j == 0 ? (q < 2 ? rdw[d].x : rdw[d].y) : (q < 2 ? rdw[d].z : rdw[d].w);
+                const uint32_t hp = j + half == 0 ? (q < 2 ? rdw[d].x : rdw[d].y)
+                                                  : (q < 2 ? rdw[d].z : rdw[d].w);
                 const uint16_t hb = (uint16_t)((q & 1) ? hp >> 16 : hp & 0xFFFFu);
                 const float dw = half_bits_to_float(hb);
                 const float cm = -kMagic * dw; // exact: dw has 11 significant bits
@@ -427,10 +429,12 @@ hipError_t launch_cfg(const GemmProblem &p, hipStream_t stream)
     const size_t lds = skinny_lds<C>(p);
     const int64_t chunks = (p.rows + C::kRows - 1) / C::kRows;
     const dim3 grid((unsigned)(p.n / C::kCols * chunks));
-    if (p.epilogue)
+    if (C::TN == 1 || p.epilogue) {
         skinny_kernel<C, true><<<grid, C::kThreads, lds, stream>>>(p);
-    else
-        skinny_kernel<C, false><<<grid, C::kThreads, lds, stream>>>(p);
+    } else {
+        if constexpr (C::TN == 2)
+            skinny_kernel<C, false><<<grid, C::kThreads, lds, stream>>>(p);
+    }
     return hipGetLastError();
 }
 
@@ -505,7 +509,7 @@ bool skinny_fits(const GemmProblem &p)
     return (p.k / 32 + 3) / 4 * 4 * rows_cov * 4 <= 65536;
 }
 
-// With an epilogue the kernel also runs more rows, in chunks of 16:
+// With an epilogue the kernel also runs more rows than 32, in chunks of 16:
 // every chunk streams the weights again, from L2 but for the first, and its
 // workgroups' waves split K, so the time of a product with few output tiles is
 // that of a wave's share of K instead of the whole of K in series.  T = chunks
@@ -517,15 +521,26 @@ bool skinny_fits(const GemmProblem &p)
 // 21.0 / 22.4 (one chunk of 32 rows); just past the bounds, 256 x 512 x 5120
 // (T = 2560) 12.4 / 9.8, 64 x 2048 x 17408 (T = 2176) 17.5 / 19.9 and
 // 96 x 5120 x 17408 (T = 3264) 49.7 / 40.3.
+//
+// With T <= 128 a workgroup takes half an image tile (16 columns), so that
+// twice as many CUs stream: 1 x 5120 x 1024 6.4 -> 5.5, 100 x 5120 x 512
+// 6.8 -> 6.0, 64 x 17408 x 640 13.5 -> 10.7; at T = 160 (1 x 5120 x 5120)
+// 7.1 -> 7.8.
+int64_t chunk_tiles(const GemmProblem &p) { return (p.rows + 15) / 16 * (p.n / 32); }
+
+constexpr int64_t kHalfTiles = 128;
+
 bool chunks_fit(const GemmProblem &p)
 {
-    const int64_t t = (p.rows + 15) / 16 * (p.n / 32);
-    return p.epilogue && p.rows > 16 && (p.k / 32 + 3) / 4 * 4 * 16 * 4 <= 65536 &&
-           t <= (p.k >= 2048 ? 2048 : 1024);
+    const int64_t t = chunk_tiles(p);
+    return p.epilogue && (p.rows > 16 || t <= kHalfTiles) &&
+           (p.k / 32 + 3) / 4 * 4 * 16 * 4 <= 65536 && t <= (p.k >= 2048 ? 2048 : 1024);
 }
 
 hipError_t launch_chunks(const GemmProblem &p, hipStream_t stream)
 {
+    if (chunk_tiles(p) <= kHalfTiles)
+        return p.act_bits == 4 ? launch_tn<4, 1, 1>(p, stream) : launch_tn<8, 1, 1>(p, stream);
     return p.act_bits == 4 ? launch_tm<4, 1>(p, stream) : launch_tm<8, 1>(p, stream);
 }
 

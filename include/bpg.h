@@ -334,9 +334,8 @@ bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64
  *   ep        host, not NULL; read during the call only
  *   y         device, [m][ldy] of y_dt; fp32: ldy % 4 == 0, bf16: ldy % 8 == 0
  * Other arguments as w4a4_gemm.  The kernel is the one that
- * w4a4_gemm_epilogue_kernel_name names; with more than 16 rows and few output
- * tiles it is another one than w4a4_gemm's, which adds the blocks' sums in
- * another (fixed) order.
+ * w4a4_gemm_epilogue_kernel_name names, for many shapes another one than
+ * w4a4_gemm's, which adds the blocks' sums in another (fixed) order.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, STAMP, DEVICE, LAUNCH.
  */
 typedef struct {
