@@ -248,7 +248,7 @@ __device__ __forceinline__ bool take_fast(const RouteProblem &p, uint32_t (&key)
     constexpr float tol1 = (2 + 2 * (NE - 1)) * 0x1p-24f;
 #pragma unroll
     for (int i = 0; i < NE; i++)
-        key[i] = key[i] != 0 ? (key[i] & ~(uint32_t)(NE - 1)) | (NE - 1 - i) : 0u;
+        key[i] = (key[i] & ~(uint32_t)(NE - 1)) | (NE - 1 - i); // below NE: not in the choice
     sort_lane<NE>(key);
     uint32_t word = 0; // lane j keeps the word of choice j
     int from = 0;      // and its lane
@@ -269,7 +269,7 @@ __device__ __forceinline__ bool take_fast(const RouteProblem &p, uint32_t (&key)
             key[NE - 1] &= ~pop;
         }
     };
-    // bit j: words j and j + 1 are too close (a word of 0: nothing was left)
+    // bit j: words j and j + 1 are too close (a word below NE: nothing was left)
     auto too_close = [&]() -> uint64_t {
         const uint32_t next = (uint32_t)__shfl_down((int)word, 1);
         bool close;
@@ -280,7 +280,7 @@ __device__ __forceinline__ bool take_fast(const RouteProblem &p, uint32_t (&key)
         } else {
             close = (word ^ next) < NE;
         }
-        return __ballot(close && next != 0 && lane + 1 < count);
+        return __ballot(close && next >= NE && lane + 1 < count);
     };
     auto expert = [&]() { return (NE - 1 - (int)(word & (NE - 1))) * 64 + from; };
 
@@ -300,7 +300,7 @@ __device__ __forceinline__ bool take_fast(const RouteProblem &p, uint32_t (&key)
         take(count + 1);
         close = too_close();
     }
-    const int taken = __popcll(__ballot(word != 0)); // of count: the experts may have run out
+    const int taken = __popcll(__ballot(word >= NE)); // of count: the experts may have run out
     const int e = lane < taken ? expert() : 0;
     double k = (double)ls[e];
     if (approximate) {
@@ -374,10 +374,12 @@ __device__ __forceinline__ bool choose(const RouteProblem &p, const float (&l)[N
             tol0 = 5 * 0x1p-24f;
         } else {
             V sum = 0;
+            // (a row of -inf only: 0 instead of the difference of infinities)
+            const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
             for (int i = 0; i < NE; i++) {
                 if constexpr (fast)
-                    score[i] = l[i] == -INFINITY ? 0.0f : exp_fast(l[i] - top);
+                    score[i] = exp_fast(l[i] - base);
                 else
                     score[i] = exp_f64(l[i], top);
                 sum += score[i];
