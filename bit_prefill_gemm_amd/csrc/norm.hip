@@ -261,10 +261,12 @@ __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
         live[r] = b < nb;
         at[r] = (live[r] ? b : 0) * 32 + 8 * t;
     }
-    // few blocks per lane: the next row's values are loaded a row ahead
-    constexpr bool ahead = R <= 2;
-    Raw<Tx> rx[ahead ? R : 1];
-    Raw<Tr> rr[ahead ? R : 1];
+    // as far as the registers go, the next row's values are loaded a row ahead,
+    // or a row's values all before the first is used
+    constexpr bool ahead = R <= 2 || (R == 3 && sizeof(Tx) + sizeof(Tr) == 4);
+    constexpr bool whole = R <= 3;
+    Raw<Tx> rx[whole ? R : 1];
+    Raw<Tr> rr[whole ? R : 1];
     auto load_row = [&](int64_t row) {
 #pragma unroll
         for (int r = 0; r < R; r++)
@@ -311,10 +313,12 @@ __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
     for (int64_t row = blockIdx.x; row < p.m; row += gridDim.x, parity ^= 1) {
         float v[R][8];
         double ss = 0.0;
+        if constexpr (whole && !ahead)
+            load_row(row);
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            const int q = ahead ? r : 0;
-            if constexpr (!ahead) {
+            const int q = whole ? r : 0;
+            if constexpr (!whole) {
                 rx[0].load(x + row * p.ldx + at[r]);
                 if (res)
                     rr[0].load(res + row * p.ldr + at[r]);
@@ -448,10 +452,11 @@ hipError_t launch_norm_rounds(const NormProblem &p, hipStream_t stream)
         kernel<<<grid, dim3((unsigned)(64 * waves)), 0, stream>>>(p);
     };
     // One block per quad while every row has a workgroup at once (the shortest
-    // chain from the loads to the stores); with more rows than that, two: half
-    // the reductions and barriers a row.
-    const bool once = p.m <= (int64_t)kCUs * (32 / ((nb + 15) / 16 < 32 ? (nb + 15) / 16 : 32));
-    if (nb <= 256 && (once || nb < 32))
+    // chain from the loads to the stores); with more rows than that, two (half
+    // the reductions and barriers a row), unless more lanes would idle.
+    const int w1 = (nb + 15) / 16, w2 = (nb + 31) / 32;
+    const bool once = w1 <= 16 && p.m <= (int64_t)kCUs * (32 / w1);
+    if (w1 <= 16 && (once || 2 * w2 > w1))
         launch(norm_quantize_kernel<Tx, Tr, BITS, 1>, 1, 32);
     else if (nb <= 512)
         launch(norm_quantize_kernel<Tx, Tr, BITS, 2>, 2, 20);

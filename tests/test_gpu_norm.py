@@ -192,6 +192,26 @@ def test_many_rows_walk_the_grid(torch):
     assert int((scales > 0).sum()) == m
 
 
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("fp32", "fp32"), ("bf16", None)])
+def test_more_rows_than_fit_at_once(torch, xt, rt):
+    """Workgroups that walk several rows, one to eight blocks per quad, the rows' loads ahead or not."""
+    for m, k, bits in ((8200, 64, 4), (2000, 544, 4), (1700, 2048, 8), (1300, 8224, 4), (300, 17408, 4),
+                       (270, 32768, 8), (260, 33792, 4)):
+        print("norm many rows", xt, rt, m, k, bits, flush=True)
+        g = torch.Generator(device="cuda").manual_seed(m + k)
+        types = {"bf16": torch.bfloat16, "fp32": torch.float32}
+        x = torch.randn(m, k, device="cuda", generator=g).to(types[xt])
+        r = None if rt is None else torch.randn(m, k, device="cuda", generator=g).to(types[rt])
+        w = torch.rand(k, device="cuda", generator=g)
+        h, codes, scales = bb.rmsnorm_quantize_act(x, residual=r, weight=w, act_bits=bits)
+        rows = np.unique(np.r_[0:3, m // 2, m - 40:m:7, m - 1, 255, 256, min(m - 1, 1024)])
+        at = torch.from_numpy(rows).cuda()
+        ref_h, v = expected(host(x[at]), None if r is None else host(r[at]), host(w), 1e-6)
+        q, d = quantized(v, bits, 32)
+        assert np.array_equal(host(h[at]), ref_h)
+        assert np.array_equal(host(codes[at]), oracle_codes(q, bits)) and np.array_equal(host(scales[at]), d)
+
+
 def test_zero_tiny_and_huge_rows(torch):
     k = 256
     rng = np.random.default_rng(5)
