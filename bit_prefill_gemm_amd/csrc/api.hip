@@ -11,6 +11,7 @@
 #include <cstring>
 
 #include "bpg.h"
+#include "between.h"
 #include "internal.h"
 
 namespace {

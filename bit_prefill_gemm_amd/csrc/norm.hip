@@ -28,7 +28,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "internal.h"
+#include "between.h"
 #include "rotate.h"
 
 namespace bpg {

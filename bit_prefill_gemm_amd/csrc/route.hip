@@ -26,7 +26,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "internal.h"
+#include "between.h"
 
 namespace bpg {
 
