@@ -9,8 +9,8 @@
 // result: the residual may be y itself, so a load after a store could not be
 // moved ahead of it and would wait for it.  They are loaded as raw bits and
 // converted where they are added, so that nothing waits for them before.
-// With a bf16 residual, 512 x 5120 x 5120 takes 39.4 us (39.1 without one; 43.6
-// with the loads where the values are added).
+// 512 x 5120 x 5120 takes 39.4 us with a bf16 residual and 38.9 without; with
+// the loads where the values are added 43.6.
 #pragma once
 
 #include <hip/hip_runtime.h>

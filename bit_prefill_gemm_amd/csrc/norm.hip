@@ -13,9 +13,11 @@
 //   v_i = (h_i * s) * g_i    two fp32 roundings
 // then the rotation and quantization of quantize.hip on v, step by step.
 // The squares of fp32 values are exact in fp64 and their sum is off by less
-// than k 2^-53, so s does not depend on the order of the sum (but for about
-// one row in 10^8, next to a rounding border) and the codes are those of a
-// plain evaluation, bit for bit.  The fp64 sum is one instruction per value.
+// than k 2^-53 relative, so s depends on the order of the sum only where the
+// exact value lies that close to a rounding border of fp32: at most k rows in
+// 2^29 by that bound, some k^(1/2) in 2^29 with the usual cancelling of
+// roundings.  The codes of all others are a plain evaluation's, bit for bit.
+// The fp64 sum is a conversion and an FMA per value.
 //
 // A row belongs to a workgroup, a 32-block to a quad of lanes (lane t holds
 // elements 8t..8t+7: one 16-byte load per 8 bf16 values), R blocks per quad in
@@ -59,7 +61,6 @@ template <> struct Raw<uint16_t> {
     u32x4 w;
     __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const u32x4 *>(p); }
     __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<u32x4 *>(p) = w; }
-    __device__ __forceinline__ void zero() { w = u32x4{0, 0, 0, 0}; }
     __device__ __forceinline__ float at(int i) const
     {
         return __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
@@ -84,7 +85,6 @@ template <> struct Raw<float> {
         *reinterpret_cast<float4 *>(p) = a;
         *reinterpret_cast<float4 *>(p + 4) = b;
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ float at(int i) const
     {
         return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w
