@@ -178,10 +178,15 @@ void check_bits(const char *where, int64_t bits)
         fail(where, "act_bits must be 4 or 8, got %lld", (long long)bits);
 }
 
-void check_span(const char *where, int64_t rotation, int64_t k)
+void check_rotation(const char *where, int64_t rotation)
 {
     if (rotation != 0 && rotation != 32 && rotation != 64 && rotation != 128)
         fail(where, "rotation must be 0, 32, 64 or 128, got %lld", (long long)rotation);
+}
+
+void check_span(const char *where, int64_t rotation, int64_t k)
+{
+    check_rotation(where, rotation);
     const int64_t unit = rotation ? rotation : 32;
     if (k <= 0 || k % unit != 0)
         fail(where, "K = %lld is not a positive multiple of %lld", (long long)k, (long long)unit);
@@ -390,6 +395,7 @@ PyObject *w4a4_gemm_epilogue(PyObject *, PyObject *const *a, Py_ssize_t)
         const bpg_weights_desc *w =
             reinterpret_cast<const bpg_weights_desc *>(static_cast<uintptr_t>(integer(a[3])));
         check_bits(where, bits);
+        check_rotation(where, rotation);
         const int64_t m = codes.size(0), n = w->n;
         check_codes(where, codes, scales, bits, m, w->k);
         if (!THPVariable_Check(a[4]))

@@ -207,6 +207,28 @@ def test_product_binding_checks():
            dtype=torch.bfloat16, match="cuda device")
 
 
+@pytest.mark.parametrize("rotation", [16, -32, 256, (1 << 32) + 32, 1 << 32])
+def test_product_binding_refuses_other_spans(rotation):
+    """Also those that a C int would turn into a valid one."""
+    W = bb.Weights(desc(n=96), torch.zeros(3 * 2304, dtype=torch.uint8))
+    raises(bb.w4a4_gemm_epilogue, torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4), 4, W,
+           rotation=rotation, match="rotation must be")
+
+
+@pytest.mark.parametrize("bits,m,n,k,name", [
+    (4, 0, 5120, 5120, "none"), (4, 1, 1024, 5120, "weight-stream chunks"),
+    (4, 1, 5120, 5120, "weight-stream"), (8, 77, 1056, 2080, "weight-stream chunks"),
+    (4, 512, 5120, 5120, "wide 64x160"), (8, 512, 5120, 17408, "tiled 64x160"),
+    (4, 1024, 17408, 5120, "strip 32x128"), (8, 1024, 17376, 5120, "strip 32x128"),
+    (4, 1024, 1056, 2080, "tiled 64x32"),
+])
+def test_product_epilogue_kernels(bits, m, n, k, name):
+    if m == 0:
+        name = bb.lib().w4a4_gemm_kernel_name(bits, 0, ctypes.byref(desc(n, k))).decode()
+    got = bb.lib().w4a4_gemm_epilogue_kernel_name(bits, m, ctypes.byref(desc(n, k)))
+    assert got.decode() == name
+
+
 def test_route_binding_checks():
     f = bb.moe_route_topk
     logits = torch.zeros(4, 16)
