@@ -71,9 +71,11 @@ __device__ __forceinline__ void ep_activate(int act, float (&v)[N])
             v[i] = v[i] * ep_sigmoid(v[i]);
         break;
     case BPG_ACT_GELU:
+        // x Phi(x) = x / 2 erfc(-x / sqrt 2): 1 + erf would cancel below zero
+        // (4% off at -5, 0 from -6 on)
 #pragma unroll
         for (int i = 0; i < N; i++)
-            v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+            v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
         break;
     case BPG_ACT_GELU_TANH:
         // 0.5 (1 + tanh u) = sigmoid(2 u), u = sqrt(2 / pi) (x + 0.044715 x^3)

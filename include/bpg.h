@@ -323,8 +323,9 @@ bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64
  * joins them there).  With t = the fp32 result of w4a4_gemm (w4a4_gemm_rot,
  * w4a4_gemm_unrotated for rotation 64 / 128, 0):
  *   y = act(t + bias[column]) + residual[row][column]
- * each step in fp32 (the exponential, erf and reciprocal of an activation
- * within a few units in the last place), rounded once to y's type.  Where both
+ * each step in fp32 (the exponential, erfc and reciprocal of an activation
+ * within a few units in the last place; GELU is v / 2 erfc(-v / sqrt 2), whose
+ * tail below zero keeps its relative accuracy), rounded once to y's type.  Where both
  * run the same kernel (see the routing queries below), with no bias,
  * BPG_ACT_NONE and no residual every element equals w4a4_gemm's (or its bf16
  * rounding).

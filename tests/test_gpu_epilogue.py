@@ -262,3 +262,43 @@ def test_no_rows(torch):
                               torch.empty(0, 8, device="cuda"), 4, W,
                               residual=torch.empty(0, 64, device="cuda"), bias=torch.zeros(64, device="cuda"))
     assert y.shape == (0, 64)
+
+
+# every kernel that an epilogue runs, the weight-stream one with one and two row tiles
+TAILS = [(16, 512, 16416, 4, "weight-stream"), (25, 512, 16640, 4, "weight-stream"),
+         (33, 416, 128, 4, "weight-stream chunks"), (650, 96, 2144, 4, "strip 32x128"),
+         (601, 1056, 2112, 8, "strip 32x128"), (512, 1056, 5120, 4, "wide 64x160"),
+         (449, 4128, 5120, 8, "tiled 64x160"), (1025, 96, 576, 4, "tiled 64x32")]
+
+
+def own_result(torch, case, act):
+    """(t, y), where the product is exactly 0 (all codes are), so that t is the bias itself."""
+    m, k, n, bits, kernel = case
+    W = random_weights(torch, n, k, 1)
+    assert bb.w4a4_gemm_epilogue_kernel_name(bits, m, W) == kernel
+    print("tails", case, act, flush=True)
+    t = np.random.default_rng(n).permutation(np.linspace(-130.0, 20.0, n)).astype(np.float32)
+    t[:8] = -5.5, -12.5, -90.0, -104.0, 1e-30, -1e-30, -1e30, 0.0
+    codes = torch.zeros(m, k * bits // 8, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(m, k // 32, device="cuda")
+    y = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=torch.from_numpy(t).cuda(), activation=act)
+    assert (y == y[0]).all()
+    return t.astype(np.float64), host(y[0]).astype(np.float64)
+
+
+def off(y, y64, relative, absolute):
+    err, lim = np.abs(y - y64), (relative * np.abs(y64) + absolute) * (1 + 2.0 ** -10)
+    bad = np.flatnonzero(~(err <= lim))
+    return [(y[i], y64[i], err[i] / lim[i]) for i in bad[:5]]
+
+
+@pytest.mark.parametrize("case", TAILS, ids=["%dx%dx%d-%d" % c[:4] for c in TAILS])
+def test_gelu_tail(torch, case):
+    """GELU relative to its result, down to where erfc leaves fp32's normal numbers (below them
+    erfc may be 0: times |t| / 2 < 8 that is 2^-123).  y = t / 2 erfc(x), x = -t / sqrt 2 with the
+    constant's rounding and the product's (1.3 2^-24), which enter times
+    |d ln erfc / d ln x| <= x (x + sqrt(x^2 + 2)) <= t^2 + 1; erfc within the 16 ulp that OpenCL
+    asks of it (32 2^-24), and a product's rounding."""
+    t, y = own_result(torch, case, "gelu")
+    y64 = 0.5 * t * np.vectorize(math.erfc, otypes=[np.float64])(-t / math.sqrt(2.0))
+    assert off(y, y64, 2.0 ** -24 * (33 + 1.3 * (np.minimum(t * t, 200.0) + 1)), 2.0 ** -123) == []
