@@ -302,3 +302,43 @@ def test_gelu_tail(torch, case):
     t, y = own_result(torch, case, "gelu")
     y64 = 0.5 * t * np.vectorize(math.erfc, otypes=[np.float64])(-t / math.sqrt(2.0))
     assert off(y, y64, 2.0 ** -24 * (33 + 1.3 * (np.minimum(t * t, 200.0) + 1)), 2.0 ** -123) == []
+
+
+@pytest.mark.parametrize("case", TAILS, ids=["%dx%dx%d-%d" % c[:4] for c in TAILS])
+def test_silu_tail(torch, case):
+    """SiLU relative to its result, down to fp32's subnormal numbers: the sigmoid within 8 2^-24
+    and a product's rounding; a subnormal result is rounded to a multiple of 2^-149 at most twice."""
+    t, y = own_result(torch, case, "silu")
+    with np.errstate(over="ignore"):
+        y64 = t / (1.0 + np.exp(-t))
+    assert off(y, y64, 9 * 2.0 ** -24, 2.0 ** -149) == []
+
+
+@pytest.mark.parametrize("case", TAILS, ids=["%dx%dx%d-%d" % c[:4] for c in TAILS])
+def test_gelu_tanh_tail(torch, case):
+    """As SiLU at z = 2 sqrt(2 / pi) (t + 0.044715 t^3), whose roundings are within 7 2^-24 (the
+    cubic's constant and three products, a sum, the factor's constant and its product) and enter
+    times |d ln sigmoid / d ln z| <= |z|; beyond |z| = 150 the result is 0 or t."""
+    t, y = own_result(torch, case, "gelu_tanh")
+    z = 2.0 * math.sqrt(2.0 / math.pi) * (t + 0.044715 * t ** 3)
+    with np.errstate(over="ignore"):
+        y64 = t / (1.0 + np.exp(-z))
+    assert off(y, y64, 2.0 ** -24 * (9 + 7 * np.minimum(np.abs(z), 150.0)), 2.0 ** -149) == []
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("case", TAILS, ids=["%dx%dx%d-%d" % c[:4] for c in TAILS])
+def test_far_values_leave_the_others_their_bits(torch, case, act):
+    """Alone in its columns' wave or beside values far out, a value's result is the same."""
+    m, k, n, bits = case[:4]
+    W = random_weights(torch, n, k, 2)
+    codes = torch.zeros(m, k * bits // 8, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(m, k // 32, device="cuda")
+    near = torch.from_numpy(np.random.default_rng(m).uniform(-60.0 if act == "silu" else -8.0, 20.0, n).astype(np.float32)).cuda()
+    far = near.clone()
+    at = torch.arange(n, device="cuda") % 3 == 0
+    far[at] = torch.linspace(-130.0, -9.0, int(at.sum()), device="cuda")
+    print("neighbours", case, act, flush=True)
+    a = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=near, activation=act)
+    b = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=far, activation=act)
+    assert torch.equal(a[:, ~at], b[:, ~at]) and not torch.equal(a[:, at], b[:, at])
