@@ -65,6 +65,18 @@ PyObject *guarded(F &&body)
     END_HANDLE_TH_ERRORS
 }
 
+// f() without the interpreter's lock: an allocation may wait for the device
+// and a launch for room in its queue, and what is before it there may be a
+// host callback that needs the lock.  f touches no Python object.
+template <class F> auto unlocked(F &&f)
+{
+    struct Unlocked {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    } guard;
+    return f();
+}
+
 int64_t integer(PyObject *o)
 {
     const long long v = PyLong_AsLongLong(o);
@@ -229,7 +241,9 @@ c10::Device one_device(const char *where, std::initializer_list<const at::Tensor
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &like)
 {
     if (like.is_cuda())
-        return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+        return unlocked([&] {
+            return at::Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+        });
     return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
@@ -281,6 +295,7 @@ PyObject *rmsnorm_quantize_act(PyObject *, PyObject *const *a, Py_ssize_t)
         const bpg_x_dtype x_dt = float_code(where, "x", x.scalar_type());
         check_rows(where, "x", x);
         const int64_t bits = integer(a[4]), rotation = integer(a[5]);
+        const float eps = (float)number(a[3]);
         check_bits(where, bits);
         const int64_t m = x.size(0), k = x.size(1);
         check_span(where, rotation, k);
@@ -320,12 +335,14 @@ PyObject *rmsnorm_quantize_act(PyObject *, PyObject *const *a, Py_ssize_t)
         check_codes(where, codes, scales, bits, m, k);
         const c10::Device device = one_device(where, {&x, &residual, &h, &weight, &codes, &scales});
         const c10::DeviceGuard guard(device);
-        check_status(where, ::rmsnorm_quantize_act(
-                                address(x), x_dt, row_stride(x, 4), address(residual), r_dt,
-                                residual.defined() ? row_stride(residual, 4) : 0, address(h),
-                                h.defined() ? row_stride(h, 4) : 0, address(weight), w_dt,
-                                (float)number(a[3]), m, k, (int)bits, (int)rotation, address(codes),
-                                address<float>(scales), stream_of(device)));
+        check_status(where, unlocked([&] {
+                         return ::rmsnorm_quantize_act(
+                             address(x), x_dt, row_stride(x, 4), address(residual), r_dt,
+                             residual.defined() ? row_stride(residual, 4) : 0, address(h),
+                             h.defined() ? row_stride(h, 4) : 0, address(weight), w_dt, eps, m, k,
+                             (int)bits, (int)rotation, address(codes), address<float>(scales),
+                             stream_of(device));
+                     }));
         auto given = [](PyObject *o) { return Py_INCREF(o), o; };
         return tuple_of({!residual.defined() ? given(a[0]) : new_h ? wrap(h) : given(a[6]),
                          new_codes ? wrap(codes) : given(a[7]),
@@ -360,9 +377,11 @@ PyObject *dequantize_act(PyObject *, PyObject *const *a, Py_ssize_t)
         check_rows(where, "y", y);
         const c10::Device device = one_device(where, {&codes, &scales, &y});
         const c10::DeviceGuard guard(device);
-        check_status(where, ::dequantize_act(address(codes), address<float>(scales), (int)bits,
-                                             (int)rotation, m, k, address(y), y_dt,
-                                             row_stride(y, 4), stream_of(device)));
+        check_status(where, unlocked([&] {
+                         return ::dequantize_act(address(codes), address<float>(scales), (int)bits,
+                                                 (int)rotation, m, k, address(y), y_dt,
+                                                 row_stride(y, 4), stream_of(device));
+                     }));
         return made ? wrap(y) : (Py_INCREF(a[4]), a[4]);
     });
 }
@@ -434,10 +453,12 @@ PyObject *w4a4_gemm_epilogue(PyObject *, PyObject *const *a, Py_ssize_t)
         }
         const c10::Device device = one_device(where, {&codes, &scales, &image, &y, &bias, &residual});
         const c10::DeviceGuard guard(device);
-        check_status(where, ::w4a4_gemm_epilogue(address(codes), address<float>(scales), (int)bits,
-                                                 (int)rotation, m, w, address(image), &ep,
-                                                 address(y), y_dt, row_stride(y, 8),
-                                                 stream_of(device)));
+        check_status(where, unlocked([&] {
+                         return ::w4a4_gemm_epilogue(address(codes), address<float>(scales),
+                                                     (int)bits, (int)rotation, m, w, address(image),
+                                                     &ep, address(y), y_dt, row_stride(y, 8),
+                                                     stream_of(device));
+                     }));
         return made ? wrap(y) : (Py_INCREF(a[8]), a[8]);
     });
 }
@@ -483,15 +504,19 @@ PyObject *moe_route_topk(PyObject *, PyObject *const *a, Py_ssize_t)
         const int renormalize = PyObject_IsTrue(a[7]);
         if (renormalize < 0)
             throw Raised{};
+        const int64_t groups = integer(a[4]), topk_groups = integer(a[5]);
+        const float scale = (float)number(a[8]);
         const c10::Device device = one_device(where, {&logits, &bias, &ids, &weights});
         const c10::DeviceGuard guard(device);
-        check_status(where, ::moe_route_topk(
-                                address(logits), dt, tokens, experts, row_stride(logits, 1),
-                                score == "softmax" ? BPG_SCORE_SOFTMAX : BPG_SCORE_SIGMOID,
-                                address<float>(bias), integer(a[4]), integer(a[5]),
-                                group_score == "max" ? BPG_GROUP_MAX : BPG_GROUP_TOP2, topk,
-                                renormalize, (float)number(a[8]), address<int32_t>(ids),
-                                address<float>(weights), stream_of(device)));
+        check_status(where, unlocked([&] {
+                         return ::moe_route_topk(
+                             address(logits), dt, tokens, experts, row_stride(logits, 1),
+                             score == "softmax" ? BPG_SCORE_SOFTMAX : BPG_SCORE_SIGMOID,
+                             address<float>(bias), groups, topk_groups,
+                             group_score == "max" ? BPG_GROUP_MAX : BPG_GROUP_TOP2, topk,
+                             renormalize, scale, address<int32_t>(ids), address<float>(weights),
+                             stream_of(device));
+                     }));
         return tuple_of({new_ids ? wrap(ids) : (Py_INCREF(a[9]), a[9]),
                          new_weights ? wrap(weights) : (Py_INCREF(a[10]), a[10])});
     });

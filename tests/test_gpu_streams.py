@@ -2,7 +2,9 @@
 its own stream, give the same results as the same calls one after the other
 (the library keeps no per-call state; its one process-wide cache, the device
 check, is written once and atomically)."""
+import sys
 import threading
+import time
 
 import numpy as np
 import pytest
@@ -67,3 +69,57 @@ def test_two_threads_two_streams(torch):
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+def calls():
+    """The compiled entry points on small inputs with their outputs given."""
+    torch = torch_mod()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(4, 256, device="cuda", generator=g)
+    h = torch.empty_like(x)
+    _, codes, scales = bb.rmsnorm_quantize_act(x)
+    v = torch.empty_like(x)
+    W = weights_to_device(synth.draw_q4_0(np.random.default_rng(3), (64,), 256, 0.002, 0.02), 64, 256)
+    y = torch.empty(4, 64, device="cuda")
+    ids, w = bb.moe_route_topk(y.normal_(generator=g).clone(), 2)
+    return {"norm": lambda: bb.rmsnorm_quantize_act(x, residual=x, h=h, codes=codes, scales=scales),
+            "decode": lambda: bb.dequantize_act(codes, scales, y=v),
+            "product": lambda: bb.w4a4_gemm_epilogue(codes, scales, 4, W, y=y),
+            "route": lambda: bb.moe_route_topk(x, 2, expert_of=ids, weights=w)}
+
+
+@pytest.mark.parametrize("name", ["norm", "decode", "product", "route"])
+def test_other_threads_run_during_a_call(torch, name):
+    """The interpreter's lock is free while a kernel is launched (a launch into a full queue
+    waits, and a host callback in that queue may need the lock).  With a switch interval of
+    minutes another thread runs only where the lock is given up."""
+    call = calls()[name]
+    call()
+    torch.cuda.synchronize()
+    ran = []
+    ready, go = threading.Event(), threading.Lock()
+    go.acquire()
+
+    def other():
+        ready.set()
+        go.acquire()  # waits without the interpreter's lock, then for it
+        ran.append(1)
+
+    thread = threading.Thread(target=other)
+    thread.start()
+    ready.wait()
+    time.sleep(0.05)
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(300.0)
+    try:
+        go.release()
+        for n in range(20000):
+            call()
+            if ran:
+                break
+        seen = bool(ran)
+    finally:
+        sys.setswitchinterval(interval)
+    thread.join(30)
+    torch.cuda.synchronize()
+    assert seen, "the other thread had not run after %d calls" % (n + 1)
