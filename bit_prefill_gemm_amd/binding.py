@@ -605,7 +605,9 @@ def w4a4_gemm_rot(codes, scales, act_bits: int, rotation: int, w: Weights, y=Non
 #
 # These four come between the products of one token, where host time counts:
 # their tensor checks, output allocation and C ABI call are compiled
-# (csrc/native.cpp).
+# (csrc/native.cpp).  An output that is given must not share memory with an
+# input or another output (ValueError), but for the residual stream updated
+# where it is.
 
 _native_mod = None
 

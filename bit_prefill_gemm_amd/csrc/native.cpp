@@ -11,8 +11,8 @@
 //
 // The C ABI sees only pointers and sizes, so a tensor of the wrong shape would
 // become an out-of-bounds device access: every tensor is checked here first,
-// shapes, types and layouts before devices, so that every shape error is
-// reported the same way with or without a GPU.
+// shapes, types, layouts and overlaps before devices, so that every such error
+// is reported the same way with or without a GPU.
 #include <torch/csrc/python_headers.h>
 
 #include <ATen/hip/EmptyTensor.h>
@@ -23,6 +23,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <string>
 
@@ -184,6 +185,70 @@ int64_t row_stride(const at::Tensor &t, int64_t unit)
     return t.size(0) > 1 ? t.stride(0) : (t.size(1) + unit - 1) / unit * unit;
 }
 
+// The bytes of a tensor: rows of `width` bytes that begin `stride` apart.
+struct Bytes {
+    int64_t at, rows, width, stride;
+};
+
+Bytes bytes_of(const at::Tensor &t)
+{
+    const int64_t size = (int64_t)t.element_size();
+    const int64_t at = (int64_t)reinterpret_cast<uintptr_t>(t.data_ptr());
+    if (t.numel() == 0 || at == 0)
+        return {0, 0, 0, 0};
+    if (t.is_contiguous() || t.dim() != 2)
+        return {at, 1, t.numel() * size, 0};
+    return {at, t.size(0), t.size(1) * size, t.stride(0) * size};
+}
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b < 0); } // b > 0
+
+// whether two tensors share a byte
+bool share(Bytes a, Bytes b)
+{
+    if (a.rows == 0 || b.rows == 0 || a.at + (a.rows - 1) * a.stride + a.width <= b.at ||
+        b.at + (b.rows - 1) * b.stride + b.width <= a.at)
+        return false;
+    if (a.rows == 1 && b.rows == 1)
+        return true;
+    if (a.rows == 1 || b.rows == 1 || a.stride == b.stride) {
+        // row i of a and row i + t of b do where -b.width < d + t stride < a.width
+        const int64_t stride = a.rows == 1 ? b.stride : a.stride, d = b.at - a.at;
+        const int64_t first = floor_div(-b.width - d, stride) + 1;
+        const int64_t last = -floor_div(d - a.width, stride) - 1;
+        return std::max(first, 1 - a.rows) <= std::min(last, b.rows - 1);
+    }
+    if (a.rows > b.rows)
+        std::swap(a, b);
+    for (int64_t i = 0; i < a.rows; i++)
+        if (share({a.at + i * a.stride, 1, a.width, 0}, b))
+            return true;
+    return false;
+}
+
+// Rows of two matrices of one shape and type in the same place.
+bool same_rows(const at::Tensor &a, const at::Tensor &b)
+{
+    return a.data_ptr() == b.data_ptr() && a.scalar_type() == b.scalar_type() &&
+           (a.size(0) <= 1 || a.stride(0) == b.stride(0));
+}
+
+struct Named {
+    const char *name;
+    const at::Tensor &tensor;
+};
+
+// An output given by the caller shares no memory with what the kernel reads or
+// writes beside it: one workgroup's store could come before another's load.
+void check_apart(const char *where, const char *name, const at::Tensor &out,
+                 std::initializer_list<Named> others)
+{
+    const Bytes bytes = bytes_of(out);
+    for (const Named &o : others)
+        if (o.tensor.defined() && share(bytes, bytes_of(o.tensor)))
+            fail(where, "%s overlaps %s", name, o.name);
+}
+
 void check_bits(const char *where, int64_t bits)
 {
     if (bits != 4 && bits != 8)
@@ -333,6 +398,18 @@ PyObject *rmsnorm_quantize_act(PyObject *, PyObject *const *a, Py_ssize_t)
         if (new_scales)
             scales = make({m, k / 32}, at::kFloat, x);
         check_codes(where, codes, scales, bits, m, k);
+        if (h.defined() && !new_h) {
+            check_apart(where, "h", h, {{"x", x}, {"the weight", weight}});
+            if (!same_rows(h, residual))
+                check_apart(where, "h", h, {{"the residual", residual}});
+        }
+        if (!new_codes)
+            check_apart(where, "codes", codes,
+                        {{"x", x}, {"the residual", residual}, {"h", h}, {"the weight", weight}});
+        if (!new_scales)
+            check_apart(where, "scales", scales,
+                        {{"x", x}, {"the residual", residual}, {"h", h}, {"the weight", weight},
+                         {"codes", codes}});
         const c10::Device device = one_device(where, {&x, &residual, &h, &weight, &codes, &scales});
         const c10::DeviceGuard guard(device);
         check_status(where, unlocked([&] {
@@ -375,6 +452,8 @@ PyObject *dequantize_act(PyObject *, PyObject *const *a, Py_ssize_t)
         check_type(where, "y", y, type);
         check_shape(where, "y", y, {m, k});
         check_rows(where, "y", y);
+        if (!made)
+            check_apart(where, "y", y, {{"codes", codes}, {"scales", scales}});
         const c10::Device device = one_device(where, {&codes, &scales, &y});
         const c10::DeviceGuard guard(device);
         check_status(where, unlocked([&] {
@@ -451,6 +530,13 @@ PyObject *w4a4_gemm_epilogue(PyObject *, PyObject *const *a, Py_ssize_t)
             ep.residual = address(residual);
             ep.ldr = row_stride(residual, 1);
         }
+        if (!made) {
+            check_apart(where, "y", y,
+                        {{"codes", codes}, {"scales", scales}, {"the weight image", image},
+                         {"the bias", bias}});
+            if (residual.defined() && !same_rows(y, residual))
+                check_apart(where, "y", y, {{"the residual", residual}});
+        }
         const c10::Device device = one_device(where, {&codes, &scales, &image, &y, &bias, &residual});
         const c10::DeviceGuard guard(device);
         check_status(where, unlocked([&] {
@@ -506,6 +592,11 @@ PyObject *moe_route_topk(PyObject *, PyObject *const *a, Py_ssize_t)
             throw Raised{};
         const int64_t groups = integer(a[4]), topk_groups = integer(a[5]);
         const float scale = (float)number(a[8]);
+        if (!new_ids)
+            check_apart(where, "expert_of", ids, {{"logits", logits}, {"the bias", bias}});
+        if (!new_weights)
+            check_apart(where, "weights", weights,
+                        {{"logits", logits}, {"the bias", bias}, {"expert_of", ids}});
         const c10::Device device = one_device(where, {&logits, &bias, &ids, &weights});
         const c10::DeviceGuard guard(device);
         check_status(where, unlocked([&] {

@@ -268,10 +268,11 @@ bpg_status w4a4_gemm_rot(const void *codes, const float *scales, int act_bits, i
  *             and ldh are then not used)
  *   h         device, [m][ldh] of residual_dt, receives the new stream, or
  *             NULL (not written); may be residual itself (ldh = ldr), must
- *             not overlap it or x otherwise
+ *             not overlap it otherwise, nor x
  *   weight    device, [k] of weight_dt, or NULL
  *   eps       finite and > 0 (else SHAPE)
- *   codes, scales  as quantize_act_rot writes them
+ *   codes, scales  as quantize_act_rot writes them; must not overlap one
+ *             another nor anything above
  * Limits: k <= 65536 and a multiple of 32 and of the span; ldx, ldr and ldh
  * multiples of 4; pointers 16-byte aligned.  NaN or Inf in a row gives
  * unspecified codes of that row.
@@ -293,7 +294,8 @@ bpg_status rmsnorm_quantize_act(const void *x, bpg_x_dtype x_dt, int64_t ldx,
  * rotated), rounded once to y's type.
  *
  *   codes, scales  device, as the quantizers write them for m rows of k values
- *   y              device, [m][ldy] of y_dt, ldy >= k, ldy % 4 == 0, overwritten
+ *   y              device, [m][ldy] of y_dt, ldy >= k, ldy % 4 == 0,
+ *                  overwritten; must not overlap codes or scales
  * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
  */
 bpg_status dequantize_act(const void *codes, const float *scales, int act_bits, int rotation,
@@ -333,7 +335,8 @@ bpg_status w4a4_gemm(const void *codes, const float *scales, int act_bits, int64
  *   rotation  0, 32, 64 or 128: the span of the codes; the image's stamp must
  *             record the same (else STAMP)
  *   ep        host, not NULL; read during the call only
- *   y         device, [m][ldy] of y_dt; fp32: ldy % 4 == 0, bf16: ldy % 8 == 0
+ *   y         device, [m][ldy] of y_dt; fp32: ldy % 4 == 0, bf16: ldy % 8 == 0;
+ *             must not overlap an input but the residual (see there)
  * Other arguments as w4a4_gemm.  The kernel is the one that
  * w4a4_gemm_epilogue_kernel_name names, for many shapes another one than
  * w4a4_gemm's, which adds the blocks' sums in another (fixed) order.
@@ -427,7 +430,8 @@ bpg_status w4a4_grouped_gemm_bf16(const void *codes, const float *scales, int ac
  *   logits_dev      device, [tokens][ldl] of dt, aligned to its type, ldl >= experts
  *   bias_dev        device, fp32 [experts], or NULL
  *   expert_of_dev   device, int32 [tokens*topk], as moe_route_sort takes it
- *   weights_dev     device, fp32 [tokens*topk], as moe_combine takes it
+ *   weights_dev     device, fp32 [tokens*topk], as moe_combine takes it; neither
+ *                   output may overlap the other or an input
  * Limits: experts <= 512, topk <= 64, groups <= 64 and a divisor of experts,
  * 1 <= topk_groups <= groups, topk <= topk_groups * (experts / groups),
  * BPG_GROUP_TOP2 with groups of two experts at least (where groups > 1),

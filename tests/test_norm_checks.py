@@ -4,6 +4,7 @@ host before any HIP call, and the binding checks every tensor first.  Pointers
 of the ABI tests are never dereferenced.
 """
 import ctypes
+import random
 
 import pytest
 import torch
@@ -243,3 +244,120 @@ def test_route_binding_checks():
     raises(f, logits, 2, expert_of=torch.zeros(8), match="expert_of has dtype")
     raises(f, logits, 2, weights=torch.zeros(9), match="weights has shape")
     raises(f, logits.bfloat16(), 2, bias=torch.zeros(16), match="cuda device")
+
+
+# ------------------------------------------------------------------ outputs over inputs
+
+def columns(rows, *widths, dtype=torch.float32):
+    """Matrices beside one another in the rows of one buffer."""
+    buf = torch.zeros(rows, sum(widths), dtype=dtype)
+    return buf.split(list(widths), 1)
+
+
+def test_norm_binding_refuses_overlaps():
+    f = bb.rmsnorm_quantize_act
+    x, r = torch.zeros(4, 128), torch.zeros(5, 128)
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4)
+    raises(f, x, residual=r[1:], h=r[:4], match="h overlaps the residual")
+    raises(f, x, residual=r[:4], h=r[1:], match="h overlaps the residual")
+    raises(f, x, residual=torch.zeros(4, 128), h=x, match="h overlaps x")
+    raises(f, x, residual=x, h=x, match="h overlaps x")
+    # the same memory as rows of another stride
+    raises(f, x, residual=r.view(-1)[:512].view(4, 128), h=r.view(-1).as_strided((4, 128), (132, 1)),
+           match="h overlaps the residual")
+    raises(f, x, scales=x.view(-1)[:16].view(4, 4), match="scales overlaps x")
+    raises(f, x, codes=x.view(torch.uint8).view(-1)[-256:].view(4, 64), match="codes overlaps x")
+    raises(f, x, codes=codes, scales=codes.view(torch.float32).view(-1)[:16].view(4, 4),
+           match="scales overlaps codes")
+    w = torch.zeros(128)
+    raises(f, x, weight=w, scales=w[112:].view(4, 4), match="scales overlaps the weight")
+    h = torch.zeros(4, 128)
+    raises(f, x, residual=r[:4], h=h, codes=h.view(torch.uint8).view(-1)[:256].view(4, 64), match="codes overlaps h")
+    # no overlap: the stream where it is, a row that ends where the next matrix begins, columns of one buffer
+    raises(f, x, residual=r[:4], h=r[:4], match="cuda device")
+    raises(f, x[:1], residual=r[:1], h=r[:1].as_strided((1, 128), (500, 1)), match="cuda device")
+    both = torch.zeros(8, 128)
+    raises(f, x, residual=both[:4], h=both[4:], match="cuda device")
+    a, b, c = columns(4, 128, 128, 128)
+    raises(f, a, residual=b, h=c, match="cuda device")
+    raises(f, a, residual=b, h=b, match="cuda device")
+    raises(f, a[:1], residual=b[1:2], h=c[:1], match="cuda device")
+    raises(f, c[1:2], residual=a[3:], h=b[:1], match="cuda device")
+    raises(f, x, residual=r[:4], h=h, codes=codes, scales=scales, match="cuda device")
+    # rows of another stride between those of the buffer's first columns
+    wide = torch.zeros(8, 256)
+    raises(f, x, residual=wide[:4, :128], h=wide.view(-1).as_strided((4, 128), (512, 1), 128), match="cuda device")
+    raises(f, x, residual=wide[:4, :128], h=wide.view(-1).as_strided((4, 128), (388, 1), 128), match="h overlaps the residual")
+
+
+def test_decode_binding_refuses_overlaps():
+    f = bb.dequantize_act
+    buf = torch.zeros(4 * 128 + 16)
+    scales = buf[:16].view(4, 4)
+    codes = torch.zeros(4, 64, dtype=torch.uint8)
+    raises(f, codes, scales, y=buf[4:516].view(4, 128), match="y overlaps scales")
+    raises(f, buf[-64:].view(torch.uint8).view(4, 64), scales, y=buf[16:].view(4, 128), match="y overlaps codes")
+    raises(f, codes, scales, y=buf[16:].view(4, 128), match="cuda device")
+
+
+def test_product_binding_refuses_overlaps():
+    f = bb.w4a4_gemm_epilogue
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4)
+    w = bb.Weights(desc(), torch.zeros(desc().bytes, dtype=torch.uint8))
+    buf = torch.zeros(5, 64)
+    raises(f, codes, scales, 4, w, residual=buf[1:], y=buf[:4], match="y overlaps the residual")
+    raises(f, codes, scales, 4, w, residual=buf[:4], y=buf[1:], match="y overlaps the residual")
+    # the same place, but as another type or with rows another stride apart
+    raises(f, codes, scales, 4, w, residual=buf[:4].view(torch.bfloat16)[:, :64], y=buf[:4],
+           match="y overlaps the residual")
+    raises(f, codes, scales, 4, w, residual=buf[:4], y=buf.view(-1).as_strided((4, 64), (68, 1)),
+           match="y overlaps the residual")
+    raises(f, codes, scales, 4, w, bias=buf[3], y=buf[:4], match="y overlaps the bias")
+    raises(f, codes, buf.view(-1)[:16].view(4, 4), 4, w, y=buf[:4], match="y overlaps scales")
+    raises(f, buf.view(torch.uint8).view(-1)[:256].view(4, 64), scales, 4, w, y=buf[:4], match="y overlaps codes")
+    raises(f, codes, scales, 4, w, y=w.image[:1024].view(torch.float32).view(4, 64), match="y overlaps the weight image")
+    raises(f, codes, scales, 4, w, residual=buf[:4], y=buf[:4], match="cuda device")
+    a, b = columns(4, 64, 64)
+    raises(f, codes, scales, 4, w, residual=a, y=b, bias=buf[4], match="cuda device")
+    raises(f, codes, scales, 4, w, residual=b, y=a, match="cuda device")
+    a, b = columns(4, 64, 64, dtype=torch.bfloat16)
+    raises(f, codes, scales, 4, w, residual=b, y=b, match="cuda device")
+
+
+def test_route_binding_refuses_overlaps():
+    f = bb.moe_route_topk
+    buf = torch.zeros(4, 16)
+    out = torch.zeros(16, dtype=torch.int32)
+    raises(f, buf, 2, weights=buf.view(-1)[:8], match="weights overlaps logits")
+    raises(f, buf, 2, expert_of=buf.view(torch.int32).view(-1)[56:], match="expert_of overlaps logits")
+    raises(f, buf, 2, expert_of=out[:8], weights=out.view(torch.float32)[7:15], match="weights overlaps expert_of")
+    b = torch.zeros(16)
+    raises(f, buf, 2, bias=b, weights=b[8:], match="weights overlaps the bias")
+    raises(f, buf, 2, bias=b, expert_of=out[:8], weights=out.view(torch.float32)[8:], match="cuda device")
+    # columns beside the logits
+    raises(f, buf[:1, :8], 2, weights=buf[0, 8:10], expert_of=out[:2], match="cuda device")
+
+
+def overlap_by_bytes(a, b):
+    def at(t):
+        return {t.data_ptr() + i * t.stride(0) * t.element_size() + j
+                for i in range(t.shape[0]) for j in range(t.shape[1] * t.element_size())}
+    return bool(at(a) & at(b))
+
+
+def test_overlaps_of_random_rows():
+    """Against the sets of bytes: both strides, both orders, one row and many."""
+    rng = random.Random(4)
+    buf = torch.zeros(4096)
+    met = set()
+    for _ in range(600):
+        m, k = rng.randint(1, 6), 32
+        strides = [rng.choice([32, 36, 64, 64, 68, 96, 128]) for _ in range(2)]
+        at = [4 * rng.randrange(0, 100) for _ in range(2)]
+        r, h = (buf.as_strided((m, k), (s, 1), o) for s, o in zip(strides, at))
+        same = at[0] == at[1] and (m == 1 or strides[0] == strides[1])
+        bad = not same and overlap_by_bytes(r, h)
+        met.add((bad, m == 1, strides[0] == strides[1]))
+        raises(bb.rmsnorm_quantize_act, torch.zeros(m, k), residual=r, h=h,
+               match="h overlaps the residual" if bad else "cuda device")
+    assert len(met) == 8
