@@ -15,7 +15,7 @@ import oracle
 from bit_prefill_gemm_amd import binding as bb
 from bit_prefill_gemm_amd import synth
 
-from gpu_util import act_to_device, fp32_bound, oracle_codes, torch_mod
+from gpu_util import act_to_device, assert_within_bound, fp32_bound, oracle_codes, rects, torch_mod
 
 pytestmark = pytest.mark.gpu
 
@@ -342,3 +342,52 @@ def test_far_values_leave_the_others_their_bits(torch, case, act):
     a = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=near, activation=act)
     b = bb.w4a4_gemm_epilogue(codes, scales, bits, W, bias=far, activation=act)
     assert torch.equal(a[:, ~at], b[:, ~at]) and not torch.equal(a[:, at], b[:, at])
+
+
+# two row tiles of the weight-stream kernel: 17 to 32 rows past the chunks' bound
+TWO_ROW_TILES = [(25, 416, 16416, 4, "weight-stream"), (32, 96, 16448, 8, "weight-stream"),
+                 (17, 1056, 16512, 8, "weight-stream")]
+
+
+@pytest.mark.parametrize("case", TWO_ROW_TILES, ids=["%dx%dx%d-%d" % c[:4] for c in TWO_ROW_TILES])
+def test_every_step_on_two_row_tiles(torch, case):
+    test_empty_epilogue_is_the_product(torch, case)
+    test_every_step_on_every_kernel(torch, case)
+
+
+@pytest.mark.parametrize("m,k,n,bits,kernel", [(1, 2048, 5120, 4, "weight-stream"), (25, 512, 16640, 8, "weight-stream"),
+                                               (40, 384, 96, 4, "weight-stream chunks"), (700, 128, 2144, 8, "strip 32x128"),
+                                               (500, 1024, 5120, 4, "wide 64x160"), (449, 4096, 5120, 8, "tiled 64x160"),
+                                               (1025, 128, 576, 4, "tiled 64x32")])
+@pytest.mark.parametrize("rotation", [64, 128])
+def test_longer_rotations(torch, rotation, m, k, n, bits, kernel):
+    """Codes and weights of the longer spans, through their own quantizer and packer: the product
+    within its fp32 bound of the 64-bit one of the same codes, and, with bias, activation and
+    residual, the bits that the same image and codes give where the stamp says 32."""
+    rng = np.random.default_rng(m + rotation)
+    blocks = synth.draw_q4_0(rng, (n,), k, 0.02 / math.sqrt(k), 0.6 / math.sqrt(k))
+    W = bb.rotate_pack_weights_rot(blocks, bb.SRC_Q4_0_ROTATED, n, k, rotation).to("cuda")
+    assert W.desc.rotation == rotation and bb.w4a4_gemm_epilogue_kernel_name(bits, m, W) == kernel
+    print("rotation", rotation, m, k, n, bits, flush=True)
+    x = torch.from_numpy(rng.standard_normal((m, k)).astype(np.float32)).cuda()
+    codes, scales = bb.quantize_act_rot(x, rotation, bits)
+    y = bb.w4a4_gemm_epilogue(codes, scales, bits, W, rotation=rotation)
+    if bb.w4a4_gemm_kernel_name(bits, m, W) == kernel:
+        assert torch.equal(y, bb.w4a4_gemm_rot(codes, scales, bits, rotation, W))
+    # the codes themselves: their values at scales of 1, not rotated back
+    q = host(bb.dequantize_act(codes, torch.ones_like(scales), bits, 0)).astype(np.int8)
+    w, dw = oracle.q4_0_decode(blocks, k)
+    for m0, m1, n0, n1 in rects(m, n, 96, 3, rotation):
+        ref = oracle.gemm_rect(q, host(scales), w, dw, m0, m1, n0, n1)
+        mag = oracle.gemm_abs_rect(q, host(scales), w, dw, m0, m1, n0, n1)
+        assert_within_bound(host(y)[m0:m1, n0:n1], ref, mag, k, "rotation %d" % rotation)
+    bias = torch.from_numpy(rng.standard_normal(n).astype(np.float32)).cuda()
+    res = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32)).cuda().bfloat16()
+    steps = dict(bias=bias, activation="gelu_tanh", residual=res, dtype=torch.bfloat16)
+    got = bb.w4a4_gemm_epilogue(codes, scales, bits, W, rotation=rotation, **steps)
+    plain = bb.WeightsDesc.from_buffer_copy(W.desc)
+    plain.rotation = 32
+    assert torch.equal(got, bb.w4a4_gemm_epilogue(codes, scales, bits, bb.Weights(plain, W.image), **steps))
+    with pytest.raises(bb.BpgError) as e:
+        bb.w4a4_gemm_epilogue(codes, scales, bits, W, rotation=32)
+    assert e.value.status == 5
