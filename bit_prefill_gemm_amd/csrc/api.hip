@@ -50,7 +50,8 @@ constexpr int64_t kMaxSortEntries = (int64_t)1 << 20;
 // routing: a wave holds the choices and the group scores of a token one per lane
 constexpr int64_t kMaxTopk = 64;
 constexpr int64_t kMaxGroups = 64;
-// norm: a row stays in one workgroup's registers
+// norm: a row belongs to one workgroup (from 32769 values on a part of it is
+// spilled from its registers)
 constexpr int64_t kMaxNormK = (int64_t)1 << 16;
 
 bpg_status launch_status(hipError_t e) { return e == hipSuccess ? BPG_OK : BPG_ERR_LAUNCH; }

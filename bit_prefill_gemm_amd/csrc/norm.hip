@@ -20,15 +20,23 @@
 // The fp64 sum is a conversion and an FMA per value.
 //
 // A row belongs to a workgroup, a 32-block to a quad of lanes (lane t holds
-// elements 8t..8t+7: one 16-byte load per 8 bf16 values), R blocks per quad in
-// registers between the sum and the codes.  What bounds it is memory (two
-// reads, a write and the codes) as long as loads are always in flight, so the
-// grid holds just the workgroups that fit the chip; each walks several rows
-// and issues the next row's loads before it reduces the current one.
-// Measured (bf16 rows with residual): 8192 x 5120 with 8-bit codes and H128
-// 66 us for 299 MB (4.5 TB/s; a large copy reaches 5.07), 101 us before with a
-// workgroup per row, 8-byte loads and a check per value; 512 x 5120 7.0 us
-// (354 vector instructions per wave and row), one row 3.7 us (a launch is 1.9).
+// elements 8t..8t+7: one 16-byte load per 8 bf16 values), R blocks per quad
+// between the sum and the codes: in registers up to R = 4 (32768 values), while
+// R = 8 spills 96 to 144 of them.  What bounds it is memory (two reads, a write
+// and the codes) as long as loads are always in flight, so the grid holds about
+// the workgroups that fit the chip (see launch_norm_rounds); each walks several
+// rows and, up to R = 2 (bf16 x and stream 3), issues the next row's loads
+// before it reduces the current one.  From R = 4 on a block's loads also wait
+// for the store of h before them, as h may be the residual.  A row of fewer
+// than 16 blocks leaves lanes of its wave idle.
+// Measured in graph replays (8-bit codes): 8192 x 5120 with H128, bf16 x and
+// stream, 66 us for 299 MB (4.5 TB/s; a large copy reaches 5.07), 101 us before
+// with a workgroup per row, 8-byte loads and a check per value; bf16 x into an
+// fp32 stream 106 us (4.4 TB/s), both fp32 117 (4.7), fp32 without a residual
+// 68 (3.2).  Long bf16 rows: 2000 x 28672 115 us (3.6 TB/s), 500 x 65536 122
+// (1.9); narrow ones: 100000 x 256 49 us (3.7), 100000 x 64 43 (1.1).  With
+// 4-bit codes 512 x 5120 takes 7.0 us (354 vector instructions per wave and
+// row), one row 3.7 us (a launch is 1.9).
 //
 // This file must be compiled with -ffp-contract=off (see quantize.hip).
 #include <hip/hip_runtime.h>
@@ -255,8 +263,10 @@ __global__ __launch_bounds__(1024) void norm_quantize_kernel(NormProblem p)
     if (waves > 1 && tid < 32)
         partial[tid >> 4][tid & 15] = 0.0; // the waves that do not exist
 
-    // The lane's part of block qd + r quads; quads past the row's end repeat
-    // its last span's place in it and store nothing.
+    // The lane's part of block qd + r quads; quads past the row's end read its
+    // first block instead and store nothing.  (Where h is the residual another
+    // wave may store that block meanwhile; these quads' values reach nothing
+    // but the wave's vote in quantize_lanes, whose two ways give the same codes.)
     int at[R];
     bool live[R];
 #pragma unroll
@@ -449,8 +459,10 @@ template <typename Tx, typename Tr, int BITS>
 hipError_t launch_norm_rounds(const NormProblem &p, hipStream_t stream)
 {
     const int nb = (int)(p.k / 32);
-    // per_cu: waves that a CU holds of the kernel (by its registers); the grid
-    // is no more workgroups than fit at once
+    // per_cu: waves that a CU holds of the kernel by its registers.  The grid is
+    // no more workgroups than fit at once; only of R = 2 with an fp32 x or stream
+    // (100 to 104 registers: 16 waves, not the 20 that bf16 with 89 has) it may
+    // be more, four where three fit at K = 5120: the rest waits for a place.
     auto launch = [&](auto kernel, int rounds, int per_cu) {
         const int waves = (nb + 16 * rounds - 1) / (16 * rounds);
         const int64_t most = (int64_t)kCUs * (per_cu / waves > 0 ? per_cu / waves : 1);
@@ -459,7 +471,8 @@ hipError_t launch_norm_rounds(const NormProblem &p, hipStream_t stream)
     };
     // One block per quad while every row has a workgroup at once (the shortest
     // chain from the loads to the stores); with more rows than that, two (half
-    // the reductions and barriers a row), unless more lanes would idle.
+    // the reductions and barriers a row), unless more lanes would idle.  A row of
+    // fewer than 16 blocks takes a wave all the same.
     const int w1 = (nb + 15) / 16, w2 = (nb + 31) / 32;
     const bool once = w1 <= 16 && p.m <= (int64_t)kCUs * (32 / w1);
     if (w1 <= 16 && (once || 2 * w2 > w1))

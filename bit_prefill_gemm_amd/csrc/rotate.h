@@ -1,9 +1,12 @@
-// rotate.h -- the 32-value blocks of activations in registers, shared by the
-// kernels that rotate, quantize or decode them (gfx950).  Internal; included
-// by the kernel sources only, which must be compiled with -ffp-contract=off.
+// rotate.h -- the 32-value blocks of activations in registers (gfx950).
+// Internal; included by the kernel sources only, which must be compiled with
+// -ffp-contract=off.
 //
-// A quad of lanes owns a block: lane t holds elements {4t..4t+3} and
-// {16+4t..16+4t+3}.
+// A quad of lanes owns a block.  The exchanges across lanes (quad_swap,
+// cross_stage, cross_quad_stage) are shared by the quantizers (quantize.hip)
+// and the norm and the decoding (norm.hip).  load8, rotate_p and quantize_block
+// are the quantizers' alone: there lane t holds elements {4t..4t+3} and
+// {16+4t..16+4t+3}, while norm.hip's lanes hold 8t..8t+7.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -24,7 +24,9 @@
 // experts' scores are then computed in fp64 (all of them for softmax weights
 // that are not renormalised).  Measured (in a graph; an empty launch is 1.9
 // us): 1 x 128, top-8 softmax 2.6 us; 512 x 128 3.1; 4099 x 256 bf16 in 8
-// groups, sigmoid and bias 7.9; 16384 x 512, top-10 softmax and bias 20.2, of
+// groups, sigmoid and bias 7.9 (675 vector and 345 scalar instructions a token,
+// most of the scalar ones from the merge of a group's lanes, whose distance is a
+// run-time value); 16384 x 512, top-10 softmax and bias 20.2, of
 // which 690 vector instructions a token are 18.7.  With every score and key in
 // fp64 and shuffles for the reductions these were 6.5, 7.3, 31.6 and 53.4 us.
 #include <hip/hip_runtime.h>

@@ -206,7 +206,9 @@ strip_kernel(GemmProblem p, int tiles_m, int parts_m, int row_group)
     // the residual values of the lane's results: loaded behind the first
     // stage's operands, so that nothing waits for them at the end (4-bit codes;
     // with 8-bit ones the 16 registers would cost the fourth workgroup of a CU,
-    // 271 against 260 us at 1024 x 5120 x 17408, and they are loaded at the end)
+    // 271 against 260 us at 1024 x 5120 x 17408, and they are loaded at the end:
+    // there a bf16 residual, 36 MB, makes 274 us 280 and an fp32 one 283, where
+    // 4-bit codes go from 274 to 282 and 284)
     uint32_t res[EP ? 16 : 1];
     auto load_residual = [&] {
         const int64_t r0 = row0 * p.ep.ldr + col0 + min(wave, last_tile) * 32 + c;
