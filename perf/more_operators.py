@@ -4,8 +4,8 @@ Four kinds of pass, each what a prompt or a decode step does:
 
 * ``quantize``: rows of activations (or whole weights) to e4m3 codes with a scale per block of 128 (128 x 128);
 * ``product``: the product of such codes, every block of 128 under its own scales;
-* ``gated``: both projections of a gated feed-forward block, activation and product, as values or as the codes
-  that the down projection reads;
+* ``gated``: both projections of a gated feed-forward block, activation and product, as values, or as the codes
+  that the down projection reads, with that projection;
 * ``logprobs``: log probabilities of given tokens, the entropy of each row of logits and its top alternatives.
 
 ``run`` computes them in elementary torch operations where ``own`` is false, and through the library's entry
@@ -37,12 +37,12 @@ def listed():
         dict(name="product_attn512", op="product", tokens=512, k=5120, n=5120, out="bf16"),
         # the up projection of several users' prompts batched
         dict(name="product_batch8192", op="product", tokens=8192, k=5120, n=17408, out="bf16"),
-        # the gate, the up projection and the codes for the down projection, for one new token
-        dict(name="gated_token", op="gated", tokens=1, k=5120, f=17408, act="silu", out="fp8"),
+        # a whole feed-forward block for one new token: gate and up projection to codes, and the down projection of those
+        dict(name="gated_token", op="gated", tokens=1, k=5120, f=17408, act="silu", out="down"),
         # odd: neither rows nor columns fill tiles, K ends inside a block; fp32 values
         dict(name="gated_odd", op="gated", tokens=77, k=2080, f=1061, act="gelu_tanh", out="fp32"),
         # the same block over a 1024-token micro-batch
-        dict(name="gated_long1024", op="gated", tokens=1024, k=5120, f=17408, act="silu", out="fp8"),
+        dict(name="gated_long1024", op="gated", tokens=1024, k=5120, f=17408, act="silu", out="down"),
         # the answer of one decode step with twenty alternatives
         dict(name="logprobs_token", op="logprobs", tokens=1, vocab=131072, dtype="fp32", topk=20, masked=False),
         # odd: a prompt's tokens scored (perplexity) with five alternatives, part of the vocabulary masked
@@ -73,8 +73,8 @@ def draw(rng):
         tokens = _log(rng, 1, 1024)
         k = 32 * max(1, _log(rng, 32, 17408) // 32)
         f = _log(rng, 32, min(17408, 1024 * 5120 * 17408 // (tokens * k)))
-        out = rng.choice(["bf16", "fp32", "fp8"])
-        return dict(op=op, tokens=tokens, k=k, f=32 * (f // 32) if out == "fp8" else f, act=rng.choice(["silu", "gelu", "gelu_tanh", "relu"]), out=out)
+        out = rng.choice(["bf16", "fp32", "down"])
+        return dict(op=op, tokens=tokens, k=k, f=32 * (f // 32) if out == "down" else f, act=rng.choice(["silu", "gelu", "gelu_tanh", "relu"]), out=out)
     tokens = _log(rng, 1, 4096)
     vocab = _log(rng, 32, min(262144, 4096 * 131072 // tokens))
     dtype = rng.choice(["bf16", "fp32"]) if tokens * vocab < 128 << 20 else "bf16"
@@ -131,10 +131,11 @@ def prepare(case, seed):
     elif case["op"] == "product":
         state["codes"], state["scales"] = _codes(_outliers(g, _normal(g, case["tokens"], case["k"]), 30.0), 1)
         state["w"] = _weights(g, case["n"], case["k"])
-    elif case["op"] == "gated":
-        state["codes"], state["scales"] = _codes(_outliers(g, _normal(g, case["tokens"], case["k"]), 30.0), 1)
+    elif case["op"] == "gated":  # behind a norm, whose weights damp the largest channels
+        state["codes"], state["scales"] = _codes(_outliers(g, _normal(g, case["tokens"], case["k"]), 8.0), 1)
         state["gate"] = _weights(g, case["f"], case["k"])
         state["up"] = _weights(g, case["f"], case["k"])
+        state["down"] = _weights(g, case["k"], case["f"]) if case["out"] == "down" else None
     else:
         t, v = case["tokens"], case["vocab"]
         logits = _normal(g, t, v)
@@ -218,13 +219,16 @@ def _gated(s):
     if own:
         from bit_prefill_gemm_amd import binding as bpg
         gate, up = bpg.Fp8Weights(*s["gate"]), bpg.Fp8Weights(*s["up"])
-        if s["out"] == "fp8":
+        if s["out"] == "down":
             codes, scales = bpg.fp8_gemm_gated_quantize(s["codes"], s["scales"], gate, up, activation=s["act"])
-            return {"codes": codes, "scales": scales}
+            return bpg.fp8_gemm(codes, scales, bpg.Fp8Weights(*s["down"]), dtype=torch.bfloat16)
         return bpg.fp8_gemm_gated(s["codes"], s["scales"], gate, up, activation=s["act"], dtype=FLOATS[s["out"]])
     a = _values(s["codes"], s["scales"], 1)
     h = _activation(torch.mm(a, _values(*s["gate"], BLOCK).t()), s["act"]) * torch.mm(a, _values(*s["up"], BLOCK).t())
-    return _quantized(h, 1) if s["out"] == "fp8" else h.to(FLOATS[s["out"]])
+    if s["out"] != "down":
+        return h.to(FLOATS[s["out"]])
+    q = _quantized(h, 1)
+    return torch.mm(_values(q["codes"], q["scales"], 1), _values(*s["down"], BLOCK).t()).to(torch.bfloat16)
 
 
 def _logprobs(s):
@@ -253,7 +257,7 @@ def _logprobs(s):
 # ---------------------------------------------------------------- what a pass cannot do without
 
 def work(case):
-    size = {"bf16": 2, "fp32": 4, "fp8": 1}
+    size = {"bf16": 2, "fp32": 4}
     if case["op"] == "quantize":
         m, k, rows = case["rows"], case["width"], case["block_rows"]
         return {"bytes": m * k * (size[case["dtype"]] + 1) + 4 * ((m + rows - 1) // rows) * _blocks(k), "flops": 4 * m * k}
@@ -262,8 +266,9 @@ def work(case):
         return {"bytes": (m + n) * k + 4 * (m + _blocks(n)) * _blocks(k) + m * n * size[case["out"]], "flops": 2 * m * n * k}
     if case["op"] == "gated":
         m, k, f = case["tokens"], case["k"], case["f"]
-        out = m * f * size[case["out"]] + 4 * m * _blocks(f) * (case["out"] == "fp8")
-        return {"bytes": (m + 2 * f) * k + 4 * (m + 2 * _blocks(f)) * _blocks(k) + out, "flops": 4 * m * f * k}
+        down = case["out"] == "down"
+        out = k * f + 4 * _blocks(k) * _blocks(f) + 2 * m * k if down else m * f * size[case["out"]]
+        return {"bytes": (m + 2 * f) * k + 4 * (m + 2 * _blocks(f)) * _blocks(k) + out, "flops": (6 if down else 4) * m * f * k}
     t, v = case["tokens"], case["vocab"]
     return {"bytes": t * v * size[case["dtype"]] + t * 16 + t * case["topk"] * 8, "flops": 6 * t * v}
 
@@ -303,7 +308,7 @@ def _exact_mm(codes, scales, w):
     column = torch.arange(b.shape[0], device=a.device) // BLOCK
     for j in range(scales.shape[1]):
         at = slice(j * BLOCK, (j + 1) * BLOCK)
-        left = a[:, at] * scales[:, j].double()[:, None]
+        left = a[:, at] * scales[:, j].double()[:, None]  # scales: fp32, or 64 bits
         right = b[:, at].double() * e[:, j].double()[column][:, None]
         y.addmm_(left, right.t())
     return y
@@ -323,7 +328,11 @@ def _exact_gated(s):
         g = g * torch.special.ndtr(g)
     else:
         g = g * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))
-    return _exact_codes(g * u, 1) if s["out"] == "fp8" else g * u
+    h = g * u
+    if s["out"] != "down":
+        return h
+    q = _exact_codes(h, 1)  # the codes are a part of the definition
+    return _exact_mm(q["codes"].to(E4M3), q["scales"], s["down"])
 
 
 def _exact_logprobs(s):
