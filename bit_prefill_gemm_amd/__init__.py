@@ -14,7 +14,10 @@ Public names mirror the C ABI in include/bpg.h:
     and rotations over 64 or 128 values: rotate_pack_weights_rot,
     quantize_act_rot, w4a4_gemm_rot; and bf16 output: w4a4_gemm_bf16,
     w4a4_grouped_gemm_bf16; and what sits between the products of a block:
-    rmsnorm_quantize_act, dequantize_act, w4a4_gemm_epilogue, moe_route_topk
+    rmsnorm_quantize_act, dequantize_act, w4a4_gemm_epilogue, moe_route_topk;
+    and an 8-bit floating-point route with a scale per block of 128:
+    quantize_fp8, quantize_weights_fp8, fp8_gemm, fp8_gemm_gated,
+    fp8_gemm_gated_quantize; and what a head's logits say: token_logprobs
 
 The binding is loaded lazily so that ``bit_prefill_gemm_amd.synth`` (input
 generators) imports without the HIP library.
@@ -28,6 +31,8 @@ _BINDING_NAMES = {
     "rotate_pack_weights_rot", "quantize_act_rot", "w4a4_gemm_rot",
     "w4a4_gemm_bf16", "w4a4_grouped_gemm_bf16",
     "rmsnorm_quantize_act", "dequantize_act", "w4a4_gemm_epilogue", "moe_route_topk",
+    "Fp8Weights", "quantize_fp8", "quantize_weights_fp8", "fp8_gemm", "fp8_gemm_gated",
+    "fp8_gemm_gated_quantize", "token_logprobs",
 }
 
 

@@ -30,7 +30,9 @@ ENTRY_POINTS = ("bpg_status_str", "rotate_pack_weights_bytes", "rotate_pack_weig
                 "rotate_pack_weights_rot", "quantize_act_rot", "w4a4_gemm_rot",
                 "w4a4_gemm_bf16", "w4a4_grouped_gemm_bf16", "w4a4_gemm_kernel_name",
                 "w4a4_grouped_gemm_kernel_name", "rmsnorm_quantize_act", "dequantize_act",
-                "w4a4_gemm_epilogue", "w4a4_gemm_epilogue_kernel_name", "moe_route_topk")
+                "w4a4_gemm_epilogue", "w4a4_gemm_epilogue_kernel_name", "moe_route_topk",
+                "quantize_fp8", "fp8_gemm", "fp8_gemm_gated", "fp8_gemm_gated_quantize_bytes",
+                "fp8_gemm_gated_quantize", "token_logprobs_bytes", "token_logprobs")
 
 
 class WeightsDesc(ctypes.Structure):
@@ -129,6 +131,24 @@ def _lib_handle():
     lib.moe_route_topk.restype = _int
     lib.moe_route_topk.argtypes = [_vp, _int, _i64, _i64, _i64, _int, _vp, _i64, _i64, _int, _i64,
                                    _int, _f32, _vp, _vp, _vp]
+    _size = ctypes.c_size_t
+    lib.quantize_fp8.restype = _int
+    lib.quantize_fp8.argtypes = [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp]
+    lib.fp8_gemm.restype = _int
+    lib.fp8_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64, _vp]
+    lib.fp8_gemm_gated.restype = _int
+    lib.fp8_gemm_gated.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _int,
+                                   _i64, _vp]
+    lib.fp8_gemm_gated_quantize_bytes.restype = _size
+    lib.fp8_gemm_gated_quantize_bytes.argtypes = [_i64, _i64, _i64]
+    lib.fp8_gemm_gated_quantize.restype = _int
+    lib.fp8_gemm_gated_quantize.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int,
+                                            _vp, _vp, _vp, _size, _vp]
+    lib.token_logprobs_bytes.restype = _size
+    lib.token_logprobs_bytes.argtypes = [_i64, _i64, _i64]
+    lib.token_logprobs.restype = _int
+    lib.token_logprobs.argtypes = [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp, _vp,
+                                   _vp, _size, _vp]
     _lib = lib
     return lib
 
@@ -688,3 +708,93 @@ def moe_route_topk(logits, topk: int, score: str = "softmax", bias=None, groups:
                    topk_groups, group_score, renormalize, scale, expert_of, weights)
     return call(logits, topk, score, bias, groups, topk_groups, group_score, renormalize, scale,
                 expert_of, weights)
+
+
+# ------------------------------------------------------------------ 8-bit floating point
+#
+# Checked and called by the same compiled extension, with the same rule for
+# outputs that are given.
+
+class Fp8Weights:
+    """Weights of the 8-bit floating-point route: e4m3 codes [N, K] (torch.float8_e4m3fn) and
+    float32 scales [ceil(N / 128), ceil(K / 128)], one per block of 128 x 128 values; a code times
+    its scale is the weight.  A checkpoint's tensors of that form are taken as they are."""
+
+    def __init__(self, codes, scales):
+        self.codes = codes
+        self.scales = scales
+
+    @property
+    def n(self):
+        return self.codes.shape[0]
+
+    @property
+    def k(self):
+        return self.codes.shape[1]
+
+    def to(self, device):
+        return Fp8Weights(self.codes.to(device), self.scales.to(device))
+
+
+def quantize_fp8(x, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """x: 2-D cuda tensor (float32 or bfloat16, unit stride along K) to e4m3 codes [rows, K] and
+    float32 scales: [rows, ceil(K / 128)] (block_rows 1, activations) or
+    [ceil(rows / 128), ceil(K / 128)] (block_rows 128, weights).  Returns (codes, scales)."""
+    call = _native().quantize_fp8
+    if stream is not None:
+        return _on(stream, "quantize_fp8", x, call, x, block_rows, codes, scales)
+    return call(x, block_rows, codes, scales)
+
+
+def quantize_weights_fp8(w, stream=None) -> Fp8Weights:
+    """Weights [N, K] (a float32 or bfloat16 cuda tensor) in blocks of 128 x 128."""
+    return Fp8Weights(*quantize_fp8(w, 128, stream=stream))
+
+
+def fp8_gemm(codes, scales, w: Fp8Weights, y=None, dtype=None, stream=None):
+    """x . W^T from codes and scales of quantize_fp8: [M, N] of `dtype` (float32 unless y or dtype
+    says bfloat16, which is twice as fast; see include/bpg.h for how each is summed)."""
+    call = _native().fp8_gemm
+    if stream is not None:
+        return _on(stream, "fp8_gemm", codes, call, codes, scales, w.codes, w.scales, y, dtype)
+    return call(codes, scales, w.codes, w.scales, y, dtype)
+
+
+def fp8_gemm_gated(codes, scales, gate: Fp8Weights, up: Fp8Weights, activation: str = "silu",
+                   y=None, dtype=None, stream=None):
+    """act(x . gate^T) * (x . up^T): [M, F] of `dtype` (float32 unless y or dtype says bfloat16).
+    activation: none, relu, silu, gelu or gelu_tanh."""
+    call = _native().fp8_gemm_gated
+    if stream is not None:
+        return _on(stream, "fp8_gemm_gated", codes, call, codes, scales, gate.codes, gate.scales,
+                   up.codes, up.scales, activation, y, dtype)
+    return call(codes, scales, gate.codes, gate.scales, up.codes, up.scales, activation, y, dtype)
+
+
+def fp8_gemm_gated_quantize(codes, scales, gate: Fp8Weights, up: Fp8Weights,
+                            activation: str = "silu", out_codes=None, out_scales=None,
+                            stream=None):
+    """As fp8_gemm_gated, quantized for the down projection: (codes [M, F], scales
+    [M, ceil(F / 128)])."""
+    call = _native().fp8_gemm_gated_quantize
+    if stream is not None:
+        return _on(stream, "fp8_gemm_gated_quantize", codes, call, codes, scales, gate.codes,
+                   gate.scales, up.codes, up.scales, activation, out_codes, out_scales)
+    return call(codes, scales, gate.codes, gate.scales, up.codes, up.scales, activation, out_codes,
+                out_scales)
+
+
+# ------------------------------------------------------------------ what a head's logits say
+
+def token_logprobs(logits, tokens=None, topk: int = 0, logprobs=None, entropy=None, ids=None,
+                   top=None, stream=None):
+    """logits: cuda [rows, vocab] (float32 or bfloat16, unit stride along the vocabulary); tokens:
+    int32 or int64 [rows], a negative one for a position without a token.  Returns (logprobs,
+    entropy, ids, top): the log probability of each row's token (None without tokens, 0 without a
+    token), the entropy of each row, and the topk likeliest tokens (int32) with their log
+    probabilities, both [rows, topk]."""
+    call = _native().token_logprobs
+    if stream is not None:
+        return _on(stream, "token_logprobs", logits, call, logits, tokens, topk, logprobs, entropy,
+                   ids, top)
+    return call(logits, tokens, topk, logprobs, entropy, ids, top)

@@ -12,6 +12,7 @@
 
 #include "bpg.h"
 #include "between.h"
+#include "fp8.h"
 #include "internal.h"
 
 namespace {
@@ -838,6 +839,217 @@ bpg_status w4a4_gemm_blocksums(const void *codes, const float *scales, int act_b
     p.n1 = n1;
     p.expert = expert;
     return launch_status(bpg::launch_blocksums(p, static_cast<hipStream_t>(stream)));
+}
+
+} // extern "C"
+
+// ------------------------------------------------------------------ 8-bit floating point
+
+namespace {
+
+// rows of activations or weights: what a launch's grid and 32-bit row numbers hold
+constexpr int64_t kMaxFp8Rows = (int64_t)1 << 22;
+constexpr int64_t kMaxVocab = (int64_t)1 << 24;
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool act_ok(bpg_activation act) { return act >= BPG_ACT_NONE && act <= BPG_ACT_GELU_TANH; }
+
+// up_codes, up_scales: the second matrix (gated), else null
+bpg_status check_fp8(const void *codes, const float *scales, int64_t m, const void *w_codes,
+                     const float *w_scales, bool gated, const void *up_codes,
+                     const float *up_scales, int64_t n, int64_t k)
+{
+    if (m < 0 || m > kMaxFp8Rows || n < 1 || n > kMaxFp8Rows || k < 1 || k % 32 != 0 ||
+        k > kMaxGemmK)
+        return BPG_ERR_SHAPE;
+    if (!w_codes || !w_scales || (gated && (!up_codes || !up_scales)) ||
+        (m > 0 && (!codes || !scales)))
+        return BPG_ERR_NULL;
+    if (!aligned16(codes) || !aligned4(scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
+        (gated && (!aligned16(up_codes) || !aligned16(up_scales))))
+        return BPG_ERR_ALIGN;
+    return BPG_OK;
+}
+
+bpg::Fp8Problem fp8_problem(const void *codes, const float *scales, int64_t m, const void *w_codes,
+                            const float *w_scales, const void *up_codes, const float *up_scales,
+                            int64_t n, int64_t k)
+{
+    bpg::Fp8Problem p{};
+    p.codes = static_cast<const uint8_t *>(codes);
+    p.scales = scales;
+    p.w = static_cast<const uint8_t *>(w_codes);
+    p.w_scales = w_scales;
+    p.up = static_cast<const uint8_t *>(up_codes);
+    p.up_scales = up_scales;
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    return p;
+}
+
+bpg_status fp8_product(bpg::Fp8Problem &p, void *y, bpg_x_dtype y_dt, int64_t ldy, void *stream)
+{
+    if (!dtype_ok(y_dt))
+        return BPG_ERR_DTYPE;
+    if (ldy < p.n || ldy > ((int64_t)1 << 40))
+        return BPG_ERR_SHAPE;
+    if (p.m > 0 && !y)
+        return BPG_ERR_NULL;
+    if (!aligned_to(y, y_dt))
+        return BPG_ERR_ALIGN;
+    const bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    p.y = y;
+    p.ldy = ldy;
+    p.y_bf16 = y_dt == BPG_X_BF16;
+    p.exact = !p.y_bf16;
+    return launch_status(bpg::launch_fp8_gemm(p, static_cast<hipStream_t>(stream)));
+}
+
+} // namespace
+
+extern "C" {
+
+bpg_status quantize_fp8(const void *x, bpg_x_dtype dt, int64_t m, int64_t k, int64_t ldx,
+                        int64_t block_rows, void *codes, float *scales, void *stream)
+{
+    if (!dtype_ok(dt))
+        return BPG_ERR_DTYPE;
+    if ((block_rows != 1 && block_rows != bpg::kFp8Block) || m < 0 || k < 1 || k % 32 != 0 ||
+        k > kMaxGemmK || ldx < k || ldx > ((int64_t)1 << 40) || m >= ((int64_t)1 << 31) ||
+        (block_rows == 1 ? m * bpg::fp8_blocks(k) >= ((int64_t)1 << 31) : m > kMaxFp8Rows))
+        return BPG_ERR_SHAPE;
+    if (m > 0 && (!x || !codes || !scales))
+        return BPG_ERR_NULL;
+    if (!aligned16(x) || !aligned16(codes) || !aligned4(scales) || ldx % 4 != 0)
+        return BPG_ERR_ALIGN;
+    const bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    return launch_status(bpg::launch_fp8_quantize(x, dt == BPG_X_BF16, m, k, ldx,
+                                                  block_rows != 1, codes, scales,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const void *w_codes,
+                    const float *w_scales, int64_t n, int64_t k, void *y, bpg_x_dtype y_dt,
+                    int64_t ldy, void *stream)
+{
+    const bpg_status s =
+        check_fp8(codes, scales, m, w_codes, w_scales, false, nullptr, nullptr, n, k);
+    if (s != BPG_OK)
+        return s;
+    bpg::Fp8Problem p =
+        fp8_problem(codes, scales, m, w_codes, w_scales, nullptr, nullptr, n, k);
+    return fp8_product(p, y, y_dt, ldy, stream);
+}
+
+bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
+                          const void *gate_codes, const float *gate_scales, const void *up_codes,
+                          const float *up_scales, int64_t f, int64_t k, bpg_activation act, void *y,
+                          bpg_x_dtype y_dt, int64_t ldy, void *stream)
+{
+    if (!act_ok(act))
+        return BPG_ERR_DTYPE;
+    const bpg_status s =
+        check_fp8(codes, scales, m, gate_codes, gate_scales, true, up_codes, up_scales, f, k);
+    if (s != BPG_OK)
+        return s;
+    bpg::Fp8Problem p =
+        fp8_problem(codes, scales, m, gate_codes, gate_scales, up_codes, up_scales, f, k);
+    p.act = act;
+    return fp8_product(p, y, y_dt, ldy, stream);
+}
+
+size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k)
+{
+    if (m < 0 || m > kMaxFp8Rows || f < 1 || f > kMaxFp8Rows || k < 1)
+        return 0;
+    return bpg::fp8_gated_quantize_bytes(m, f, k);
+}
+
+bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64_t m,
+                                   const void *gate_codes, const float *gate_scales,
+                                   const void *up_codes, const float *up_scales, int64_t f,
+                                   int64_t k, bpg_activation act, void *out_codes,
+                                   float *out_scales, void *workspace, size_t workspace_bytes,
+                                   void *stream)
+{
+    if (!act_ok(act))
+        return BPG_ERR_DTYPE;
+    bpg_status s =
+        check_fp8(codes, scales, m, gate_codes, gate_scales, true, up_codes, up_scales, f, k);
+    if (s != BPG_OK)
+        return s;
+    if (f % 32 != 0 || m * bpg::fp8_blocks(f) >= ((int64_t)1 << 31))
+        return BPG_ERR_SHAPE;
+    const size_t need = m > 0 ? bpg::fp8_gated_quantize_bytes(m, f, k) : 0;
+    if (m > 0 && (!out_codes || !out_scales || (need > 0 && !workspace)))
+        return BPG_ERR_NULL;
+    if (!aligned16(out_codes) || !aligned4(out_scales) || !aligned16(workspace))
+        return BPG_ERR_ALIGN;
+    if (workspace_bytes < need)
+        return BPG_ERR_BUFFER;
+    s = check_device();
+    if (s != BPG_OK)
+        return s;
+    bpg::Fp8Problem p =
+        fp8_problem(codes, scales, m, gate_codes, gate_scales, up_codes, up_scales, f, k);
+    p.act = act;
+    return launch_status(bpg::launch_fp8_gated_quantize(p, static_cast<uint8_t *>(out_codes),
+                                                        out_scales, workspace,
+                                                        static_cast<hipStream_t>(stream)));
+}
+
+size_t token_logprobs_bytes(int64_t rows, int64_t vocab, int64_t topk)
+{
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || topk < 0 ||
+        topk > kMaxTopk)
+        return 0;
+    return bpg::logprobs_bytes(rows, vocab, (int)topk);
+}
+
+bpg_status token_logprobs(const void *logits, bpg_x_dtype dt, int64_t rows, int64_t vocab,
+                          int64_t ldl, const void *tokens, bpg_index_dtype token_dt, int64_t topk,
+                          float *logprobs, float *entropy, int32_t *ids, float *top,
+                          void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dt) || (tokens && token_dt != BPG_I32 && token_dt != BPG_I64))
+        return BPG_ERR_DTYPE;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || ldl < vocab ||
+        ldl > ((int64_t)1 << 40) || topk < 0 || topk > kMaxTopk || topk > vocab ||
+        rows * topk >= ((int64_t)1 << 31))
+        return BPG_ERR_SHAPE;
+    const size_t need = rows > 0 ? bpg::logprobs_bytes(rows, vocab, (int)topk) : 0;
+    if (rows > 0 && (!logits || (tokens && !logprobs) || (topk > 0 && (!ids || !top)) ||
+                     (need > 0 && !workspace)))
+        return BPG_ERR_NULL;
+    if (!aligned_to(logits, dt) || !aligned4(logprobs) || !aligned4(entropy) || !aligned4(ids) ||
+        !aligned4(top) || !aligned16(workspace) ||
+        (tokens && (reinterpret_cast<uintptr_t>(tokens) & (token_dt == BPG_I64 ? 7u : 3u)) != 0))
+        return BPG_ERR_ALIGN;
+    if (workspace_bytes < need)
+        return BPG_ERR_BUFFER;
+    const bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    bpg::LogprobsProblem p{};
+    p.logits = logits;
+    p.tokens = tokens;
+    p.logprobs = logprobs;
+    p.entropy = entropy;
+    p.ids = ids;
+    p.top = top;
+    p.rows = rows;
+    p.vocab = vocab;
+    p.ldl = ldl;
+    p.topk = (int)topk;
+    p.bf16 = dt == BPG_X_BF16;
+    p.wide = token_dt == BPG_I64;
+    return launch_status(bpg::launch_logprobs(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 } // extern "C"

@@ -1,0 +1,61 @@
+// fp8.h -- launchers of the 8-bit floating-point route (fp8_quantize.hip,
+// fp8_stream.hip) and of the log probabilities of tokens (logprobs.hip).  Not
+// part of the public interface (see include/bpg.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace bpg {
+
+constexpr int kFp8Block = 128; // values under one scale
+
+__host__ __device__ inline int64_t fp8_blocks(int64_t k)
+{
+    return (k + kFp8Block - 1) / kFp8Block;
+}
+
+// x [m][ldx] (fp32, or bf16 bits) to e4m3 codes [m][k] with a scale per block
+// of 1 x 128 values, or of 128 x 128 (square).
+hipError_t launch_fp8_quantize(const void *x, bool bf16, int64_t m, int64_t k, int64_t ldx,
+                               bool square, void *codes, float *scales, hipStream_t stream);
+
+// Products of e4m3 codes: y = x . w^T, or act(x . w^T) * (x . up^T) where `up`
+// is set.
+struct Fp8Problem {
+    const uint8_t *codes;  // activations [m][k]
+    const float *scales;   // [m][blocks of k]
+    const uint8_t *w;      // [n][k]
+    const float *w_scales; // [blocks of n][blocks of k]
+    const uint8_t *up;     // the second matrix of a gated product, or null
+    const float *up_scales;
+    int64_t m, n, k;
+    void *y;               // [m][ldy], bf16 bits when y_bf16, else fp32
+    int64_t ldy;
+    bool y_bf16;
+    bool exact;            // products added in fp32 (fp8_mma.h)
+    int act;               // bpg_activation (gated)
+};
+hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t stream);
+// The gated product (p.y, ldy, y_bf16 unused) as codes [m][n] and scales
+// [m][blocks of n]; workspace: fp8_gated_quantize_bytes(m, n, k) bytes.
+size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
+                                     void *workspace, hipStream_t stream);
+
+// Log probabilities, entropies and top alternatives of rows of logits.
+struct LogprobsProblem {
+    const void *logits;  // [rows][ldl], bf16 bits when bf16, else fp32
+    const void *tokens;  // [rows] int32 or int64 (wide), or null
+    float *logprobs;     // [rows], or null without tokens
+    float *entropy;      // [rows]
+    int32_t *ids;        // [rows][topk]
+    float *top;          // [rows][topk]
+    int64_t rows, vocab, ldl;
+    int topk;
+    bool bf16, wide;
+};
+size_t logprobs_bytes(int64_t rows, int64_t vocab, int topk);
+hipError_t launch_logprobs(const LogprobsProblem &p, void *workspace, hipStream_t stream);
+
+} // namespace bpg

@@ -1,6 +1,7 @@
 // native.cpp -- the Python entry points of the operators between the products
 // (rmsnorm_quantize_act, dequantize_act, w4a4_gemm_epilogue, moe_route_topk),
-// compiled: their tensor checks, output allocation and the call of the C ABI
+// of the 8-bit floating-point route (quantize_fp8, fp8_gemm, fp8_gemm_gated,
+// fp8_gemm_gated_quantize) and of token_logprobs, compiled: their tensor checks, output allocation and the call of the C ABI
 // (include/bpg.h).  Host code only; every step of the operators runs in
 // libbpg.so's kernels.
 //
@@ -118,6 +119,8 @@ std::string type_text(at::ScalarType t)
     case at::kDouble: return "torch.float64";
     case at::kInt: return "torch.int32";
     case at::kByte: return "torch.uint8";
+    case at::kLong: return "torch.int64";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
     }
 }
@@ -613,6 +616,290 @@ PyObject *moe_route_topk(PyObject *, PyObject *const *a, Py_ssize_t)
     });
 }
 
+// The type of an output: `dtype`, else that of a given y, else `otherwise`.
+at::ScalarType output_type(const char *where, PyObject *dtype, const at::Tensor &y,
+                           at::ScalarType otherwise)
+{
+    if (dtype != Py_None && !THPDtype_Check(dtype))
+        fail(where, "dtype must be a torch.dtype");
+    if (dtype == Py_None)
+        return y.defined() ? y.scalar_type() : otherwise;
+    return reinterpret_cast<THPDtype *>(dtype)->scalar_type;
+}
+
+// blocks of 128 values
+int64_t blocks_of(int64_t k) { return (k + 127) / 128; }
+
+// e4m3 codes [rows][k], k a positive multiple of 32, under fp32 scales
+// [scale_rows][ceil(k / 128)]
+void check_fp8_codes(const char *where, const char *name, const at::Tensor &codes,
+                     const char *scales_name, const at::Tensor &scales, int64_t rows, int64_t k,
+                     int64_t scale_rows)
+{
+    check_type(where, name, codes, at::kFloat8_e4m3fn);
+    if (k <= 0 || k % 32 != 0)
+        fail(where, "K = %lld is not a positive multiple of 32", (long long)k);
+    check_shape(where, name, codes, {rows, k});
+    check_contiguous(where, name, codes);
+    check_type(where, scales_name, scales, at::kFloat);
+    check_shape(where, scales_name, scales, {scale_rows, blocks_of(k)});
+    check_contiguous(where, scales_name, scales);
+}
+
+// (x, block_rows, codes, scales)
+PyObject *quantize_fp8(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    return guarded([&]() -> PyObject * {
+        const char *where = "quantize_fp8";
+        at::AutoDispatchBelowADInplaceOrView below;
+        const at::Tensor x = matrix(where, "x", a[0]);
+        const bpg_x_dtype dt = float_code(where, "x", x.scalar_type());
+        check_rows(where, "x", x);
+        const int64_t m = x.size(0), k = x.size(1), block_rows = integer(a[1]);
+        if (block_rows != 1 && block_rows != 128)
+            fail(where, "block_rows must be 1 or 128, got %lld", (long long)block_rows);
+        if (k <= 0 || k % 32 != 0)
+            fail(where, "K = %lld is not a positive multiple of 32", (long long)k);
+        at::Tensor codes = optional_tensor(where, "codes", a[2]);
+        at::Tensor scales = optional_tensor(where, "scales", a[3]);
+        const bool new_codes = !codes.defined(), new_scales = !scales.defined();
+        const int64_t lines = block_rows == 1 ? m : blocks_of(m);
+        if (new_codes)
+            codes = make({m, k}, at::kFloat8_e4m3fn, x);
+        if (new_scales)
+            scales = make({lines, blocks_of(k)}, at::kFloat, x);
+        check_fp8_codes(where, "codes", codes, "scales", scales, m, k, lines);
+        if (!new_codes)
+            check_apart(where, "codes", codes, {{"x", x}});
+        if (!new_scales)
+            check_apart(where, "scales", scales, {{"x", x}, {"codes", codes}});
+        const c10::Device device = one_device(where, {&x, &codes, &scales});
+        const c10::DeviceGuard guard(device);
+        check_status(where, unlocked([&] {
+                         return ::quantize_fp8(address(x), dt, m, k, row_stride(x, 4), block_rows,
+                                               address(codes), address<float>(scales),
+                                               stream_of(device));
+                     }));
+        return tuple_of({new_codes ? wrap(codes) : (Py_INCREF(a[2]), a[2]),
+                         new_scales ? wrap(scales) : (Py_INCREF(a[3]), a[3])});
+    });
+}
+
+// Activations and one or two weight matrices of the products below.
+struct Fp8Operands {
+    at::Tensor codes, scales, w, w_scales, up, up_scales;
+    int64_t m, n, k;
+};
+
+Fp8Operands fp8_operands(const char *where, PyObject *const *a, bool gated)
+{
+    Fp8Operands o;
+    o.codes = matrix(where, "codes", a[0]);
+    o.scales = matrix(where, "scales", a[1]);
+    const char *name = gated ? "the gate's codes" : "the weights' codes";
+    const char *scales_name = gated ? "the gate's scales" : "the weights' scales";
+    o.w = matrix(where, name, a[2]);
+    o.w_scales = matrix(where, scales_name, a[3]);
+    o.m = o.codes.size(0);
+    o.n = o.w.size(0);
+    o.k = o.w.size(1);
+    if (o.n < 1)
+        fail(where, "the weights have no rows");
+    check_fp8_codes(where, name, o.w, scales_name, o.w_scales, o.n, o.k, blocks_of(o.n));
+    check_fp8_codes(where, "codes", o.codes, "scales", o.scales, o.m, o.k, o.m);
+    if (gated) {
+        o.up = matrix(where, "the up projection's codes", a[4]);
+        o.up_scales = matrix(where, "the up projection's scales", a[5]);
+        check_fp8_codes(where, "the up projection's codes", o.up, "the up projection's scales",
+                        o.up_scales, o.n, o.k, blocks_of(o.n));
+    }
+    return o;
+}
+
+void check_apart(const char *where, const char *name, const at::Tensor &out, const Fp8Operands &o)
+{
+    check_apart(where, name, out,
+                {{"codes", o.codes}, {"scales", o.scales}, {"the weights", o.w},
+                 {"the weights' scales", o.w_scales}, {"the up projection", o.up},
+                 {"the up projection's scales", o.up_scales}});
+}
+
+bpg_activation activation_of(const char *where, PyObject *o)
+{
+    static const char *const names[] = {"none", "relu", "silu", "gelu", "gelu_tanh"};
+    const std::string activation = text_of(o);
+    for (int act = 0; act < 5; act++)
+        if (activation == names[act])
+            return (bpg_activation)act;
+    fail(where, "activation must be one of none, relu, silu, gelu, gelu_tanh, got %s",
+         activation.c_str());
+}
+
+// (codes, scales, w, w_scales, y, dtype), or
+// (codes, scales, gate, gate_scales, up, up_scales, activation, y, dtype)
+PyObject *fp8_product(const char *where, PyObject *const *a, bool gated)
+{
+    return guarded([&]() -> PyObject * {
+        at::AutoDispatchBelowADInplaceOrView below;
+        PyObject *given = a[gated ? 7 : 4];
+        const bpg_activation act = gated ? activation_of(where, a[6]) : BPG_ACT_NONE;
+        at::Tensor y = optional_tensor(where, "y", given);
+        const at::ScalarType type = output_type(where, a[gated ? 8 : 5], y, at::kFloat);
+        const bpg_x_dtype y_dt = float_code(where, "y", type);
+        const Fp8Operands o = fp8_operands(where, a, gated);
+        const bool made = !y.defined();
+        if (made)
+            y = make({o.m, o.n}, type, o.codes);
+        check_type(where, "y", y, type);
+        check_shape(where, "y", y, {o.m, o.n});
+        check_rows(where, "y", y);
+        if (!made)
+            check_apart(where, "y", y, o);
+        const c10::Device device =
+            one_device(where, {&o.codes, &o.scales, &o.w, &o.w_scales, &o.up, &o.up_scales, &y});
+        const c10::DeviceGuard guard(device);
+        check_status(where, unlocked([&] {
+                         const int64_t ldy = row_stride(y, 1);
+                         if (gated)
+                             return ::fp8_gemm_gated(
+                                 address(o.codes), address<float>(o.scales), o.m, address(o.w),
+                                 address<float>(o.w_scales), address(o.up),
+                                 address<float>(o.up_scales), o.n, o.k, act, address(y), y_dt, ldy,
+                                 stream_of(device));
+                         return ::fp8_gemm(address(o.codes), address<float>(o.scales), o.m,
+                                           address(o.w), address<float>(o.w_scales), o.n, o.k,
+                                           address(y), y_dt, ldy, stream_of(device));
+                     }));
+        return made ? wrap(y) : (Py_INCREF(given), given);
+    });
+}
+
+PyObject *fp8_gemm(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    return fp8_product("fp8_gemm", a, false);
+}
+
+PyObject *fp8_gemm_gated(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    return fp8_product("fp8_gemm_gated", a, true);
+}
+
+// (codes, scales, gate, gate_scales, up, up_scales, activation, out_codes, out_scales)
+PyObject *fp8_gemm_gated_quantize(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    return guarded([&]() -> PyObject * {
+        const char *where = "fp8_gemm_gated_quantize";
+        at::AutoDispatchBelowADInplaceOrView below;
+        const bpg_activation act = activation_of(where, a[6]);
+        const Fp8Operands o = fp8_operands(where, a, true);
+        if (o.n % 32 != 0)
+            fail(where, "F = %lld is not a multiple of 32", (long long)o.n);
+        at::Tensor codes = optional_tensor(where, "out_codes", a[7]);
+        at::Tensor scales = optional_tensor(where, "out_scales", a[8]);
+        const bool new_codes = !codes.defined(), new_scales = !scales.defined();
+        if (new_codes)
+            codes = make({o.m, o.n}, at::kFloat8_e4m3fn, o.codes);
+        if (new_scales)
+            scales = make({o.m, blocks_of(o.n)}, at::kFloat, o.codes);
+        check_fp8_codes(where, "out_codes", codes, "out_scales", scales, o.m, o.n, o.m);
+        if (!new_codes)
+            check_apart(where, "out_codes", codes, o);
+        if (!new_scales) {
+            check_apart(where, "out_scales", scales, o);
+            check_apart(where, "out_scales", scales, {{"out_codes", codes}});
+        }
+        const c10::Device device = one_device(
+            where, {&o.codes, &o.scales, &o.w, &o.w_scales, &o.up, &o.up_scales, &codes, &scales});
+        const c10::DeviceGuard guard(device);
+        // on the current stream, like the call: free for the next one behind it
+        const int64_t bytes = (int64_t)::fp8_gemm_gated_quantize_bytes(o.m, o.n, o.k);
+        const at::Tensor workspace = bytes ? make({bytes}, at::kByte, o.codes) : at::Tensor();
+        check_status(where, unlocked([&] {
+                         return ::fp8_gemm_gated_quantize(
+                             address(o.codes), address<float>(o.scales), o.m, address(o.w),
+                             address<float>(o.w_scales), address(o.up), address<float>(o.up_scales),
+                             o.n, o.k, act, address(codes), address<float>(scales),
+                             address(workspace), (size_t)bytes, stream_of(device));
+                     }));
+        return tuple_of({new_codes ? wrap(codes) : (Py_INCREF(a[7]), a[7]),
+                         new_scales ? wrap(scales) : (Py_INCREF(a[8]), a[8])});
+    });
+}
+
+// (logits, tokens, topk, logprobs, entropy, ids, top)
+PyObject *token_logprobs(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    return guarded([&]() -> PyObject * {
+        const char *where = "token_logprobs";
+        at::AutoDispatchBelowADInplaceOrView below;
+        const at::Tensor logits = matrix(where, "logits", a[0]);
+        const bpg_x_dtype dt = float_code(where, "logits", logits.scalar_type());
+        check_rows(where, "logits", logits);
+        const int64_t rows = logits.size(0), vocab = logits.size(1), topk = integer(a[2]);
+        if (vocab < 1)
+            fail(where, "the logits have no columns");
+        if (topk < 0 || topk > 64 || topk > vocab)
+            fail(where, "topk must be between 0 and the smaller of 64 and the %lld logits, got %lld",
+                 (long long)vocab, (long long)topk);
+        const at::Tensor tokens = optional_tensor(where, "tokens", a[1]);
+        at::Tensor logprobs = optional_tensor(where, "logprobs", a[3]);
+        at::Tensor entropy = optional_tensor(where, "entropy", a[4]);
+        at::Tensor ids = optional_tensor(where, "ids", a[5]);
+        at::Tensor top = optional_tensor(where, "top", a[6]);
+        if (tokens.defined()) {
+            if (tokens.scalar_type() != at::kInt && tokens.scalar_type() != at::kLong)
+                fail(where, "tokens has dtype %s, expected torch.int32 or torch.int64",
+                     type_text(tokens.scalar_type()).c_str());
+            check_shape(where, "tokens", tokens, {rows});
+            check_contiguous(where, "tokens", tokens);
+        } else if (logprobs.defined()) {
+            fail(where, "logprobs needs tokens");
+        }
+        auto output = [&](const char *name, at::Tensor &t, at::ScalarType type,
+                          at::IntArrayRef shape) {
+            if (!t.defined()) {
+                t = make(shape, type, logits);
+                return true;
+            }
+            check_type(where, name, t, type);
+            check_shape(where, name, t, shape);
+            check_contiguous(where, name, t);
+            check_apart(where, name, t, {{"logits", logits}, {"tokens", tokens}});
+            return false;
+        };
+        const bool new_logprobs =
+            tokens.defined() && output("logprobs", logprobs, at::kFloat, {rows});
+        const bool new_entropy = output("entropy", entropy, at::kFloat, {rows});
+        const bool new_ids = output("ids", ids, at::kInt, {rows, topk});
+        const bool new_top = output("top", top, at::kFloat, {rows, topk});
+        if (!new_entropy)
+            check_apart(where, "entropy", entropy, {{"logprobs", logprobs}});
+        if (!new_ids)
+            check_apart(where, "ids", ids, {{"logprobs", logprobs}, {"entropy", entropy}});
+        if (!new_top)
+            check_apart(where, "top", top,
+                        {{"logprobs", logprobs}, {"entropy", entropy}, {"ids", ids}});
+        const c10::Device device =
+            one_device(where, {&logits, &tokens, &logprobs, &entropy, &ids, &top});
+        const c10::DeviceGuard guard(device);
+        const int64_t bytes = (int64_t)::token_logprobs_bytes(rows, vocab, topk);
+        const at::Tensor workspace = bytes ? make({bytes}, at::kByte, logits) : at::Tensor();
+        const bool wide = tokens.defined() && tokens.scalar_type() == at::kLong;
+        check_status(where, unlocked([&] {
+                         return ::token_logprobs(
+                             address(logits), dt, rows, vocab, row_stride(logits, 1),
+                             address(tokens), wide ? BPG_I64 : BPG_I32, topk,
+                             address<float>(logprobs), address<float>(entropy),
+                             address<int32_t>(ids), address<float>(top), address(workspace),
+                             (size_t)bytes, stream_of(device));
+                     }));
+        auto given = [](PyObject *o) { return Py_INCREF(o), o; };
+        return tuple_of({new_logprobs ? wrap(logprobs) : given(a[3]),
+                         new_entropy ? wrap(entropy) : given(a[4]), new_ids ? wrap(ids) : given(a[5]),
+                         new_top ? wrap(top) : given(a[6])});
+    });
+}
+
 // (BpgError): the class of the library's own errors
 PyObject *set_error(PyObject *, PyObject *cls)
 {
@@ -643,6 +930,11 @@ PyMethodDef methods[] = {
     BPG_METHOD(dequantize_act, 6),
     BPG_METHOD(w4a4_gemm_epilogue, 11),
     BPG_METHOD(moe_route_topk, 11),
+    BPG_METHOD(quantize_fp8, 4),
+    BPG_METHOD(fp8_gemm, 6),
+    BPG_METHOD(fp8_gemm_gated, 9),
+    BPG_METHOD(fp8_gemm_gated_quantize, 9),
+    BPG_METHOD(token_logprobs, 7),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

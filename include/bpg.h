@@ -505,6 +505,100 @@ bpg_status moe_combine(const float *dn, int64_t lddn, int64_t rows, const int32_
                        float *y, int64_t ldy, void *stream);
 
 /*
+ * The 8-bit floating-point route: products of e4m3 codes (the finite OCP form:
+ * 1 sign, 4 exponent and 3 mantissa bits, largest value 448, no infinities)
+ * with an fp32 scale per block of 128.  The pages have no such route; it serves
+ * layers that are kept at 8 bits beside the 4-bit ones, heads among them.
+ * Activations have blocks of 1 x 128 values, weights of 128 x 128; the last
+ * block of a row or column holds what is left.  Codes are [rows][k] bytes,
+ * scales [rows][KB] (activations) or [NB][KB] (weights) fp32, KB = ceil(k/128),
+ * NB = ceil(n/128); a code c under scale d stands for c d.  K is a multiple of
+ * 32, at most 2^22; N is any positive number; x, codes and weight scales are
+ * 16-byte aligned, scales of activations 4-byte; y and its rows are aligned to
+ * y's type.  Neither output may overlap another or an input.
+ *
+ * quantize_fp8: the codes and scales of x, [m][ldx] of dt, ldx >= k,
+ * ldx % 4 == 0.  block_rows is 1 (activations) or 128 (weights).  Per block
+ * a = max |x|, d = a / 448, r = min(1 / d, FLT_MAX) (0 if d is 0), code =
+ * e4m3(x r): every step one fp32 rounding to nearest even, then one to e4m3.  A
+ * NaN makes its block's scale NaN, an infinity makes it infinite and its own
+ * code NaN.  m * KB < 2^31 (block_rows 1), m <= 2^22 (128).
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ */
+bpg_status quantize_fp8(const void *x, bpg_x_dtype dt, int64_t m, int64_t k, int64_t ldx,
+                        int64_t block_rows, void *codes, float *scales, void *stream);
+
+/*
+ * fp8_gemm: y = x . w^T, y[m][n] = sum over blocks b of
+ *   scales[m][b] w_scales[n / 128][b] (sum over k of block b of codes w_codes),
+ * the blocks' sums and their total in fp32, in a fixed order per shape; y is
+ * fp32 or bf16 (rounded once) [m][ldy], ldy >= n.  With y fp32 a block's
+ * products are added in fp32.  With y bf16 they are added by the 8-bit matrix
+ * instruction, which takes eight consecutive k at a time and may drop from each
+ * product what is below 2^-12 of the largest of the eight: an error of at most
+ * 2^-9 of the sum over the eights of their largest product, typically 2e-5 of y.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ */
+bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const void *w_codes,
+                    const float *w_scales, int64_t n, int64_t k, void *y, bpg_x_dtype y_dt,
+                    int64_t ldy, void *stream);
+
+/*
+ * fp8_gemm_gated: the gated feed-forward block's y = act(x . gate^T) *
+ * (x . up^T), both products as fp8_gemm's and one rounding at the store; gate
+ * and up are [f][k] codes with scales of their own, y [m][ldy], ldy >= f.
+ * fp8_gemm_gated_quantize: the same values in fp32, products as with y bf16,
+ * written as quantize_fp8 does: codes [m][f], scales [m][ceil(f/128)], f a
+ * multiple of 32: what fp8_gemm reads for the down projection.  workspace is
+ * device memory of fp8_gemm_gated_quantize_bytes(m, f, k) bytes at least (may be
+ * 0), 16-byte aligned, written and read by the call's kernels only: calls that
+ * can run at one time need one each.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
+ */
+bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
+                          const void *gate_codes, const float *gate_scales, const void *up_codes,
+                          const float *up_scales, int64_t f, int64_t k, bpg_activation act, void *y,
+                          bpg_x_dtype y_dt, int64_t ldy, void *stream);
+size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k);
+bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64_t m,
+                                   const void *gate_codes, const float *gate_scales,
+                                   const void *up_codes, const float *up_scales, int64_t f,
+                                   int64_t k, bpg_activation act, void *out_codes,
+                                   float *out_scales, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * token_logprobs: what a head's logits say of each position.  Per row l of
+ * `vocab` logits, p = softmax(l):
+ *   logprobs[r] = log p(tokens[r]); 0 where tokens[r] is negative (a position
+ *     that holds no token), NaN where it is vocab or more;
+ *   entropy[r] = -sum p log p (0 log 0 is 0);
+ *   ids[r][0..topk), top[r][0..topk): the topk likeliest tokens, the likeliest
+ *     first, equal logits by the lowest id, and their log probabilities.
+ * A logit of -inf has probability 0.  A row with a NaN or +inf, or of -inf only,
+ * has no distribution: its log probabilities and its entropy are NaN, and a NaN
+ * counts as -inf in the order of its ids.  Exponentials are fp32, sums beyond a
+ * thread's few fp64, results rounded once.
+ *   logits     device, [rows][ldl] of dt, aligned to its type, ldl >= vocab
+ *   tokens     device, int32 or int64 (token_dt) [rows], or NULL: no logprobs
+ *   logprobs   device, fp32 [rows] (may be NULL if tokens is)
+ *   entropy    device, fp32 [rows], or NULL
+ *   ids, top   device, int32 and fp32 [rows][topk] (may be NULL if topk is 0)
+ *   workspace  device memory of token_logprobs_bytes(rows, vocab, topk) bytes at
+ *              least (may be 0), 16-byte aligned; calls that can run at one time
+ *              need one each
+ * Neither output may overlap another or an input.
+ * Limits: 1 <= vocab <= 2^24, 0 <= topk <= min(vocab, 64), rows * topk < 2^31.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
+ */
+typedef enum { BPG_I32 = 0, BPG_I64 = 1 } bpg_index_dtype;
+size_t token_logprobs_bytes(int64_t rows, int64_t vocab, int64_t topk);
+bpg_status token_logprobs(const void *logits, bpg_x_dtype dt, int64_t rows, int64_t vocab,
+                          int64_t ldl, const void *tokens, bpg_index_dtype token_dt, int64_t topk,
+                          float *logprobs, float *entropy, int32_t *ids, float *top,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Parity and debug: the exact int32 block dot products
  * S[m][n][b] = sum_i q_a[m][32b+i] * (u[n][32b+i] - 8) ("509 tokens a second
  * of prompt: the Hadamard route ships", section "Why prompts are a

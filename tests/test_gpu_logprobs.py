@@ -1,0 +1,206 @@
+"""token_logprobs against the definition in 64 bits.
+
+With u = 2^-23 (an fp32 rounding, or the hardware's exponential) and d = l - m:
+every d carries one rounding and is scaled by log2 e with one more, so e^d is
+off by a factor 1 + 2 u |d| + 2 u, S by S u (2 E|d| + 4) with the fp32 sums of a
+thread's few values (E: the mean under p), T by u (2 E d^2 + 6 E|d|) S.  Then
+log S has u (2 E|d| + 4), log p(t) that and the roundings of d and of itself,
+and the entropy log S - T / S the two and its own.
+"""
+import math
+
+import pytest
+
+from bit_prefill_gemm_amd import binding as bb
+
+from gpu_util import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_mod()
+    if not t.cuda.is_available():
+        pytest.skip("no GPU")
+    return t
+
+
+def check(torch, logits, tokens, topk):
+    lp, ent, ids, top = bb.token_logprobs(logits, tokens, topk=topk)
+    l = logits.double()
+    rows, vocab = l.shape
+    m = l.amax(1, keepdim=True)
+    d = l - m
+    z = torch.logsumexp(d, 1, keepdim=True)
+    logp = d - z
+    p = logp.exp()
+    finite = torch.where(p > 0, d, 0.0)
+    e1, e2 = (p * finite.abs()).sum(1), (p * finite ** 2).sum(1)
+    tol_s = U * (2 * e1 + 4)
+    h = -(p * torch.where(p > 0, logp, 0.0)).sum(1)
+    tol_h = tol_s + U * (2 * e2 + 6 * e1 + e1 * (2 * e1 + 4)) + U * h
+    assert ent.shape == (rows,) and ((ent.double() - h).abs() <= tol_h).all(), (
+        (ent.double() - h).abs() / tol_h).max()
+    if tokens is None:
+        assert lp is None
+    else:
+        safe = tokens.long().clamp(0, vocab - 1)[:, None]
+        want = torch.gather(logp, 1, safe)[:, 0]
+        tol = tol_s + U * (torch.gather(finite, 1, safe)[:, 0].abs() + want.abs())
+        good = torch.where(want == -math.inf, lp.double() == -math.inf,
+                           (lp.double() - want).abs() <= tol)
+        good = torch.where(tokens < 0, lp == 0, good)
+        good = torch.where(tokens >= vocab, torch.isnan(lp), good)
+        assert good.all()
+    assert ids.shape == (rows, topk) and top.shape == (rows, topk)
+    if topk:
+        order = torch.sort(logits.float(), dim=1, descending=True, stable=True).indices[:, :topk]
+        assert torch.equal(ids.long(), order), torch.nonzero(ids.long() != order)[:4]
+        want = torch.gather(logp, 1, order)
+        tol = tol_s[:, None] + U * (torch.gather(finite, 1, order).abs() + want.abs())
+        assert ((want == top.double()) | ((top.double() - want).abs() <= tol)).all()
+
+
+def make(torch, rows, vocab, dtype, kind, seed, pad=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    x = torch.randn(rows, vocab + pad, generator=g, device="cuda")
+    if kind == "normal":
+        x *= 3.0
+    elif kind == "peaked":
+        x[:, vocab // 3] += 40.0
+    elif kind == "flat":
+        x *= 1e-3
+    elif kind == "large":  # far from zero, differences of many orders
+        x = x * 300.0 - 5000.0
+    elif kind == "ties":  # few distinct values, both zeros among them
+        x = (x * 2).round() / 4
+    elif kind == "masked":
+        x[torch.rand(x.shape, generator=g, device="cuda") < 0.9] = -math.inf
+        x[:, 0] = 0.5
+    elif kind == "lowest":  # masks of the type's lowest value
+        x[torch.rand(x.shape, generator=g, device="cuda") < 0.5] = torch.finfo(dtype).min
+        x[:, vocab // 2] = 0.0
+    elif kind == "equal":
+        x[:] = -2.5
+    elif kind == "rising":  # the largest last: every stretch has larger ones than those before
+        x = x * 0.01 + torch.arange(vocab + pad, device="cuda") * 0.01
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    return x.to(dtype)[:, :vocab], tokens
+
+
+KINDS = ["normal", "peaked", "flat", "large", "ties", "masked", "lowest", "equal", "rising"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab,topk,pad", [
+    (1, 1, 1, 0), (1, 2, 2, 0), (3, 31, 5, 1), (5, 64, 64, 0), (2, 65, 3, 3), (300, 100, 20, 0),
+    (7, 255, 1, 0), (9, 1000, 20, 8), (1, 8191, 64, 0), (33, 8193, 7, 1), (4, 32768, 0, 0),
+    (65, 50001, 20, 0), (1, 131072, 20, 0), (2, 131073, 64, 5), (1, 262144, 5, 0), (260, 33000, 32, 2)])
+def test_rows(torch, rows, vocab, topk, pad, dtype, kind):
+    logits, tokens = make(torch, rows, vocab, getattr(torch, dtype), kind, rows + vocab, pad)
+    check(torch, logits, tokens, topk)
+
+
+@pytest.mark.parametrize("topk", [0, 1, 2, 3, 8, 16, 31, 33, 63, 64])
+@pytest.mark.parametrize("vocab", [64, 777, 20000, 70001])
+def test_alternatives(torch, vocab, topk):
+    for rows in (1, 40, 600):
+        for kind in ("normal", "ties", "rising"):
+            logits, tokens = make(torch, rows, vocab, torch.bfloat16, kind, topk, 0)
+            check(torch, logits, tokens, topk)
+
+
+def test_many_rows(torch):
+    for rows, vocab in ((70001, 33), (4099, 2000)):
+        logits, tokens = make(torch, rows, vocab, torch.float32, "normal", 1)
+        check(torch, logits, tokens, 5)
+
+
+def test_token_types_and_padding(torch):
+    logits, tokens = make(torch, 12, 4000, torch.float32, "normal", 2)
+    tokens[3] = -1
+    tokens[4] = -100
+    tokens[5] = 4000
+    tokens[6] = (1 << 40) + 3
+    tokens[7] = -(1 << 40)
+    check(torch, logits, tokens, 2)
+    tokens[6], tokens[7] = 2 ** 31 - 1, -2 ** 31
+    check(torch, logits, tokens.to(torch.int32), 2)
+    check(torch, logits, None, 2)
+
+
+@pytest.mark.parametrize("vocab", [40, 5000, 140000])
+def test_rows_without_a_distribution(torch, vocab):
+    """NaN, +inf, and nothing but -inf: NaN results, ids of the order in which NaN is -inf; the rows
+    beside them as ever."""
+    for dtype in (torch.float32, torch.bfloat16):
+        logits, tokens = make(torch, 6, vocab, dtype, "normal", 3)
+        good = logits.clone()
+        logits[1, vocab - 1] = math.nan
+        logits[2, 7] = math.inf
+        logits[3] = -math.inf
+        logits[4] = math.nan
+        tokens[1] = -1
+        lp, ent, ids, top = bb.token_logprobs(logits, tokens, topk=5)
+        assert torch.isnan(ent[1:5]).all() and torch.isnan(lp[2:5]).all() and lp[1] == 0
+        assert torch.isnan(top[1:5]).all()
+        order = torch.where(torch.isnan(logits), -math.inf, logits.float())
+        order = torch.sort(order, dim=1, descending=True, stable=True).indices[:, :5]
+        assert torch.equal(ids.long(), order)
+        want = bb.token_logprobs(good, tokens, topk=5)
+        for a, b in zip((lp, ent, ids, top), want):
+            assert torch.equal(a[[0, 5]], b[[0, 5]])
+
+
+def test_given_outputs_and_streams(torch):
+    logits, tokens = make(torch, 50, 3000, torch.bfloat16, "normal", 4)
+    want = bb.token_logprobs(logits, tokens, topk=6)
+    outs = dict(logprobs=torch.empty(50, device="cuda"), entropy=torch.empty(50, device="cuda"),
+                ids=torch.empty(50, 6, dtype=torch.int32, device="cuda"),
+                top=torch.empty(50, 6, device="cuda"))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = bb.token_logprobs(logits, tokens, topk=6, stream=st, **outs)
+    st.synchronize()
+    for a, b, name in zip(got, want, outs):
+        assert a is outs[name] and torch.equal(a, b)
+
+
+def test_repeats_and_graphs(torch):
+    """The same bits every time, from two graphs that share nothing but the inputs."""
+    for rows, vocab in ((1, 131072), (3, 200000), (90, 5000)):
+        logits, tokens = make(torch, rows, vocab, torch.float32, "normal", 5)
+        want = bb.token_logprobs(logits, tokens, topk=20)
+        torch.cuda.synchronize()
+        graphs, outs = [], []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs.append(bb.token_logprobs(logits, tokens, topk=20))
+            graphs.append(g)
+        for _ in range(4):
+            for g, out in zip(graphs, outs):
+                for t in out:
+                    t.fill_(0)
+                g.replay()
+                eager = bb.token_logprobs(logits, tokens, topk=20)
+                torch.cuda.synchronize()
+                for a, b, c in zip(out, want, eager):
+                    assert torch.equal(a, b) and torch.equal(c, b)
+
+
+def test_logits_past_4_gib(torch):
+    rows, vocab = 9000, 131072
+    logits = torch.zeros(rows, vocab, dtype=torch.float32, device="cuda")
+    at = (torch.arange(rows, device="cuda") * 7919) % vocab
+    logits[torch.arange(rows, device="cuda"), at] = 20.0
+    lp, ent, ids, top = bb.token_logprobs(logits, at, topk=2)
+    assert torch.equal(ids[:, 0].long(), at)
+    assert torch.equal(ids[:, 1].long(), (at == 0).long())
+    want = -math.log1p((vocab - 1) * math.exp(-20.0))
+    assert (lp.double() - want).abs().max() <= U * 30 and torch.equal(lp, top[:, 0])
