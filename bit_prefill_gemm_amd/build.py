@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libbpg.so")
 NATIVE = os.path.join(HERE, "_native.so")
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "skinny.hip", "wide.hip", "strip.hip", "grouped.hip", "moe.hip",
-           "norm.hip", "route.hip", "fp8_quantize.hip", "fp8_stream.hip", "logprobs.hip"]
+           "norm.hip", "route.hip", "fp8_quantize.hip", "fp8_stream.hip", "fp8_tile.hip", "logprobs.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # code-generation flags (the part of the command line that shapes the kernels;
 # the include directories below are paths of this checkout)

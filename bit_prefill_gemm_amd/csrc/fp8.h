@@ -42,6 +42,10 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t stream);
 size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
                                      void *workspace, hipStream_t stream);
+// The kernels over LDS tiles (fp8_tile.hip).
+hipError_t launch_fp8_tile(const Fp8Problem &p, int size, hipStream_t stream);
+hipError_t launch_fp8_tile_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
+                                    hipStream_t stream);
 
 // Log probabilities, entropies and top alternatives of rows of logits.
 struct LogprobsProblem {

@@ -114,6 +114,8 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
 {
     if (p.m == 0)
         return hipSuccess;
+    if (p.m > 64)
+        return launch_fp8_tile(p, p.m > 128 ? 256 : 128, s);
     if (p.m <= 16)
         return p.exact ? stream<1, true>(p, s) : stream<1, false>(p, s);
     if (p.m <= 32)
@@ -123,12 +125,14 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
 
 size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t)
 {
-    return (size_t)m * (size_t)n * sizeof(float);
+    return m > 64 ? 0 : (size_t)m * (size_t)n * sizeof(float);
 }
 
 hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
                                      void *workspace, hipStream_t s)
 {
+    if (p.m > 64)
+        return launch_fp8_tile_quantize(p, codes, scales, s);
     Fp8Problem values = p;
     values.y = workspace;
     values.ldy = p.n;
