@@ -4,6 +4,8 @@
 #include "epilogue.h"
 #include "fp8_mma.h"
 
+#include <type_traits>
+
 namespace bpg {
 namespace {
 
@@ -16,26 +18,46 @@ template <int NI_, int MJ_, int NW_, int MW_> struct Tile {
     static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_;
     static constexpr int kWaves = NW * MW;
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
-    static constexpr int kLoadsW = kRowsW / 8 / kWaves, kLoadsX = kRowsX / 8 / kWaves;
 };
 
-// Codes [rows][k] from `row` on, as a buffer whose reads past the last row
-// give zeros; `most` rows at most.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t *codes, int64_t row,
-                                                          int64_t rows, int64_t k, int most)
+// [rows][row_bytes] from `row` on, `most` rows at most, as a buffer: reads past
+// its last row give zeros.
+__device__ __forceinline__ v4i rows_of(const void *at, int64_t row, int64_t rows, int64_t row_bytes,
+                                       int most)
 {
+    const int64_t first = min(row, rows - 1);
     const int64_t left = max((int64_t)0, min(rows - row, (int64_t)most));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(codes + min(row, rows - 1) * k), 0,
-                                             (int)(left * k), 0x00020000);
+    const uint64_t base = reinterpret_cast<uint64_t>(at) + (uint64_t)(first * row_bytes);
+    return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
+               __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)),
+               __builtin_amdgcn_readfirstlane((int)(left * row_bytes)), 0x00020000};
 }
 
-// 8 rows of 128 codes to LDS.  The 16-byte pieces of a row are stored in the
-// order piece ^ (row % 8), so that the 16 rows that a quarter wave reads at one
-// piece lie in different banks.
-__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t from, uint8_t *to, uint32_t lane_at,
-                                          uint32_t at)
+// Direct loads of 16 or 4 bytes a lane, to LDS addresses to + 16 lane or
+// to + 4 lane.  Written out so that the compiler, which cannot tell the stages
+// of one LDS array apart, waits for none of them before a read: the waits are
+// at the barriers (`arrived`).
+__device__ __forceinline__ void load16(v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
 {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)to, 16, (int)lane_at, (int)at, 0, 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(lane_at), "s"(from), "s"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ void load4(v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(lane_at), "s"(from), "s"(at)
+                 : "memory");
+}
+
+// All direct loads of this wave but the last N are in LDS, its own LDS reads
+// are done, and so are those of the other waves.
+template <int N> __device__ __forceinline__ void arrived()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
@@ -44,8 +66,9 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
 {
     constexpr int NI = T::NI, MJ = T::MJ, G = GATED ? 2 : 1;
     constexpr int kCols = T::kRowsW / G;
-    __shared__ __attribute__((aligned(16))) uint8_t lw0[T::kRowsW * 128], lx0[T::kRowsX * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t lw1[T::kRowsW * 128], lx1[T::kRowsX * 128];
+    constexpr int kX = T::kRowsX * 128, kW = T::kRowsW * 128;
+    constexpr int kStage = kX + kW + T::kRowsX * 4; // codes of x and w, scales of x
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % T::NW, wm = wave / T::NW;
@@ -65,66 +88,59 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
     const int64_t k = p.k;
     const int blocks = (int)fp8_blocks(k);
 
-    // ---- direct loads: lane l of an instruction brings piece l % 8 of row l / 8
+    // ---- direct loads.  Lane l of an instruction brings a 16-byte piece of row
+    //      l / 8: piece l % 8 of the row in LDS, which is piece (l % 8) ^ (l / 8)
+    //      of the row in memory, so that the 16 rows that a quarter wave reads at
+    //      one piece lie in different banks.
+    const uint32_t base = (uint32_t) reinterpret_cast<uintptr_t>((lds_void *)lds);
     const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
     const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
-    const __amdgpu_buffer_rsrc_t xs = rows_of(p.codes, m0, p.m, k, T::kRowsX);
-    const __amdgpu_buffer_rsrc_t ws = rows_of(p.w, n0, p.n, k, kCols);
-    const __amdgpu_buffer_rsrc_t us = GATED ? rows_of(p.up, n0, p.n, k, kCols) : ws;
-    auto load = [&](uint8_t *lw, uint8_t *lx, int b) {
-        const uint32_t at = (uint32_t)b * kFp8Block;
-        // pieces past K are read from past the buffer: zeros
-        const uint32_t l = at + piece < k ? lane_at : 0x80000000u;
-#pragma unroll
-        for (int u = 0; u < T::kLoadsX; u++) {
+    const v4i xs = rows_of(p.codes, m0, p.m, k, T::kRowsX);
+    const v4i ws = rows_of(p.w, n0, p.n, k, kCols);
+    const v4i us = GATED ? rows_of(p.up, n0, p.n, k, kCols) : ws;
+    const v4i ss = rows_of(p.scales, m0, p.m, (int64_t)blocks * 4, T::kRowsX);
+    const int sline = wave % (T::kRowsX / 64) * 64; // rows whose scales this wave brings
+    const uint32_t slane = (uint32_t)((sline + lane) * blocks) * 4;
+    // What a stage brings comes in two groups: x, the scales and each wave's
+    // first half of w's row tiles; and their second half.
+    constexpr int kLoadsX = T::kRowsX / 8 / T::kWaves, kLoadsW = T::kRowsW / 16 / T::kWaves;
+    constexpr int kFirst = kLoadsX + 1 + kLoadsW, kSecond = kLoadsW;
+    auto load_w = [&](uint32_t to, int b, uint32_t l, int half, int u) {
+        constexpr int kHalf = 8 * NI, kParts = kHalf / 8; // rows and loads of a wave's half
+        const int i = wave + T::kWaves * u, owner = i / kParts, row = i % kParts * 8;
+        const int in = owner * 2 * kHalf + half * kHalf + row;
+        const int col = GATED ? owner * kHalf + row : in;
+        load16(GATED && half ? us : ws, to + kX + in * 128, l, (uint32_t)(col * k) + b * kFp8Block);
+    };
+    // pieces past K are read from past the buffer: zeros
+    auto lane_from = [&](int b) {
+        return (uint32_t)(b * kFp8Block) + piece < k ? lane_at : 0x80000000u;
+    };
+    auto load_first = [&](int b, int u) {
+        const uint32_t to = base + (b & 1) * kStage, l = lane_from(b);
+        if (u < kLoadsX) {
             const int i = wave + T::kWaves * u;
-            load_rows(xs, lx + 1024 * i, l, (uint32_t)(8 * i * k) + at);
-        }
-#pragma unroll
-        for (int u = 0; u < T::kLoadsW; u++) {
-            const int i = wave + T::kWaves * u;
-            if constexpr (GATED) {
-                constexpr int kWaveRows = 16 * NI, kHalf = kWaveRows / 2;
-                const int row = 8 * i, in_wave = row % kWaveRows;
-                const int col = row / kWaveRows * kHalf + in_wave % kHalf;
-                if (in_wave < kHalf)
-                    load_rows(ws, lw + 1024 * i, l, (uint32_t)(col * k) + at);
-                else
-                    load_rows(us, lw + 1024 * i, l, (uint32_t)(col * k) + at);
-            } else {
-                load_rows(ws, lw + 1024 * i, l, (uint32_t)(8 * i * k) + at);
-            }
+            load16(xs, to + 1024 * i, l, (uint32_t)(8 * i * k) + b * kFp8Block);
+        } else if (u < kLoadsX + kLoadsW) {
+            load_w(to, b, l, 0, u - kLoadsX);
+        } else {
+            load4(ss, to + kX + kW + 4 * sline, b < blocks ? slane : 0x80000000u, b * 4);
         }
     };
+    auto load_second = [&](int b, int u) {
+        load_w(base + (b & 1) * kStage, b, lane_from(b), 1, u);
+    };
 
-    // ---- scales: one per lane and row tile of x, one per wave of the weights
-    const __amdgpu_buffer_rsrc_t xscales = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float *>(p.scales + m0 * blocks), 0,
-        (int)(min(p.m - m0, (int64_t)T::kRowsX) * blocks * 4), 0x00020000);
-    const uint32_t sx_at = (uint32_t)(16 * wm * MJ + r) * (uint32_t)blocks * 4;
+    // ---- scales of the weights: one per wave and block
+    typedef const __attribute__((address_space(4))) float *Scalars;
     const int64_t wb = min((n0 + wn * (16 * NI / G)) / kFp8Block, fp8_blocks(p.n) - 1) * blocks;
-    const float *sw[G];
-    sw[0] = p.w_scales + wb;
-    if constexpr (GATED)
-        sw[1] = p.up_scales + wb;
-    float sx[MJ], ws_now[G];
-    auto load_scales = [&](int b) {
-#pragma unroll
-        for (int j = 0; j < MJ; j++)
-            sx[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                xscales, (int)sx_at, (16 * j * blocks + b) * 4, 0));
-#pragma unroll
-        for (int q = 0; q < G; q++)
-            ws_now[q] = sw[q][b];
-    };
-
-    float sv[G][MJ];
-    auto make_scales = [&] {
-#pragma unroll
-        for (int j = 0; j < MJ; j++)
-#pragma unroll
-            for (int q = 0; q < G; q++)
-                sv[q][j] = sx[j] * ws_now[q];
+    const Scalars sw = (Scalars)(p.w_scales + wb), su = (Scalars)(GATED ? p.up_scales + wb : nullptr);
+    float w_scale[G], w_next[G];
+    auto load_scalars = [&](int b) {
+        b = min(b, blocks - 1);
+        w_next[0] = sw[b];
+        if constexpr (GATED)
+            w_next[1] = su[b];
     };
 
     v4f acc[NI][MJ];
@@ -135,63 +151,135 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
             acc[i][j] = v4f{0, 0, 0, 0};
 
     const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
-    const uint32_t wrow = (uint32_t)(wn * NI) * 2048, xrow = (uint32_t)(wm * MJ) * 2048;
-    auto operand = [&](const uint8_t *base, uint32_t tile) {
-        return Operand<EXACT>(*reinterpret_cast<const v4i *>(base + tile + lo),
-                              *reinterpret_cast<const v4i *>(base + tile + hi));
+    const uint32_t x_lo = wm * MJ * 2048 + lo, x_hi = wm * MJ * 2048 + hi;
+    const uint32_t w_lo = kX + wn * NI * 2048 + lo, w_hi = kX + wn * NI * 2048 + hi;
+    const uint32_t s_at = kX + kW + (wm * MJ * 16 + r) * 4;
+    Operand<EXACT> x[MJ], w, next;
+    float sx[MJ], sv[MJ];
+    auto read_w = [&](int stage, int i) {
+        const uint8_t *at = lds + stage * kStage + 2048 * i;
+        next = Operand<EXACT>(*reinterpret_cast<const v4i *>(at + w_lo),
+                              *reinterpret_cast<const v4i *>(at + w_hi));
     };
-    // The additions of a tile follow its matrix instruction kLag tiles behind.
-    constexpr int kLag = 3, kTiles = NI * MJ;
-    auto compute = [&](const uint8_t *lw, const uint8_t *lx) {
-        Operand<EXACT> x[MJ];
+    auto read_x = [&](int stage, int j) {
+        const uint8_t *at = lds + stage * kStage + 2048 * j;
+        x[j] = Operand<EXACT>(*reinterpret_cast<const v4i *>(at + x_lo),
+                              *reinterpret_cast<const v4i *>(at + x_hi));
+    };
+    auto read_scales = [&](int stage) {
 #pragma unroll
         for (int j = 0; j < MJ; j++)
-            x[j] = operand(lx, xrow + 2048 * j);
-        Operand<EXACT> w = operand(lw, wrow), next = w;
-        v4f d[kLag + 1];
+            sx[j] = *reinterpret_cast<const float *>(lds + stage * kStage + s_at + 64 * j);
+    };
+    // The additions of a tile follow its matrix instruction kLag tiles behind,
+    // into the next block's: the first ones add zeros.
+    constexpr int kLag = 3, kRing = kLag + 1, kTiles = NI * MJ;
+    static_assert(kTiles % kRing == 0);
+    v4f d[kRing];
 #pragma unroll
-        for (int t = 0; t < kTiles + kLag; t++) {
-            const int i = t / MJ, j = t % MJ;
-            if (t < kTiles) {
-                if (j == 0) {
-                    w = next;
-                    if (i + 1 < NI)
-                        next = operand(lw, wrow + 2048 * (i + 1));
+    for (int q = 0; q < kRing; q++)
+        d[q] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < MJ; j++)
+        sv[j] = 0;
+    auto additions = [&](int t) { // of tile t, or of the block before for t < 0
+        const bool past = t < 0;
+        t = past ? t + kTiles : t;
+        const int i = t / MJ, j = t % MJ;
+        if (!past && i == 0)
+            sv[j] = sx[j] * w_scale[0];
+        if (GATED && !past && i == NI / 2)
+            sv[j] = sx[j] * w_scale[G - 1];
+        add_scaled(acc[i][j], d[t % kRing], sv[j]);
+    };
+
+    // One block of K from stage b & 1.  x and the first row tile of w have been
+    // read; on the way the other stage arrives and this one is loaded anew:
+    //   before row tile NI/2 - 1: the second half of w is there, and x, the
+    //     scales and the first half are read by everybody: block b + 2's follow;
+    //   before the last row tile: the next block's x, scales and first half are
+    //     there, and this one's second half is read by everybody.
+    // Each load has about one and a half blocks' time to arrive.
+    auto block = [&](auto stage_of, int b) {
+        constexpr int stage = decltype(stage_of)::value;
+        constexpr int kTurn = NI / 2 - 1, kLast = NI - 1;
+        constexpr int kPerRow = (kFirst + kLast - kTurn - 1) / (kLast - kTurn);
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+            if (i == kTurn || i == kLast)
+                arrived<kFirst + kSecond>();
+            w = next;
+            if (i == 0) {
+#pragma unroll
+                for (int q = 0; q < G; q++)
+                    w_scale[q] = w_next[q];
+                load_scalars(b + 1);
+            }
+            if (i < kLast)
+                read_w(stage, i + 1);
+            else
+                read_w(stage ^ 1, 0);
+            if (i >= kTurn && i < kLast) {
+#pragma unroll
+                for (int u = (i - kTurn) * kPerRow; u < min((i - kTurn + 1) * kPerRow, kFirst); u++)
+                    load_first(b + 2, u);
+            }
+            if (i == kLast) {
+#pragma unroll
+                for (int u = 0; u < kSecond; u++)
+                    load_second(b + 2, u);
+            }
+#pragma unroll
+            for (int j = 0; j < MJ; j++) {
+                const int t = i * MJ + j;
+                d[t % kRing] = dot(w, x[j]);
+                additions(t - kLag);
+                if (i == kLast)
+                    read_x(stage ^ 1, j);
+            }
+            if (i == kLast)
+                read_scales(stage ^ 1);
+            if (!EXACT) {
+#pragma unroll
+                for (int j = 0; j < MJ; j++) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0); // a matrix instruction
+                    __builtin_amdgcn_sched_group_barrier(0x2, 4, 0); // an earlier one's additions
                 }
-                d[t % (kLag + 1)] = dot(w, x[j]);
             }
-            if (t >= kLag) {
-                const int o = t - kLag;
-                add_scaled(acc[o / MJ][o % MJ], d[o % (kLag + 1)],
-                           sv[GATED && o / MJ >= NI / 2 ? G - 1 : 0][o % MJ]);
-            }
-            if (j == MJ - 1)
-                __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
-    // Two blocks a round, one basic block: what is loaded past the last one is
-    // zeros that nobody reads.
-    load(lw0, lx0, 0);
-    load_scales(0);
+#pragma unroll
+    for (int u = 0; u < kFirst; u++)
+        load_first(0, u);
+#pragma unroll
+    for (int u = 0; u < kSecond; u++)
+        load_second(0, u);
+#pragma unroll
+    for (int u = 0; u < kFirst; u++)
+        load_first(1, u);
+    load_scalars(0);
+    arrived<kFirst + kSecond>();
+#pragma unroll
+    for (int u = 0; u < kSecond; u++)
+        load_second(1, u);
+    read_w(0, 0);
+#pragma unroll
+    for (int j = 0; j < MJ; j++)
+        read_x(0, j);
+    read_scales(0);
     int b = 0;
     for (; b + 1 < blocks; b += 2) {
-        __syncthreads(); // block b is there, and nobody reads the other buffer any more
-        make_scales();
-        load(lw1, lx1, b + 1);
-        load_scales(b + 1);
-        compute(lw0, lx0);
-        __syncthreads();
-        make_scales();
-        load(lw0, lx0, b + 2);
-        load_scales(min(b + 2, blocks - 1));
-        compute(lw1, lx1);
+        block(std::integral_constant<int, 0>{}, b);
+        block(std::integral_constant<int, 1>{}, b + 1);
     }
-    __syncthreads();
-    if (b < blocks) {
-        make_scales();
-        compute(lw0, lx0);
-    }
+    if (b < blocks)
+        block(std::integral_constant<int, 0>{}, b);
+#pragma unroll
+    for (int t = -kLag; t < 0; t++)
+        additions(t);
+    arrived<0>(); // loads past the last block write to LDS, too
 
     // ---- results
     constexpr int NO = NI / G; // row tiles of results
@@ -209,8 +297,7 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
     if constexpr (QUANT) {
         // a block of 128 columns: the waves of a row tile share its maximum
         static_assert(!QUANT || kCols == 128);
-        __syncthreads(); // the operands are no longer read
-        uint32_t *top = reinterpret_cast<uint32_t *>(lx0);
+        uint32_t *top = reinterpret_cast<uint32_t *>(lds);
         uint32_t mine[MJ];
 #pragma unroll
         for (int j = 0; j < MJ; j++) {
