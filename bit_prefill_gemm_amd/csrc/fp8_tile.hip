@@ -4,12 +4,14 @@
 #include "epilogue.h"
 #include "fp8_mma.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace bpg {
 namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
 // weights) by 16 MJ rows.  Gated, the first half of a wave's NI row tiles are
@@ -53,6 +55,25 @@ __device__ __forceinline__ void load4(v4i from, uint32_t to, uint32_t lane_at, u
                  : "memory");
 }
 
+template <class V> __device__ __forceinline__ V lds_read(uint32_t at, int offset)
+{
+    typedef const __attribute__((address_space(3))) V *Ptr;
+    return *(Ptr)(at + offset);
+}
+
+template <class V> __device__ __forceinline__ void lds_write(uint32_t at, V v)
+{
+    typedef __attribute__((address_space(3))) V *Ptr;
+    *(Ptr)at = v;
+}
+
+// An integer that the optimizer cannot take apart.
+__device__ __forceinline__ uint32_t opaque(uint32_t x)
+{
+    asm("" : "+v"(x));
+    return x;
+}
+
 // All direct loads of this wave but the last N are in LDS, its own LDS reads
 // are done, and so are those of the other waves.
 template <int N> __device__ __forceinline__ void arrived()
@@ -61,8 +82,8 @@ template <int N> __device__ __forceinline__ void arrived()
 }
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
-__global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_tile_kernel(
-    const Fp8Problem p, uint8_t *out_codes, float *out_scales, bool vec)
+__global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
+    const Fp8Problem p, uint8_t *out_codes, float *out_scales)
 {
     constexpr int NI = T::NI, MJ = T::MJ, G = GATED ? 2 : 1;
     constexpr int kCols = T::kRowsW / G;
@@ -131,16 +152,21 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
         load_w(base + (b & 1) * kStage, b, lane_from(b), 1, u);
     };
 
-    // ---- scales of the weights: one per wave and block
-    typedef const __attribute__((address_space(4))) float *Scalars;
+    // ---- scales of the weights: one per wave and block, 64 blocks' at a time in
+    //      the lanes of a register.  (As scalar loads they would share a counter
+    //      with the LDS reads, which then could not be waited for one by one.)
     const int64_t wb = min((n0 + wn * (16 * NI / G)) / kFp8Block, fp8_blocks(p.n) - 1) * blocks;
-    const Scalars sw = (Scalars)(p.w_scales + wb), su = (Scalars)(GATED ? p.up_scales + wb : nullptr);
-    float w_scale[G], w_next[G];
-    auto load_scalars = [&](int b) {
-        b = min(b, blocks - 1);
-        w_next[0] = sw[b];
+    float w_lanes[G], w_scale[G];
+    auto load_w_scales = [&](int b) {
+        const int64_t at = wb + min(b + lane, blocks - 1);
+        w_lanes[0] = p.w_scales[at];
         if constexpr (GATED)
-            w_next[1] = su[b];
+            w_lanes[1] = p.up_scales[at];
+        // wait here, not where they are used: that is in the loop below, and the
+        // wait would be for its direct loads too
+#pragma unroll
+        for (int q = 0; q < G; q++)
+            asm volatile("" : "+v"(w_lanes[q]));
     };
 
     v4f acc[NI][MJ];
@@ -150,26 +176,34 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
         for (int j = 0; j < MJ; j++)
             acc[i][j] = v4f{0, 0, 0, 0};
 
+    // LDS addresses of this lane's operands, a register each per stage: the rest
+    // of an address is a constant of the instruction
     const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
-    const uint32_t x_lo = wm * MJ * 2048 + lo, x_hi = wm * MJ * 2048 + hi;
-    const uint32_t w_lo = kX + wn * NI * 2048 + lo, w_hi = kX + wn * NI * 2048 + hi;
-    const uint32_t s_at = kX + kW + (wm * MJ * 16 + r) * 4;
-    Operand<EXACT> x[MJ], w, next;
+    uint32_t x_lo[2], x_hi[2], w_lo[2], w_hi[2], s_at[2];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        x_lo[q] = opaque(base + q * kStage + wm * MJ * 2048 + lo);
+        x_hi[q] = opaque(base + q * kStage + wm * MJ * 2048 + hi);
+        w_lo[q] = opaque(base + q * kStage + kX + wn * NI * 2048 + lo);
+        w_hi[q] = opaque(base + q * kStage + kX + wn * NI * 2048 + hi);
+        s_at[q] = opaque(base + q * kStage + kX + kW + (wm * MJ * 16 + r) * 4);
+    }
+    // w's row tiles are read kAhead tiles before their use
+    constexpr int kAhead = 2;
+    Operand<EXACT> x[MJ], w[kAhead];
     float sx[MJ], sv[MJ];
     auto read_w = [&](int stage, int i) {
-        const uint8_t *at = lds + stage * kStage + 2048 * i;
-        next = Operand<EXACT>(*reinterpret_cast<const v4i *>(at + w_lo),
-                              *reinterpret_cast<const v4i *>(at + w_hi));
+        w[i % kAhead] = Operand<EXACT>(lds_read<v4i>(w_lo[stage], 2048 * i),
+                                       lds_read<v4i>(w_hi[stage], 2048 * i));
     };
     auto read_x = [&](int stage, int j) {
-        const uint8_t *at = lds + stage * kStage + 2048 * j;
-        x[j] = Operand<EXACT>(*reinterpret_cast<const v4i *>(at + x_lo),
-                              *reinterpret_cast<const v4i *>(at + x_hi));
+        x[j] = Operand<EXACT>(lds_read<v4i>(x_lo[stage], 2048 * j),
+                              lds_read<v4i>(x_hi[stage], 2048 * j));
     };
     auto read_scales = [&](int stage) {
 #pragma unroll
         for (int j = 0; j < MJ; j++)
-            sx[j] = *reinterpret_cast<const float *>(lds + stage * kStage + s_at + 64 * j);
+            sx[j] = lds_read<float>(s_at[stage], 64 * j);
     };
     // The additions of a tile follow its matrix instruction kLag tiles behind,
     // into the next block's: the first ones add zeros.
@@ -193,32 +227,29 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
         add_scaled(acc[i][j], d[t % kRing], sv[j]);
     };
 
-    // One block of K from stage b & 1.  x and the first row tile of w have been
-    // read; on the way the other stage arrives and this one is loaded anew:
-    //   before row tile NI/2 - 1: the second half of w is there, and x, the
-    //     scales and the first half are read by everybody: block b + 2's follow;
-    //   before the last row tile: the next block's x, scales and first half are
-    //     there, and this one's second half is read by everybody.
+    // One block of K from stage b & 1.  x and the first kAhead row tiles of w
+    // have been read; on the way the other stage arrives and this one is loaded
+    // anew:
+    //   at row tile kTurn: the second half of w is there, and x, the scales and
+    //     the first half are read by everybody: block b + 2's follow;
+    //   at row tile kLast: the next block's x, scales and first half are there,
+    //     and this one's second half is read by everybody.
     // Each load has about one and a half blocks' time to arrive.
     auto block = [&](auto stage_of, int b) {
         constexpr int stage = decltype(stage_of)::value;
-        constexpr int kTurn = NI / 2 - 1, kLast = NI - 1;
+        constexpr int kTurn = NI / 2 - kAhead, kLast = NI - kAhead;
         constexpr int kPerRow = (kFirst + kLast - kTurn - 1) / (kLast - kTurn);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
             if (i == kTurn || i == kLast)
                 arrived<kFirst + kSecond>();
-            w = next;
+            const Operand<EXACT> row = w[i % kAhead];
             if (i == 0) {
 #pragma unroll
                 for (int q = 0; q < G; q++)
-                    w_scale[q] = w_next[q];
-                load_scalars(b + 1);
+                    w_scale[q] = __uint_as_float(
+                        __builtin_amdgcn_readlane(__float_as_uint(w_lanes[q]), b & 63));
             }
-            if (i < kLast)
-                read_w(stage, i + 1);
-            else
-                read_w(stage ^ 1, 0);
             if (i >= kTurn && i < kLast) {
 #pragma unroll
                 for (int u = (i - kTurn) * kPerRow; u < min((i - kTurn + 1) * kPerRow, kFirst); u++)
@@ -232,12 +263,16 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
 #pragma unroll
             for (int j = 0; j < MJ; j++) {
                 const int t = i * MJ + j;
-                d[t % kRing] = dot(w, x[j]);
+                d[t % kRing] = dot(row, x[j]);
                 additions(t - kLag);
-                if (i == kLast)
+                if (i == NI - 1)
                     read_x(stage ^ 1, j);
             }
-            if (i == kLast)
+            if (i < kLast)
+                read_w(stage, i + kAhead);
+            else
+                read_w(stage ^ 1, i + kAhead - NI);
+            if (i == NI - 1)
                 read_scales(stage ^ 1);
             if (!EXACT) {
 #pragma unroll
@@ -259,23 +294,28 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
 #pragma unroll
     for (int u = 0; u < kFirst; u++)
         load_first(1, u);
-    load_scalars(0);
     arrived<kFirst + kSecond>();
 #pragma unroll
     for (int u = 0; u < kSecond; u++)
         load_second(1, u);
-    read_w(0, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead; i++)
+        read_w(0, i);
 #pragma unroll
     for (int j = 0; j < MJ; j++)
         read_x(0, j);
     read_scales(0);
-    int b = 0;
-    for (; b + 1 < blocks; b += 2) {
-        block(std::integral_constant<int, 0>{}, b);
-        block(std::integral_constant<int, 1>{}, b + 1);
+    for (int b0 = 0; b0 < blocks; b0 += 64) {
+        load_w_scales(b0);
+        const int end = min(b0 + 64, blocks);
+        int b = b0;
+        for (; b + 1 < end; b += 2) {
+            block(std::integral_constant<int, 0>{}, b);
+            block(std::integral_constant<int, 1>{}, b + 1);
+        }
+        if (b < end)
+            block(std::integral_constant<int, 0>{}, b);
     }
-    if (b < blocks)
-        block(std::integral_constant<int, 0>{}, b);
 #pragma unroll
     for (int t = -kLag; t < 0; t++)
         additions(t);
@@ -294,11 +334,49 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
                 acc[i][j] = v4f{t[0], t[1], t[2], t[3]} * acc[i + NO][j];
             }
     }
+    // Results go through this wave's own part of LDS, so that a store is 16 bytes
+    // a lane of whole rows: straight from the registers it would be 32 bytes of
+    // each of 16 rows.  The 16-byte pieces of a row are stored in the order
+    // piece ^ row, as above.
+    constexpr int kValue = QUANT ? 1 : EXACT ? 4 : 2, kPerPiece = 16 / kValue;
+    constexpr int kRow = 16 * NO * kValue, kPieces = kRow / 16; // bytes, 16-byte pieces
+    const uint32_t mine = base + wave * (16 * MJ * kRow);
+    static_assert(T::kWaves * 16 * MJ * kRow + 8 * T::kRowsX <= 2 * kStage);
+    auto put = [&](int i, int j, auto v) { // columns 16 i + 4 g .. + 3 of row 16 j + r
+        const int line = 16 * j + r, at = (16 * i + 4 * g) * kValue;
+        lds_write(mine + line * kRow + ((at / 16) ^ (line % kPieces)) * 16 + at % 16, v);
+    };
+    auto store = [&](void *y, int64_t ldy) {
+        constexpr int kLines = 64 / kPieces; // rows per instruction
+#pragma unroll
+        for (int q = 0; q < 16 * MJ / kLines; q++) {
+            const int line = q * kLines + lane / kPieces, c = lane % kPieces;
+            const v4i v = lds_read<v4i>(mine + line * kRow + (c ^ (line % kPieces)) * 16, 0);
+            const int64_t row = m0 + 16 * wm * MJ + line, n = col0 + c * kPerPiece;
+            if (row >= p.m || n >= p.n)
+                continue;
+            uint8_t *to = static_cast<uint8_t *>(y) + (row * ldy + n) * kValue;
+            if (n + kPerPiece <= p.n) {
+                __builtin_memcpy(__builtin_assume_aligned(to, kValue), &v, 16);
+            } else {
+                const int left = (int)(p.n - n);
+                for (int e = 0; e < left; e++) {
+                    const uint32_t word = (uint32_t)v[e * kValue / 4] >> (8 * (e * kValue % 4));
+                    if constexpr (kValue == 4)
+                        reinterpret_cast<uint32_t *>(to)[e] = word;
+                    else if constexpr (kValue == 2)
+                        reinterpret_cast<uint16_t *>(to)[e] = (uint16_t)word;
+                    else
+                        to[e] = (uint8_t)word;
+                }
+            }
+        }
+    };
     if constexpr (QUANT) {
         // a block of 128 columns: the waves of a row tile share its maximum
         static_assert(!QUANT || kCols == 128);
-        uint32_t *top = reinterpret_cast<uint32_t *>(lds);
-        uint32_t mine[MJ];
+        const uint32_t tops = base + 2 * kStage - 4 * T::NW * T::kRowsX;
+        uint32_t top[MJ];
 #pragma unroll
         for (int j = 0; j < MJ; j++) {
             uint32_t a = 0;
@@ -310,49 +388,42 @@ __global__ __launch_bounds__(64 * T::kWaves, T::kWaves == 8 ? 2 : 2) void fp8_ti
                         a = max(a, __float_as_uint(acc[i][j][q]) & 0x7fffffffu);
                 }
             a = max(a, (uint32_t)__shfl_xor((int)a, 16));
-            mine[j] = max(a, (uint32_t)__shfl_xor((int)a, 32));
+            top[j] = max(a, (uint32_t)__shfl_xor((int)a, 32));
             if (g == 0)
-                top[wn * T::kRowsX + 16 * (wm * MJ + j) + r] = mine[j];
+                lds_write(tops + 4 * (wn * T::kRowsX + 16 * (wm * MJ + j) + r), top[j]);
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < MJ; j++) {
             const int line = 16 * (wm * MJ + j) + r;
-            uint32_t a = mine[j];
 #pragma unroll
             for (int o = 0; o < T::NW; o++)
-                a = max(a, top[o * T::kRowsX + line]);
-            const float d = __uint_as_float(a) / 448.0f;
-            const float inv = d > 0.0f ? fminf(1.0f / d, 3.402823466e38f) : 0.0f;
-            const int64_t row = m0 + line;
-            if (row >= p.m)
-                continue;
-            if (wn == 0 && g == 0)
-                out_scales[row * fp8_blocks(p.n) + n0 / kFp8Block] = d;
+                top[j] = max(top[j], lds_read<uint32_t>(tops + 4 * (o * T::kRowsX + line), 0));
+            const float d = __uint_as_float(top[j]) / 448.0f;
+            const float inv = d > 0.0f ? fminf(1.0f / d, FLT_MAX) : 0.0f;
+            if (wn == 0 && g == 0 && m0 + line < p.m)
+                out_scales[(m0 + line) * fp8_blocks(p.n) + n0 / kFp8Block] = d;
 #pragma unroll
             for (int i = 0; i < NO; i++) {
                 const v4f v = acc[i][j] * inv;
                 int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-                c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], c, true);
-                const int64_t n = col0 + 16 * i + 4 * g;
-                if (n < p.n)
-                    *reinterpret_cast<int *>(out_codes + row * p.n + n) = c;
+                put(i, j, __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], c, true));
             }
         }
+        store(out_codes, p.n);
     } else {
 #pragma unroll
-        for (int j = 0; j < MJ; j++) {
-            const int64_t row = m0 + 16 * (wm * MJ + j) + r;
-            if (row >= p.m)
-                continue;
+        for (int j = 0; j < MJ; j++)
 #pragma unroll
             for (int i = 0; i < NO; i++) {
-                const int64_t n = col0 + 16 * i + 4 * g;
-                if (n < p.n)
-                    store4(p.y, p.y_bf16, vec, row * p.ldy + n, (int)min((int64_t)4, p.n - n),
-                           acc[i][j]);
+                const v4f v = acc[i][j];
+                if constexpr (EXACT)
+                    put(i, j, v);
+                else
+                    put(i, j, v2u{bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                  bf16_bits(v[2]) | bf16_bits(v[3]) << 16});
             }
-        }
+        store(p.y, p.ldy);
     }
 }
 
@@ -365,7 +436,7 @@ hipError_t launch_tile(const Fp8Problem &p, uint8_t *codes, float *scales, hipSt
     constexpr int kCols = T::kRowsW / (GATED ? 2 : 1);
     const int64_t tiles = (p.m + T::kRowsX - 1) / T::kRowsX * ((p.n + kCols - 1) / kCols);
     fp8_tile_kernel<T, GATED, EXACT, QUANT><<<(unsigned)tiles, 64 * T::kWaves, 0, s>>>(
-        p, codes, scales, !QUANT && vector_rows(p.y, p.ldy, p.y_bf16));
+        p, codes, scales);
     return hipGetLastError();
 }
 
