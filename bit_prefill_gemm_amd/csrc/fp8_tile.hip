@@ -16,9 +16,9 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
 // weights) by 16 MJ rows.  Gated, the first half of a wave's NI row tiles are
 // rows of the gate and the second half the same rows of the up projection.
-template <int NI_, int MJ_, int NW_, int MW_> struct Tile {
-    static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_;
-    static constexpr int kWaves = NW * MW;
+template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_> struct Tile {
+    static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_, KS = KS_, S = S_;
+    static constexpr int kWaves = NW * MW; // of a group
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
 };
 
@@ -35,8 +35,8 @@ __device__ __forceinline__ v4i rows_of(const void *at, int64_t row, int64_t rows
                __builtin_amdgcn_readfirstlane((int)(left * row_bytes)), 0x00020000};
 }
 
-// Direct loads of 16 or 4 bytes a lane, to LDS addresses to + 16 lane or
-// to + 4 lane.  Written out so that the compiler, which cannot tell the stages
+// Direct loads of 16 bytes a lane, to LDS address to + 16 lane.
+// Written out so that the compiler, which cannot tell the stages
 // of one LDS array apart, waits for none of them before a read: the waits are
 // at the barriers (`arrived`).
 __device__ __forceinline__ void load16(v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
@@ -47,11 +47,14 @@ __device__ __forceinline__ void load16(v4i from, uint32_t to, uint32_t lane_at, 
                  : "memory");
 }
 
-__device__ __forceinline__ void load4(v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
+// the same where `now`, else nothing (all lanes are on around it)
+__device__ __forceinline__ void load16_if(bool now, v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    const int lanes = __builtin_amdgcn_readfirstlane(now ? -1 : 0);
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
+                 "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
                  :
-                 : "s"(to), "v"(lane_at), "s"(from), "s"(at)
+                 : "s"(to), "v"(lane_at), "s"(from), "s"(at), "s"(lanes)
                  : "memory");
 }
 
@@ -82,16 +85,18 @@ template <int N> __device__ __forceinline__ void arrived()
 }
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
-__global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
+__global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const Fp8Problem p, uint8_t *out_codes, float *out_scales)
 {
-    constexpr int NI = T::NI, MJ = T::MJ, G = GATED ? 2 : 1;
+    constexpr int NI = T::NI, MJ = T::MJ, S = T::S, KS = T::KS, G = GATED ? 2 : 1;
     constexpr int kCols = T::kRowsW / G;
     constexpr int kX = T::kRowsX * 128, kW = T::kRowsW * 128;
-    constexpr int kStage = kX + kW + T::kRowsX * 4; // codes of x and w, scales of x
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+    constexpr int kStage = kX + kW, kScales = T::kRowsX * 16; // four blocks' scales of x
+    constexpr int kGroup = S * kStage + 2 * kScales;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[KS * kGroup];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % T::kWaves;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / T::kWaves;
     const int wn = wave % T::NW, wm = wave / T::NW;
     const int r = lane & 15, g = lane >> 4;
     // ---- which tile: every XCD a stretch of them, in panels of eight row tiles
@@ -113,43 +118,51 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     //      l / 8: piece l % 8 of the row in LDS, which is piece (l % 8) ^ (l / 8)
     //      of the row in memory, so that the 16 rows that a quarter wave reads at
     //      one piece lie in different banks.
-    const uint32_t base = (uint32_t) reinterpret_cast<uintptr_t>((lds_void *)lds);
+    const uint32_t base =
+        (uint32_t) reinterpret_cast<uintptr_t>((lds_void *)lds) + group * kGroup;
     const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
     const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
     const v4i xs = rows_of(p.codes, m0, p.m, k, T::kRowsX);
     const v4i ws = rows_of(p.w, n0, p.n, k, kCols);
     const v4i us = GATED ? rows_of(p.up, n0, p.n, k, kCols) : ws;
     const v4i ss = rows_of(p.scales, m0, p.m, (int64_t)blocks * 4, T::kRowsX);
-    const int sline = wave % (T::kRowsX / 64) * 64; // rows whose scales this wave brings
-    const uint32_t slane = (uint32_t)((sline + lane) * blocks) * 4;
+    // scales: 64 rows of 16 bytes an instruction, every fourth block
+    constexpr int kScaleWaves = T::kRowsX / 64;
+    static_assert(kScaleWaves <= T::kWaves);
+    const uint32_t slane = (uint32_t)((64 * wave + lane) * blocks) * 4;
     // What a stage brings comes in two groups: x, the scales and each wave's
     // first half of w's row tiles; and their second half.
     constexpr int kLoadsX = T::kRowsX / 8 / T::kWaves, kLoadsW = T::kRowsW / 16 / T::kWaves;
-    constexpr int kFirst = kLoadsX + 1 + kLoadsW, kSecond = kLoadsW;
+    constexpr int kFirst = kLoadsX + kLoadsW, kSecond = kLoadsW;
+    // a group's block b is block b + before of K
+    const int rounds = (blocks + KS - 1) / KS, before = group * rounds;
+    auto at_of = [&](int b) { return (uint32_t)(b + before) * kFp8Block; };
     auto load_w = [&](uint32_t to, int b, uint32_t l, int half, int u) {
         constexpr int kHalf = 8 * NI, kParts = kHalf / 8; // rows and loads of a wave's half
         const int i = wave + T::kWaves * u, owner = i / kParts, row = i % kParts * 8;
         const int in = owner * 2 * kHalf + half * kHalf + row;
         const int col = GATED ? owner * kHalf + row : in;
-        load16(GATED && half ? us : ws, to + kX + in * 128, l, (uint32_t)(col * k) + b * kFp8Block);
+        load16(GATED && half ? us : ws, to + kX + in * 128, l, (uint32_t)(col * k) + at_of(b));
     };
     // pieces past K are read from past the buffer: zeros
     auto lane_from = [&](int b) {
-        return (uint32_t)(b * kFp8Block) + piece < k ? lane_at : 0x80000000u;
+        return at_of(b) + piece < k ? lane_at : 0x80000000u;
     };
-    auto load_first = [&](int b, int u) {
-        const uint32_t to = base + (b & 1) * kStage, l = lane_from(b);
+    auto load_first = [&](int stage, int b, int u) {
+        const uint32_t to = base + stage * kStage, l = lane_from(b);
         if (u < kLoadsX) {
             const int i = wave + T::kWaves * u;
-            load16(xs, to + 1024 * i, l, (uint32_t)(8 * i * k) + b * kFp8Block);
-        } else if (u < kLoadsX + kLoadsW) {
-            load_w(to, b, l, 0, u - kLoadsX);
+            load16(xs, to + 1024 * i, l, (uint32_t)(8 * i * k) + at_of(b));
         } else {
-            load4(ss, to + kX + kW + 4 * sline, b < blocks ? slane : 0x80000000u, b * 4);
+            load_w(to, b, l, 0, u - kLoadsX);
         }
     };
-    auto load_second = [&](int b, int u) {
-        load_w(base + (b & 1) * kStage, b, lane_from(b), 1, u);
+    auto load_scales = [&](int b, bool now) { // of blocks b..b+3
+        load16_if(now && wave < kScaleWaves, ss, base + S * kStage + (b / 4 & 1) * kScales + 1024 * wave,
+                  slane, (uint32_t)(b + before) * 4);
+    };
+    auto load_second = [&](int stage, int b, int u) {
+        load_w(base + stage * kStage, b, lane_from(b), 1, u);
     };
 
     // ---- scales of the weights: one per wave and block, 64 blocks' at a time in
@@ -158,10 +171,10 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     const int64_t wb = min((n0 + wn * (16 * NI / G)) / kFp8Block, fp8_blocks(p.n) - 1) * blocks;
     float w_lanes[G], w_scale[G];
     auto load_w_scales = [&](int b) {
-        const int64_t at = wb + min(b + lane, blocks - 1);
-        w_lanes[0] = p.w_scales[at];
+        const int at = b + lane + before;
+        w_lanes[0] = at < blocks ? p.w_scales[wb + at] : 0.0f;
         if constexpr (GATED)
-            w_lanes[1] = p.up_scales[at];
+            w_lanes[1] = at < blocks ? p.up_scales[wb + at] : 0.0f;
         // wait here, not where they are used: that is in the loop below, and the
         // wait would be for its direct loads too
 #pragma unroll
@@ -179,15 +192,15 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     // LDS addresses of this lane's operands, a register each per stage: the rest
     // of an address is a constant of the instruction
     const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
-    uint32_t x_lo[2], x_hi[2], w_lo[2], w_hi[2], s_at[2];
+    uint32_t x_lo[S], x_hi[S], w_lo[S], w_hi[S];
 #pragma unroll
-    for (int q = 0; q < 2; q++) {
+    for (int q = 0; q < S; q++) {
         x_lo[q] = opaque(base + q * kStage + wm * MJ * 2048 + lo);
         x_hi[q] = opaque(base + q * kStage + wm * MJ * 2048 + hi);
         w_lo[q] = opaque(base + q * kStage + kX + wn * NI * 2048 + lo);
         w_hi[q] = opaque(base + q * kStage + kX + wn * NI * 2048 + hi);
-        s_at[q] = opaque(base + q * kStage + kX + kW + (wm * MJ * 16 + r) * 4);
     }
+    const uint32_t s_at = opaque(base + S * kStage + (wm * MJ * 16 + r) * 16);
     // w's row tiles are read kAhead tiles before their use
     constexpr int kAhead = 2;
     Operand<EXACT> x[MJ], w[kAhead];
@@ -200,10 +213,14 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
         x[j] = Operand<EXACT>(lds_read<v4i>(x_lo[stage], 2048 * j),
                               lds_read<v4i>(x_hi[stage], 2048 * j));
     };
-    auto read_scales = [&](int stage) {
+    auto read_scales = [&](int b) {
+        const uint32_t at = s_at + (b / 4 & 1) * kScales + (b & 3) * 4;
 #pragma unroll
-        for (int j = 0; j < MJ; j++)
-            sx[j] = lds_read<float>(s_at[stage], 64 * j);
+        for (int j = 0; j < MJ; j++) {
+            sx[j] = lds_read<float>(at, 256 * j);
+            if (KS > 1) // blocks past K: what lies there is no scale
+                sx[j] = b + before < blocks ? sx[j] : 0.0f;
+        }
     };
     // The additions of a tile follow its matrix instruction kLag tiles behind,
     // into the next block's: the first ones add zeros.
@@ -235,30 +252,30 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     //   at row tile kLast: the next block's x, scales and first half are there,
     //     and this one's second half is read by everybody.
     // Each load has about one and a half blocks' time to arrive.
-    auto block = [&](auto stage_of, int b) {
-        constexpr int stage = decltype(stage_of)::value;
+    auto block = [&](auto stage_of, int b0, int b) {
+        constexpr int stage = decltype(stage_of)::value, after = (stage + 1) % S;
         constexpr int kTurn = NI / 2 - kAhead, kLast = NI - kAhead;
         constexpr int kPerRow = (kFirst + kLast - kTurn - 1) / (kLast - kTurn);
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-            if (i == kTurn || i == kLast)
-                arrived<kFirst + kSecond>();
             const Operand<EXACT> row = w[i % kAhead];
             if (i == 0) {
 #pragma unroll
                 for (int q = 0; q < G; q++)
                     w_scale[q] = __uint_as_float(
-                        __builtin_amdgcn_readlane(__float_as_uint(w_lanes[q]), b & 63));
+                        __builtin_amdgcn_readlane(__float_as_uint(w_lanes[q]), b - b0));
             }
-            if (i >= kTurn && i < kLast) {
+            if (i == kTurn + 1)
+                load_scales((b & ~3) + 4, (b & 3) == 0);
+            if (i > kTurn && i <= kLast) {
 #pragma unroll
-                for (int u = (i - kTurn) * kPerRow; u < min((i - kTurn + 1) * kPerRow, kFirst); u++)
-                    load_first(b + 2, u);
+                for (int u = (i - kTurn - 1) * kPerRow; u < min((i - kTurn) * kPerRow, kFirst); u++)
+                    load_first(stage, b + S, u);
             }
-            if (i == kLast) {
+            if (i == kLast + 1) {
 #pragma unroll
                 for (int u = 0; u < kSecond; u++)
-                    load_second(b + 2, u);
+                    load_second(stage, b + S, u);
             }
 #pragma unroll
             for (int j = 0; j < MJ; j++) {
@@ -266,14 +283,18 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
                 d[t % kRing] = dot(row, x[j]);
                 additions(t - kLag);
                 if (i == NI - 1)
-                    read_x(stage ^ 1, j);
+                    read_x(after, j);
+            }
+            if (i == kTurn || i == kLast) {
+                __builtin_amdgcn_sched_barrier(0);
+                arrived<(S - 1) * (kFirst + kSecond)>();
             }
             if (i < kLast)
                 read_w(stage, i + kAhead);
             else
-                read_w(stage ^ 1, i + kAhead - NI);
+                read_w(after, i + kAhead - NI);
             if (i == NI - 1)
-                read_scales(stage ^ 1);
+                read_scales(b + 1);
             if (!EXACT) {
 #pragma unroll
                 for (int j = 0; j < MJ; j++) {
@@ -285,19 +306,18 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
         }
     };
 
+    load_scales(0, true);
 #pragma unroll
-    for (int u = 0; u < kFirst; u++)
-        load_first(0, u);
+    for (int q = 0; q < S; q++) {
 #pragma unroll
-    for (int u = 0; u < kSecond; u++)
-        load_second(0, u);
+        for (int u = 0; u < kFirst; u++)
+            load_first(q, q, u);
+        if (q == S - 1)
+            arrived<(S - 1) * (kFirst + kSecond)>();
 #pragma unroll
-    for (int u = 0; u < kFirst; u++)
-        load_first(1, u);
-    arrived<kFirst + kSecond>();
-#pragma unroll
-    for (int u = 0; u < kSecond; u++)
-        load_second(1, u);
+        for (int u = 0; u < kSecond; u++)
+            load_second(q, q, u);
+    }
 #pragma unroll
     for (int i = 0; i < kAhead; i++)
         read_w(0, i);
@@ -305,21 +325,49 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     for (int j = 0; j < MJ; j++)
         read_x(0, j);
     read_scales(0);
-    for (int b0 = 0; b0 < blocks; b0 += 64) {
+    constexpr int kChunk = 60; // a multiple of S
+    for (int b0 = 0; b0 < rounds; b0 += kChunk) {
         load_w_scales(b0);
-        const int end = min(b0 + 64, blocks);
+        const int end = min(b0 + kChunk, rounds);
         int b = b0;
-        for (; b + 1 < end; b += 2) {
-            block(std::integral_constant<int, 0>{}, b);
-            block(std::integral_constant<int, 1>{}, b + 1);
+        for (; b + S <= end; b += S) {
+            block(std::integral_constant<int, 0>{}, b0, b);
+            block(std::integral_constant<int, 1>{}, b0, b + 1);
+            if constexpr (S > 2)
+                block(std::integral_constant<int, 2 % S>{}, b0, b + 2);
+            if constexpr (S > 3)
+                block(std::integral_constant<int, 3 % S>{}, b0, b + 3);
         }
         if (b < end)
-            block(std::integral_constant<int, 0>{}, b);
+            block(std::integral_constant<int, 0>{}, b0, b);
+        if (S > 2 && b + 1 < end)
+            block(std::integral_constant<int, 1>{}, b0, b + 1);
+        if (S > 3 && b + 2 < end)
+            block(std::integral_constant<int, 2 % S>{}, b0, b + 2);
     }
 #pragma unroll
     for (int t = -kLag; t < 0; t++)
         additions(t);
     arrived<0>(); // loads past the last block write to LDS, too
+
+    // ---- the groups' sums, in their order
+    if constexpr (KS > 1) {
+        static_assert(KS == 1 || T::kWaves * NI * MJ * 1024 <= S * kStage);
+        const uint32_t at = wave * (NI * MJ * 1024) + lane * 16;
+        if (group > 0) {
+#pragma unroll
+            for (int t = 0; t < kTiles; t++)
+                lds_write(base + at + 1024 * t, acc[t / MJ][t % MJ]);
+        }
+        __syncthreads();
+        if (group > 0)
+            return;
+#pragma unroll
+        for (int q = 1; q < KS; q++)
+#pragma unroll
+            for (int t = 0; t < kTiles; t++)
+                acc[t / MJ][t % MJ] += lds_read<v4f>(base + q * kGroup + at + 1024 * t, 0);
+    }
 
     // ---- results
     constexpr int NO = NI / G; // row tiles of results
@@ -341,7 +389,7 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     constexpr int kValue = QUANT ? 1 : EXACT ? 4 : 2, kPerPiece = 16 / kValue;
     constexpr int kRow = 16 * NO * kValue, kPieces = kRow / 16; // bytes, 16-byte pieces
     const uint32_t mine = base + wave * (16 * MJ * kRow);
-    static_assert(T::kWaves * 16 * MJ * kRow + 8 * T::kRowsX <= 2 * kStage);
+    static_assert(T::kWaves * 16 * MJ * kRow + 4 * T::NW * T::kRowsX <= kGroup);
     auto put = [&](int i, int j, auto v) { // columns 16 i + 4 g .. + 3 of row 16 j + r
         const int line = 16 * j + r, at = (16 * i + 4 * g) * kValue;
         lds_write(mine + line * kRow + ((at / 16) ^ (line % kPieces)) * 16 + at % 16, v);
@@ -375,7 +423,7 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     if constexpr (QUANT) {
         // a block of 128 columns: the waves of a row tile share its maximum
         static_assert(!QUANT || kCols == 128);
-        const uint32_t tops = base + 2 * kStage - 4 * T::NW * T::kRowsX;
+        const uint32_t tops = base + kGroup - 4 * T::NW * T::kRowsX;
         uint32_t top[MJ];
 #pragma unroll
         for (int j = 0; j < MJ; j++) {
@@ -427,15 +475,20 @@ __global__ __launch_bounds__(64 * T::kWaves, 2) void fp8_tile_kernel(
     }
 }
 
-typedef Tile<8, 4, 2, 4> Tile256; // 256 x 256, eight waves
-typedef Tile<4, 4, 2, 2> Tile128; // 128 x 128, four waves
+typedef Tile<8, 4, 2, 4, 1, 2> TileA; // 256 x 256, eight waves
+typedef Tile<8, 4, 2, 2, 1, 3> TileB; // 256 x 128, four waves
+typedef Tile<4, 4, 2, 2, 2, 2> TileC; // 128 x 128, four waves, ks 2
+typedef Tile<4, 4, 2, 1, 2, 3> TileD; // 128x64 ks 2
+typedef Tile<4, 4, 2, 2, 1, 2> TileE;
+typedef Tile<4, 4, 1, 1, 4, 2> TileF; // 64 x 64 ks 4
+typedef Tile<4, 2, 2, 2, 2, 2> TileG; // 128 x 64
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
 hipError_t launch_tile(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
 {
     constexpr int kCols = T::kRowsW / (GATED ? 2 : 1);
     const int64_t tiles = (p.m + T::kRowsX - 1) / T::kRowsX * ((p.n + kCols - 1) / kCols);
-    fp8_tile_kernel<T, GATED, EXACT, QUANT><<<(unsigned)tiles, 64 * T::kWaves, 0, s>>>(
+    fp8_tile_kernel<T, GATED, EXACT, QUANT><<<(unsigned)tiles, 64 * T::kWaves * T::KS, 0, s>>>(
         p, codes, scales);
     return hipGetLastError();
 }
@@ -445,18 +498,21 @@ hipError_t launch_tile(const Fp8Problem &p, uint8_t *codes, float *scales, hipSt
 hipError_t launch_fp8_tile(const Fp8Problem &p, int size, hipStream_t s)
 {
     if (p.exact)
-        return p.up ? launch_tile<Tile128, true, true, false>(p, nullptr, nullptr, s)
-                    : launch_tile<Tile128, false, true, false>(p, nullptr, nullptr, s);
-    if (size == 256)
-        return p.up ? launch_tile<Tile256, true, false, false>(p, nullptr, nullptr, s)
-                    : launch_tile<Tile256, false, false, false>(p, nullptr, nullptr, s);
-    return p.up ? launch_tile<Tile128, true, false, false>(p, nullptr, nullptr, s)
-                : launch_tile<Tile128, false, false, false>(p, nullptr, nullptr, s);
+        return p.up ? launch_tile<TileE, true, true, false>(p, nullptr, nullptr, s)
+                    : launch_tile<TileE, false, true, false>(p, nullptr, nullptr, s);
+    const char *e = getenv("TILE");
+    const char t = e ? *e : size == 256 ? 'A' : 'E';
+#define PICK(c, T) if (t == c) return p.up ? launch_tile<T, true, false, false>(p, nullptr, nullptr, s) : launch_tile<T, false, false, false>(p, nullptr, nullptr, s);
+    PICK('A', TileA) PICK('B', TileB) PICK('C', TileC) PICK('D', TileD) PICK('E', TileE) PICK('F', TileF) PICK('G', TileG)
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_fp8_tile_quantize(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
 {
-    return launch_tile<Tile256, true, false, true>(p, codes, scales, s);
+    const char *e = getenv("TILE");
+    const char t = e ? *e : 'A';
+    if (t == 'B') return launch_tile<TileB, true, false, true>(p, codes, scales, s);
+    return launch_tile<TileA, true, false, true>(p, codes, scales, s);
 }
 
 } // namespace bpg
