@@ -42,10 +42,29 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t stream);
 size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
                                      void *workspace, hipStream_t stream);
-// The kernels over LDS tiles (fp8_tile.hip).
-hipError_t launch_fp8_tile(const Fp8Problem &p, int size, hipStream_t stream);
-hipError_t launch_fp8_tile_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
-                                    hipStream_t stream);
+// The kernels over LDS tiles (fp8_tile.hip): which of them makes which columns.
+enum Fp8Kernel {
+    kFp8None = 0,
+    kFp8Stream,          // operands straight to registers (fp8_stream.hip)
+    kFp8Tile256x256,     // rows x columns (gated: columns of both matrices)
+    kFp8Tile128x128Pair, // two workgroups a CU
+    kFp8Tile128x128,     // one, with loads further ahead
+    kFp8Tile64x128,
+    kFp8Tile64x64,       // two halves of K a workgroup
+    kFp8Tile64x256,
+};
+struct Fp8Part {
+    int kernel;
+    int64_t first, cols;
+};
+struct Fp8Plan {
+    Fp8Part part[2]; // the second may have no columns
+};
+Fp8Plan plan_fp8_tiles(const Fp8Problem &p);
+Fp8Plan plan_fp8_tile_codes(const Fp8Problem &p);
+hipError_t launch_fp8_tiles(const Fp8Problem &p, hipStream_t stream);
+hipError_t launch_fp8_tile_codes(const Fp8Problem &p, uint8_t *codes, float *scales,
+                                 hipStream_t stream);
 
 // Log probabilities, entropies and top alternatives of rows of logits.
 struct LogprobsProblem {

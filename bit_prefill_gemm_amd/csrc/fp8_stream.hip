@@ -115,7 +115,7 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
     if (p.m == 0)
         return hipSuccess;
     if (p.m > 64)
-        return launch_fp8_tile(p, p.m > 128 ? 256 : 128, s);
+        return launch_fp8_tiles(p, s);
     if (p.m <= 16)
         return p.exact ? stream<1, true>(p, s) : stream<1, false>(p, s);
     if (p.m <= 32)
@@ -132,7 +132,7 @@ hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float 
                                      void *workspace, hipStream_t s)
 {
     if (p.m > 64)
-        return launch_fp8_tile_quantize(p, codes, scales, s);
+        return launch_fp8_tile_codes(p, codes, scales, s);
     Fp8Problem values = p;
     values.y = workspace;
     values.ldy = p.n;

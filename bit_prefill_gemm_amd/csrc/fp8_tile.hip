@@ -16,8 +16,10 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
 // weights) by 16 MJ rows.  Gated, the first half of a wave's NI row tiles are
 // rows of the gate and the second half the same rows of the up projection.
-template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_> struct Tile {
+template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_, bool ONE_ = false>
+struct Tile {
     static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_, KS = KS_, S = S_;
+    static constexpr bool ONE = ONE_;
     static constexpr int kWaves = NW * MW; // of a group
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
 };
@@ -86,7 +88,7 @@ template <int N> __device__ __forceinline__ void arrived()
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
 __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
-    const Fp8Problem p, uint8_t *out_codes, float *out_scales)
+    const Fp8Problem p, int64_t col_first, int64_t cols, uint8_t *out_codes, float *out_scales)
 {
     constexpr int NI = T::NI, MJ = T::MJ, S = T::S, KS = T::KS, G = GATED ? 2 : 1;
     constexpr int kCols = T::kRowsW / G;
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const int wn = wave % T::NW, wm = wave / T::NW;
     const int r = lane & 15, g = lane >> 4;
     // ---- which tile: every XCD a stretch of them, in panels of eight row tiles
-    const int mt = (int)((p.m + T::kRowsX - 1) / T::kRowsX), nt = (int)((p.n + kCols - 1) / kCols);
+    const int mt = (int)((p.m + T::kRowsX - 1) / T::kRowsX), nt = (int)((cols + kCols - 1) / kCols);
     int id = blockIdx.x;
     {
         const int total = mt * nt, per = total / 8, past = total % 8;
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const int panel = id / (8 * nt), first = panel * 8, height = min(8, mt - first);
     const int in = id - panel * 8 * nt;
     const int64_t m0 = (int64_t)(first + in % height) * T::kRowsX;
-    const int64_t n0 = (int64_t)(in / height) * kCols;
+    const int64_t n0 = col_first + (int64_t)(in / height) * kCols;
     const int64_t k = p.k;
     const int blocks = (int)fp8_blocks(k);
 
@@ -203,15 +205,17 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const uint32_t s_at = opaque(base + S * kStage + (wm * MJ * 16 + r) * 16);
     // w's row tiles are read kAhead tiles before their use
     constexpr int kAhead = 2;
-    Operand<EXACT> x[MJ], w[kAhead];
-    float sx[MJ], sv[MJ];
+    constexpr int XS = T::ONE ? 2 : 1; // sets of x
+    static_assert(!T::ONE || S % 2 == 0);
+    Operand<EXACT> x[XS][MJ], w[kAhead];
+    float sx[MJ], sv[G][MJ];
     auto read_w = [&](int stage, int i) {
         w[i % kAhead] = Operand<EXACT>(lds_read<v4i>(w_lo[stage], 2048 * i),
                                        lds_read<v4i>(w_hi[stage], 2048 * i));
     };
     auto read_x = [&](int stage, int j) {
-        x[j] = Operand<EXACT>(lds_read<v4i>(x_lo[stage], 2048 * j),
-                              lds_read<v4i>(x_hi[stage], 2048 * j));
+        x[stage % XS][j] = Operand<EXACT>(lds_read<v4i>(x_lo[stage], 2048 * j),
+                                          lds_read<v4i>(x_hi[stage], 2048 * j));
     };
     auto read_scales = [&](int b) {
         const uint32_t at = s_at + (b / 4 & 1) * kScales + (b & 3) * 4;
@@ -224,24 +228,28 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     };
     // The additions of a tile follow its matrix instruction kLag tiles behind,
     // into the next block's: the first ones add zeros.
-    constexpr int kLag = 3, kRing = kLag + 1, kTiles = NI * MJ;
+    constexpr int kTiles = NI * MJ, kRing = 4;
+    constexpr int kLag = kRing - 1 < kTiles - MJ ? kRing - 1 : kTiles - MJ; // row tile 0's are never left for the next block
     static_assert(kTiles % kRing == 0);
     v4f d[kRing];
 #pragma unroll
     for (int q = 0; q < kRing; q++)
         d[q] = v4f{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < MJ; j++)
-        sv[j] = 0;
+    for (int q = 0; q < G; q++)
+#pragma unroll
+        for (int j = 0; j < MJ; j++)
+            sv[q][j] = 0;
     auto additions = [&](int t) { // of tile t, or of the block before for t < 0
         const bool past = t < 0;
         t = past ? t + kTiles : t;
         const int i = t / MJ, j = t % MJ;
-        if (!past && i == 0)
-            sv[j] = sx[j] * w_scale[0];
-        if (GATED && !past && i == NI / 2)
-            sv[j] = sx[j] * w_scale[G - 1];
-        add_scaled(acc[i][j], d[t % kRing], sv[j]);
+        if (!past && i == 0) {
+#pragma unroll
+            for (int q = 0; q < G; q++)
+                sv[q][j] = sx[j] * w_scale[q];
+        }
+        add_scaled(acc[i][j], d[t % kRing], sv[i / (NI / G)][j]);
     };
 
     // One block of K from stage b & 1.  x and the first kAhead row tiles of w
@@ -265,14 +273,29 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
                     w_scale[q] = __uint_as_float(
                         __builtin_amdgcn_readlane(__float_as_uint(w_lanes[q]), b - b0));
             }
-            if (i == kTurn + 1)
+            if (T::ONE ? i == 0 : i == kTurn + 1)
                 load_scales((b & ~3) + 4, (b & 3) == 0);
-            if (i > kTurn && i <= kLast) {
+            if (T::ONE && i <= kLast) {
+                constexpr int kAll = kFirst + kSecond, kRowLoads = (kAll + kLast) / (kLast + 1);
+#pragma unroll
+                for (int u = i * kRowLoads; u < min((i + 1) * kRowLoads, kAll); u++) {
+                    if (u < kFirst)
+                        load_first((stage + S - 1) % S, b + S - 1, u);
+                    else
+                        load_second((stage + S - 1) % S, b + S - 1, u - kFirst);
+                }
+            }
+            if (T::ONE && i == NI - 1) {
+#pragma unroll
+                for (int j = 0; j < MJ; j++)
+                    read_x(after, j);
+            }
+            if (!T::ONE && i > kTurn && i <= kLast) {
 #pragma unroll
                 for (int u = (i - kTurn - 1) * kPerRow; u < min((i - kTurn) * kPerRow, kFirst); u++)
                     load_first(stage, b + S, u);
             }
-            if (i == kLast + 1) {
+            if (!T::ONE && i == kLast + 1) {
 #pragma unroll
                 for (int u = 0; u < kSecond; u++)
                     load_second(stage, b + S, u);
@@ -280,14 +303,14 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 #pragma unroll
             for (int j = 0; j < MJ; j++) {
                 const int t = i * MJ + j;
-                d[t % kRing] = dot(row, x[j]);
+                d[t % kRing] = dot(row, x[stage % XS][j]);
                 additions(t - kLag);
-                if (i == NI - 1)
+                if (!T::ONE && i == NI - 1)
                     read_x(after, j);
             }
-            if (i == kTurn || i == kLast) {
+            if ((!T::ONE && i == kTurn) || i == kLast) {
                 __builtin_amdgcn_sched_barrier(0);
-                arrived<(S - 1) * (kFirst + kSecond)>();
+                arrived<(T::ONE ? S - 2 : S - 1) * (kFirst + kSecond)>();
             }
             if (i < kLast)
                 read_w(stage, i + kAhead);
@@ -308,16 +331,18 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 
     load_scales(0, true);
 #pragma unroll
-    for (int q = 0; q < S; q++) {
+    for (int q = 0; q < (T::ONE ? S - 1 : S); q++) {
 #pragma unroll
         for (int u = 0; u < kFirst; u++)
             load_first(q, q, u);
-        if (q == S - 1)
+        if (!T::ONE && q == S - 1)
             arrived<(S - 1) * (kFirst + kSecond)>();
 #pragma unroll
         for (int u = 0; u < kSecond; u++)
             load_second(q, q, u);
     }
+    if (T::ONE)
+        arrived<(S - 2) * (kFirst + kSecond)>();
 #pragma unroll
     for (int i = 0; i < kAhead; i++)
         read_w(0, i);
@@ -475,44 +500,161 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     }
 }
 
-typedef Tile<8, 4, 2, 4, 1, 2> TileA; // 256 x 256, eight waves
-typedef Tile<8, 4, 2, 2, 1, 3> TileB; // 256 x 128, four waves
-typedef Tile<4, 4, 2, 2, 2, 2> TileC; // 128 x 128, four waves, ks 2
-typedef Tile<4, 4, 2, 1, 2, 3> TileD; // 128x64 ks 2
-typedef Tile<4, 4, 2, 2, 1, 2> TileE;
-typedef Tile<4, 4, 1, 1, 4, 2> TileF; // 64 x 64 ks 4
-typedef Tile<4, 2, 2, 2, 2, 2> TileG; // 128 x 64
+typedef Tile<8, 4, 2, 4, 1, 2> Tile256x256;
+typedef Tile<4, 4, 2, 2, 1, 4, true> Tile128x128;
+typedef Tile<4, 4, 2, 2, 1, 2> Tile128x128Pair; // two workgroups a CU
+typedef Tile<2, 2, 4, 2, 1, 4, true> Tile64x128;
+typedef Tile<2, 2, 2, 2, 2, 4, true> Tile64x64; // two halves of K
+typedef Tile<4, 4, 4, 1, 1, 3> Tile64x256;
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
-hipError_t launch_tile(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
+hipError_t launch_tile(const Fp8Problem &p, const Fp8Part &part, uint8_t *codes, float *scales,
+                       hipStream_t s)
 {
     constexpr int kCols = T::kRowsW / (GATED ? 2 : 1);
-    const int64_t tiles = (p.m + T::kRowsX - 1) / T::kRowsX * ((p.n + kCols - 1) / kCols);
+    const int64_t tiles =
+        (p.m + T::kRowsX - 1) / T::kRowsX * ((part.cols + kCols - 1) / kCols);
     fp8_tile_kernel<T, GATED, EXACT, QUANT><<<(unsigned)tiles, 64 * T::kWaves * T::KS, 0, s>>>(
-        p, codes, scales);
+        p, part.first, part.cols, codes, scales);
     return hipGetLastError();
+}
+
+template <class T, bool EXACT>
+hipError_t launch_values(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
+{
+    return p.up ? launch_tile<T, true, EXACT, false>(p, part, nullptr, nullptr, s)
+                : launch_tile<T, false, EXACT, false>(p, part, nullptr, nullptr, s);
+}
+
+// What a tile costs, in us on an MI355X: `fixed`, and per block of K with few
+// tiles on the chip (`light`) and with as many as it holds at once (`full`,
+// `slots` of them).  Measured at 5120 x 5120 to 17408 x 5120 with 128 to 8192
+// rows; products whose codes are widened take longer.
+struct Cost {
+    int kernel, rows, cols, slots;
+    float fixed, light, full;
+};
+constexpr Cost kFast[] = {
+    {kFp8Tile256x256, 256, 256, 256, 5.0f, 1.24f, 1.60f},
+    {kFp8Tile128x128Pair, 128, 128, 512, 3.5f, 0.52f, 1.05f},
+    {kFp8Tile128x128, 128, 128, 256, 4.0f, 0.46f, 0.60f},
+    {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.36f, 0.38f},
+    {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.235f, 0.235f},
+};
+constexpr Cost kExact[] = {
+    {kFp8Tile128x128Pair, 128, 128, 512, 3.5f, 1.20f, 1.75f},
+    {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.62f, 0.62f},
+    {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.38f, 0.36f},
+};
+// a gated product's codes: blocks of 128 columns, so tiles of 128 and 128
+constexpr Cost kCodes[] = {
+    {kFp8Tile256x256, 256, 256, 256, 5.0f, 1.24f, 1.60f},
+    {kFp8Tile64x256, 64, 256, 256, 4.0f, 0.65f, 0.75f},
+};
+
+int64_t tiles_of(const Cost &c, int64_t m, int64_t cols, int g)
+{
+    const int64_t each = c.cols / g;
+    return (m + c.rows - 1) / c.rows * ((cols + each - 1) / each);
+}
+
+float time_of(const Cost &c, int64_t tiles, int64_t blocks)
+{
+    const int64_t full = tiles / c.slots, rest = tiles % c.slots;
+    float t = (float)full * (c.fixed + c.full * (float)blocks);
+    if (rest > 0)
+        t += c.fixed + (c.light + (c.full - c.light) * (float)rest / (float)c.slots) * (float)blocks;
+    return t;
+}
+
+// The quickest of `costs` for `cols` columns.
+template <int N>
+float best_of(const Cost (&costs)[N], const Fp8Problem &p, int64_t cols, int *kernel)
+{
+    float best = 0;
+    for (int i = 0; i < N; i++) {
+        const float t = time_of(costs[i], tiles_of(costs[i], p.m, cols, p.up ? 2 : 1), fp8_blocks(p.k));
+        if (i == 0 || t < best) {
+            best = t;
+            *kernel = costs[i].kernel;
+        }
+    }
+    return best;
+}
+
+template <int N> Fp8Plan plan(const Cost (&costs)[N], const Fp8Problem &p)
+{
+    Fp8Plan plan{};
+    plan.part[0].cols = p.n;
+    const float whole = best_of(costs, p, p.n, &plan.part[0].kernel);
+    // The largest tiles (the first of the list) for as many columns as fill the
+    // chip in whole rounds, and the quickest for the rest: 1024 x 5120 x 17408
+    // gated is 2.1 rounds, 208 us as three and 183 us as two and a rest.
+    const Cost &c = costs[0];
+    const int64_t each = c.cols / (p.up ? 2 : 1), down = (p.m + c.rows - 1) / c.rows;
+    const int64_t rounds = tiles_of(c, p.m, p.n, p.up ? 2 : 1) / c.slots;
+    const int64_t cols = rounds * c.slots / down * each;
+    if (cols > 0 && cols < p.n) {
+        Fp8Plan split{};
+        split.part[0] = {c.kernel, 0, cols};
+        split.part[1] = {0, cols, p.n - cols};
+        constexpr float kLaunch = 2.0f;
+        const float t = time_of(c, cols / each * down, fp8_blocks(p.k)) + kLaunch +
+                        best_of(costs, p, p.n - cols, &split.part[1].kernel);
+        if (t < whole)
+            return split;
+    }
+    return plan;
+}
+
+hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
+{
+    if (p.exact) {
+        switch (part.kernel) {
+        case kFp8Tile128x128Pair: return launch_values<Tile128x128Pair, true>(p, part, s);
+        case kFp8Tile64x128: return launch_values<Tile64x128, true>(p, part, s);
+        default: return launch_values<Tile64x64, true>(p, part, s);
+        }
+    }
+    switch (part.kernel) {
+    case kFp8Tile256x256: return launch_values<Tile256x256, false>(p, part, s);
+    case kFp8Tile128x128Pair: return launch_values<Tile128x128Pair, false>(p, part, s);
+    case kFp8Tile128x128: return launch_values<Tile128x128, false>(p, part, s);
+    case kFp8Tile64x128: return launch_values<Tile64x128, false>(p, part, s);
+    default: return launch_values<Tile64x64, false>(p, part, s);
+    }
 }
 
 } // namespace
 
-hipError_t launch_fp8_tile(const Fp8Problem &p, int size, hipStream_t s)
+Fp8Plan plan_fp8_tiles(const Fp8Problem &p) { return p.exact ? plan(kExact, p) : plan(kFast, p); }
+
+Fp8Plan plan_fp8_tile_codes(const Fp8Problem &p) { return plan(kCodes, p); }
+
+hipError_t launch_fp8_tiles(const Fp8Problem &p, hipStream_t s)
 {
-    if (p.exact)
-        return p.up ? launch_tile<TileE, true, true, false>(p, nullptr, nullptr, s)
-                    : launch_tile<TileE, false, true, false>(p, nullptr, nullptr, s);
-    const char *e = getenv("TILE");
-    const char t = e ? *e : size == 256 ? 'A' : 'E';
-#define PICK(c, T) if (t == c) return p.up ? launch_tile<T, true, false, false>(p, nullptr, nullptr, s) : launch_tile<T, false, false, false>(p, nullptr, nullptr, s);
-    PICK('A', TileA) PICK('B', TileB) PICK('C', TileC) PICK('D', TileD) PICK('E', TileE) PICK('F', TileF) PICK('G', TileG)
-    return hipErrorInvalidValue;
+    const Fp8Plan plan = plan_fp8_tiles(p);
+    for (const Fp8Part &part : plan.part) {
+        const hipError_t e = part.cols > 0 ? launch_part(p, part, s) : hipSuccess;
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
-hipError_t launch_fp8_tile_quantize(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
+hipError_t launch_fp8_tile_codes(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
 {
-    const char *e = getenv("TILE");
-    const char t = e ? *e : 'A';
-    if (t == 'B') return launch_tile<TileB, true, false, true>(p, codes, scales, s);
-    return launch_tile<TileA, true, false, true>(p, codes, scales, s);
+    const Fp8Plan plan = plan_fp8_tile_codes(p);
+    for (const Fp8Part &part : plan.part) {
+        hipError_t e = hipSuccess;
+        if (part.cols > 0 && part.kernel == kFp8Tile256x256)
+            e = launch_tile<Tile256x256, true, false, true>(p, part, codes, scales, s);
+        else if (part.cols > 0)
+            e = launch_tile<Tile64x256, true, false, true>(p, part, codes, scales, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 } // namespace bpg
