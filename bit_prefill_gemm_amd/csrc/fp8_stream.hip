@@ -9,103 +9,174 @@
 #include "fp8.h"
 
 #include "epilogue.h"
+#include "fp8_lds.h"
 #include "fp8_mma.h"
 
 namespace bpg {
 namespace {
 
 constexpr int kWaves = 8;
+constexpr int kStreamRows = 32;
 
-template <int MT, bool GATED, bool EXACT>
+// XL: loads of 8 rows of x per block, so 8 XL rows at most.
+template <int XL, bool GATED> struct Ring {
+    static constexpr int G = GATED ? 2 : 1, MT = (XL + 1) / 2;
+    static constexpr int kLoads = 2 * G + XL;                // of 1 KiB, per block
+    static constexpr int kSlot = 2048 * (G + MT), kDepth = 2; // blocks on the way
+    static constexpr int kScales = 2 * 256 * MT;             // two times four blocks'
+    static constexpr int kWave = kDepth * kSlot + kScales;
+};
+
+template <int XL, bool GATED, bool EXACT>
 __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Problem p, bool vec)
 {
-    constexpr int G = GATED ? 2 : 1;
-    __shared__ v4f part[kWaves][G * MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    typedef Ring<XL, GATED> R;
+    constexpr int G = R::G, MT = R::MT, D = R::kDepth;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kWaves * R::kWave];
+    static_assert(G * MT * 1024 <= R::kWave);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
-    const int64_t blocks = fp8_blocks(p.k);
-    // rows past the end read the last one: their results are not stored
-    const int64_t wr = min(n0 + r, p.n - 1);
-    const uint8_t *w[G];
-    const float *ws[G];
-    w[0] = p.w + wr * p.k + 16 * g;
-    ws[0] = p.w_scales + n0 / kFp8Block * blocks;
-    if constexpr (GATED) {
-        w[1] = p.up + wr * p.k + 16 * g;
-        ws[1] = p.up_scales + n0 / kFp8Block * blocks;
-    }
-    const uint8_t *x[MT];
-    const float *xs[MT];
+    const int64_t k = p.k;
+    const int blocks = (int)fp8_blocks(k), per = (blocks + kWaves - 1) / kWaves;
+    const int first = min(wave * per, blocks), end = min(first + per, blocks);
+
+    const uint32_t base = lds_address(lds) + wave * R::kWave;
+    const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
+    const v4i w0 = buffer_of(p.w, n0, p.n, k, 16);
+    const v4i w1 = GATED ? buffer_of(p.up, n0, p.n, k, 16) : w0;
+    const v4i x = buffer_of(p.codes, m0, p.m, k, 8 * XL);
+    const v4i xs = buffer_of(p.scales, m0, p.m, (int64_t)blocks * 4, 8 * XL);
+    const uint32_t slane = (uint32_t)(lane * blocks) * 4;
+    auto load = [&](int slot, int b) {
+        const uint32_t to = base + slot * R::kSlot, at = (uint32_t)b * kFp8Block;
+        // pieces past K, and blocks past this wave's: zeros
+        const uint32_t l = b < end && at + piece < k ? lane_at : kPastBuffer;
 #pragma unroll
-    for (int j = 0; j < MT; j++) {
-        const int64_t row = min(m0 + 16 * j + r, p.m - 1);
-        x[j] = p.codes + row * p.k + 16 * g;
-        xs[j] = p.scales + row * blocks;
-    }
+        for (int u = 0; u < 2; u++) {
+            load16(w0, to + 1024 * u, l, (uint32_t)(8 * u * k) + at);
+            if constexpr (GATED)
+                load16(w1, to + 2048 + 1024 * u, l, (uint32_t)(8 * u * k) + at);
+        }
+#pragma unroll
+        for (int u = 0; u < XL; u++)
+            load16(x, to + 2048 * G + 1024 * u, l, (uint32_t)(8 * u * k) + at);
+    };
+    auto load_scales = [&](int c) { // of the wave's blocks 4 c .. 4 c + 3
+        load16_lanes((uint64_t)~0u >> (32 - 16 * MT), xs, base + D * R::kSlot + (c & 1) * 256 * MT, slane,
+                     (uint32_t)(first + 4 * c) * 4);
+    };
+    const int64_t wb = n0 / kFp8Block * blocks;
+    // scalar loads: vector ones would be counted with the direct loads
+    typedef const __attribute__((address_space(4))) float *Scalars;
+    const Scalars s0 = (Scalars)(p.w_scales + wb), s1 = (Scalars)(GATED ? p.up_scales + wb : p.w_scales);
+    float w_next[G];
+    auto w_scales = [&](int b) {
+        b = min(b, blocks - 1);
+        w_next[0] = s0[b];
+        if constexpr (GATED)
+            w_next[1] = s1[b];
+    };
+
     v4f acc[G][MT];
 #pragma unroll
     for (int i = 0; i < G; i++)
 #pragma unroll
         for (int j = 0; j < MT; j++)
             acc[i][j] = v4f{0, 0, 0, 0};
-    for (int64_t b = wave; b < blocks; b += kWaves) {
-        const int64_t at = b * kFp8Block;
-        // K is a multiple of 32, so 16 codes are all inside it or all outside
-        const bool lo = at + 16 * g < p.k, hi = at + 64 + 16 * g < p.k;
-        const v4i none{0, 0, 0, 0};
-        auto operand = [&](const uint8_t *row) {
-            return Operand<EXACT>(lo ? *reinterpret_cast<const v4i *>(row + at) : none,
-                                  hi ? *reinterpret_cast<const v4i *>(row + at + 64) : none);
+    const uint32_t lo = (uint32_t)(r * 128 + ((g ^ (r & 7)) * 16)), hi = lo ^ 64;
+    auto block = [&](int slot, int b) {
+        const uint32_t at = base + slot * R::kSlot, i = (uint32_t)(b - first);
+        auto operand = [&](uint32_t tile) {
+            return Operand<EXACT>(lds_read<v4i>(at + lo, tile), lds_read<v4i>(at + hi, tile));
         };
-        Operand<EXACT> a[G];
+        float sw[G], sx[MT];
 #pragma unroll
-        for (int i = 0; i < G; i++)
-            a[i] = operand(w[i]);
+        for (int q = 0; q < G; q++)
+            sw[q] = w_next[q];
+        w_scales(b + 1);
+        arrived<(D - 1) * R::kLoads>();
+        Operand<EXACT> a[G], c[MT];
+#pragma unroll
+        for (int q = 0; q < G; q++)
+            a[q] = operand(2048 * q);
 #pragma unroll
         for (int j = 0; j < MT; j++) {
-            const Operand<EXACT> c = operand(x[j]);
-            const float s = xs[j][b];
-#pragma unroll
-            for (int i = 0; i < G; i++)
-                add_scaled(acc[i][j], dot(a[i], c), s * ws[i][b]);
+            c[j] = operand(2048 * (G + j));
+            sx[j] = lds_read<float>(base + D * R::kSlot + (i / 4 & 1) * 256 * MT + (i & 3) * 4 + r * 16,
+                                    256 * j);
         }
+        read_done();
+        load(slot, b + D);
+        if ((i & 3) == 0)
+            load_scales((int)i / 4 + 1);
+#pragma unroll
+        for (int j = 0; j < MT; j++)
+#pragma unroll
+            for (int q = 0; q < G; q++)
+                add_scaled(acc[q][j], dot(a[q], c[j]), sx[j] * sw[q]);
+    };
+    load_scales(0);
+#pragma unroll
+    for (int q = 0; q < D; q++)
+        load(q, first + q);
+    w_scales(first);
+    static_assert(D == 2);
+    int b = first;
+    for (; b + 1 < end; b += 2) {
+        block(0, b);
+        block(1, b + 1);
     }
+    if (b < end)
+        block(0, b);
+    arrived<0>();
+
+    // ---- the waves' sums, in their order; this wave's LDS is its own until here
+    const uint32_t mine = base + lane * 16;
 #pragma unroll
     for (int i = 0; i < G; i++)
 #pragma unroll
         for (int j = 0; j < MT; j++)
-            part[wave][i * MT + j][lane] = acc[i][j];
+            lds_write(mine + 1024 * (i * MT + j), acc[i][j]);
     __syncthreads();
-    for (int j = wave; j < MT; j += kWaves) {
-        v4f sum[G];
+    if (wave >= MT)
+        return;
+    const int j = wave;
+    v4f sum[G];
 #pragma unroll
-        for (int i = 0; i < G; i++) {
-            sum[i] = part[0][i * MT + j][lane];
+    for (int i = 0; i < G; i++) {
+        const uint32_t at = lds_address(lds) + lane * 16 + 1024 * (i * MT + j);
+        sum[i] = lds_read<v4f>(at, 0);
 #pragma unroll
-            for (int u = 1; u < kWaves; u++)
-                sum[i] += part[u][i * MT + j][lane];
-        }
-        if constexpr (GATED) {
-            float t[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
-            ep_activate(p.act, t);
-            sum[0] = v4f{t[0], t[1], t[2], t[3]} * sum[G - 1];
-        }
-        const int64_t row = m0 + 16 * j + r, n = n0 + 4 * g;
-        if (row < p.m && n < p.n)
-            store4(p.y, p.y_bf16, vec, row * p.ldy + n, (int)min((int64_t)4, p.n - n), sum[0]);
+        for (int u = 1; u < kWaves; u++)
+            sum[i] += lds_read<v4f>(at, u * R::kWave);
     }
+    if constexpr (GATED) {
+        float t[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+        ep_activate(p.act, t);
+        sum[0] = v4f{t[0], t[1], t[2], t[3]} * sum[G - 1];
+    }
+    const int64_t row = m0 + 16 * j + r, n = n0 + 4 * g;
+    if (row < p.m && n < p.n)
+        store4(p.y, p.y_bf16, vec, row * p.ldy + n, (int)min((int64_t)4, p.n - n), sum[0]);
 }
 
-template <int MT, bool EXACT> hipError_t stream(const Fp8Problem &p, hipStream_t s)
+template <int XL, bool EXACT> hipError_t launch(const Fp8Problem &p, hipStream_t s)
 {
-    const dim3 grid((unsigned)((p.n + 15) / 16), (unsigned)((p.m + 16 * MT - 1) / (16 * MT)));
+    const dim3 grid((unsigned)((p.n + 15) / 16));
     const bool vec = vector_rows(p.y, p.ldy, p.y_bf16);
     if (p.up)
-        fp8_stream_kernel<MT, true, EXACT><<<grid, 64 * kWaves, 0, s>>>(p, vec);
+        fp8_stream_kernel<XL, true, EXACT><<<grid, 64 * kWaves, 0, s>>>(p, vec);
     else
-        fp8_stream_kernel<MT, false, EXACT><<<grid, 64 * kWaves, 0, s>>>(p, vec);
+        fp8_stream_kernel<XL, false, EXACT><<<grid, 64 * kWaves, 0, s>>>(p, vec);
     return hipGetLastError();
+}
+
+template <bool EXACT> hipError_t stream(const Fp8Problem &p, hipStream_t s)
+{
+    return p.m <= 8 ? launch<1, EXACT>(p, s) : p.m <= 16 ? launch<2, EXACT>(p, s) : launch<4, EXACT>(p, s);
 }
 
 } // namespace
@@ -114,24 +185,20 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
 {
     if (p.m == 0)
         return hipSuccess;
-    if (p.m > 64)
+    if (p.m > kStreamRows)
         return launch_fp8_tiles(p, s);
-    if (p.m <= 16)
-        return p.exact ? stream<1, true>(p, s) : stream<1, false>(p, s);
-    if (p.m <= 32)
-        return p.exact ? stream<2, true>(p, s) : stream<2, false>(p, s);
-    return p.exact ? stream<4, true>(p, s) : stream<4, false>(p, s);
+    return p.exact ? stream<true>(p, s) : stream<false>(p, s);
 }
 
 size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t)
 {
-    return m > 64 ? 0 : (size_t)m * (size_t)n * sizeof(float);
+    return m > kStreamRows ? 0 : (size_t)m * (size_t)n * sizeof(float);
 }
 
 hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
                                      void *workspace, hipStream_t s)
 {
-    if (p.m > 64)
+    if (p.m > kStreamRows)
         return launch_fp8_tile_codes(p, codes, scales, s);
     Fp8Problem values = p;
     values.y = workspace;

@@ -2,6 +2,7 @@
 #include "fp8.h"
 
 #include "epilogue.h"
+#include "fp8_lds.h"
 #include "fp8_mma.h"
 
 #include <cfloat>
@@ -10,7 +11,6 @@
 namespace bpg {
 namespace {
 
-typedef __attribute__((address_space(3))) void lds_void;
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
@@ -23,68 +23,6 @@ struct Tile {
     static constexpr int kWaves = NW * MW; // of a group
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
 };
-
-// [rows][row_bytes] from `row` on, `most` rows at most, as a buffer: reads past
-// its last row give zeros.
-__device__ __forceinline__ v4i rows_of(const void *at, int64_t row, int64_t rows, int64_t row_bytes,
-                                       int most)
-{
-    const int64_t first = min(row, rows - 1);
-    const int64_t left = max((int64_t)0, min(rows - row, (int64_t)most));
-    const uint64_t base = reinterpret_cast<uint64_t>(at) + (uint64_t)(first * row_bytes);
-    return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)base),
-               __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)),
-               __builtin_amdgcn_readfirstlane((int)(left * row_bytes)), 0x00020000};
-}
-
-// Direct loads of 16 bytes a lane, to LDS address to + 16 lane.
-// Written out so that the compiler, which cannot tell the stages
-// of one LDS array apart, waits for none of them before a read: the waits are
-// at the barriers (`arrived`).
-__device__ __forceinline__ void load16(v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(to), "v"(lane_at), "s"(from), "s"(at)
-                 : "memory");
-}
-
-// the same where `now`, else nothing (all lanes are on around it)
-__device__ __forceinline__ void load16_if(bool now, v4i from, uint32_t to, uint32_t lane_at, uint32_t at)
-{
-    const int lanes = __builtin_amdgcn_readfirstlane(now ? -1 : 0);
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
-                 "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
-                 :
-                 : "s"(to), "v"(lane_at), "s"(from), "s"(at), "s"(lanes)
-                 : "memory");
-}
-
-template <class V> __device__ __forceinline__ V lds_read(uint32_t at, int offset)
-{
-    typedef const __attribute__((address_space(3))) V *Ptr;
-    return *(Ptr)(at + offset);
-}
-
-template <class V> __device__ __forceinline__ void lds_write(uint32_t at, V v)
-{
-    typedef __attribute__((address_space(3))) V *Ptr;
-    *(Ptr)at = v;
-}
-
-// An integer that the optimizer cannot take apart.
-__device__ __forceinline__ uint32_t opaque(uint32_t x)
-{
-    asm("" : "+v"(x));
-    return x;
-}
-
-// All direct loads of this wave but the last N are in LDS, its own LDS reads
-// are done, and so are those of the other waves.
-template <int N> __device__ __forceinline__ void arrived()
-{
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
-}
 
 template <class T, bool GATED, bool EXACT, bool QUANT>
 __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
@@ -120,14 +58,13 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     //      l / 8: piece l % 8 of the row in LDS, which is piece (l % 8) ^ (l / 8)
     //      of the row in memory, so that the 16 rows that a quarter wave reads at
     //      one piece lie in different banks.
-    const uint32_t base =
-        (uint32_t) reinterpret_cast<uintptr_t>((lds_void *)lds) + group * kGroup;
+    const uint32_t base = lds_address(lds) + group * kGroup;
     const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
     const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
-    const v4i xs = rows_of(p.codes, m0, p.m, k, T::kRowsX);
-    const v4i ws = rows_of(p.w, n0, p.n, k, kCols);
-    const v4i us = GATED ? rows_of(p.up, n0, p.n, k, kCols) : ws;
-    const v4i ss = rows_of(p.scales, m0, p.m, (int64_t)blocks * 4, T::kRowsX);
+    const v4i xs = buffer_of(p.codes, m0, p.m, k, T::kRowsX);
+    const v4i ws = buffer_of(p.w, n0, p.n, k, kCols);
+    const v4i us = GATED ? buffer_of(p.up, n0, p.n, k, kCols) : ws;
+    const v4i ss = buffer_of(p.scales, m0, p.m, (int64_t)blocks * 4, T::kRowsX);
     // scales: 64 rows of 16 bytes an instruction, every fourth block
     constexpr int kScaleWaves = T::kRowsX / 64;
     static_assert(kScaleWaves <= T::kWaves);
@@ -148,7 +85,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     };
     // pieces past K are read from past the buffer: zeros
     auto lane_from = [&](int b) {
-        return at_of(b) + piece < k ? lane_at : 0x80000000u;
+        return at_of(b) + piece < k ? lane_at : kPastBuffer;
     };
     auto load_first = [&](int stage, int b, int u) {
         const uint32_t to = base + stage * kStage, l = lane_from(b);
@@ -160,7 +97,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
         }
     };
     auto load_scales = [&](int b, bool now) { // of blocks b..b+3
-        load16_if(now && wave < kScaleWaves, ss, base + S * kStage + (b / 4 & 1) * kScales + 1024 * wave,
+        load16_lanes(now && wave < kScaleWaves ? ~(uint64_t)0 : 0, ss, base + S * kStage + (b / 4 & 1) * kScales + 1024 * wave,
                   slane, (uint32_t)(b + before) * 4);
     };
     auto load_second = [&](int stage, int b, int u) {
@@ -310,7 +247,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
             }
             if ((!T::ONE && i == kTurn) || i == kLast) {
                 __builtin_amdgcn_sched_barrier(0);
-                arrived<(T::ONE ? S - 2 : S - 1) * (kFirst + kSecond)>();
+                arrived_all<(T::ONE ? S - 2 : S - 1) * (kFirst + kSecond)>();
             }
             if (i < kLast)
                 read_w(stage, i + kAhead);
@@ -336,13 +273,13 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
         for (int u = 0; u < kFirst; u++)
             load_first(q, q, u);
         if (!T::ONE && q == S - 1)
-            arrived<(S - 1) * (kFirst + kSecond)>();
+            arrived_all<(S - 1) * (kFirst + kSecond)>();
 #pragma unroll
         for (int u = 0; u < kSecond; u++)
             load_second(q, q, u);
     }
     if (T::ONE)
-        arrived<(S - 2) * (kFirst + kSecond)>();
+        arrived_all<(S - 2) * (kFirst + kSecond)>();
 #pragma unroll
     for (int i = 0; i < kAhead; i++)
         read_w(0, i);
@@ -373,7 +310,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 #pragma unroll
     for (int t = -kLag; t < 0; t++)
         additions(t);
-    arrived<0>(); // loads past the last block write to LDS, too
+    arrived_all<0>(); // loads past the last block write to LDS, too
 
     // ---- the groups' sums, in their order
     if constexpr (KS > 1) {
