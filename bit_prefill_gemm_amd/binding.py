@@ -32,7 +32,8 @@ ENTRY_POINTS = ("bpg_status_str", "rotate_pack_weights_bytes", "rotate_pack_weig
                 "w4a4_grouped_gemm_kernel_name", "rmsnorm_quantize_act", "dequantize_act",
                 "w4a4_gemm_epilogue", "w4a4_gemm_epilogue_kernel_name", "moe_route_topk",
                 "quantize_fp8", "fp8_gemm", "fp8_gemm_gated", "fp8_gemm_gated_quantize_bytes",
-                "fp8_gemm_gated_quantize", "token_logprobs_bytes", "token_logprobs")
+                "fp8_gemm_gated_quantize", "fp8_gemm_kernel_name",
+                "fp8_gemm_gated_quantize_kernel_name", "token_logprobs_bytes", "token_logprobs")
 
 
 class WeightsDesc(ctypes.Structure):
@@ -144,6 +145,10 @@ def _lib_handle():
     lib.fp8_gemm_gated_quantize.restype = _int
     lib.fp8_gemm_gated_quantize.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int,
                                             _vp, _vp, _vp, _size, _vp]
+    lib.fp8_gemm_kernel_name.restype = ctypes.c_char_p
+    lib.fp8_gemm_kernel_name.argtypes = [_i64, _i64, _i64, _int, _int]
+    lib.fp8_gemm_gated_quantize_kernel_name.restype = ctypes.c_char_p
+    lib.fp8_gemm_gated_quantize_kernel_name.argtypes = [_i64, _i64, _i64]
     lib.token_logprobs_bytes.restype = _size
     lib.token_logprobs_bytes.argtypes = [_i64, _i64, _i64]
     lib.token_logprobs.restype = _int
@@ -782,6 +787,24 @@ def fp8_gemm_gated_quantize(codes, scales, gate: Fp8Weights, up: Fp8Weights,
                    gate.scales, up.codes, up.scales, activation, out_codes, out_scales)
     return call(codes, scales, gate.codes, gate.scales, up.codes, up.scales, activation, out_codes,
                 out_scales)
+
+
+def fp8_gemm_kernel_name(m: int, n: int, k: int, dtype=None, gated: bool = False) -> str:
+    """The kernel that makes the first columns of fp8_gemm's (or fp8_gemm_gated's) result (host
+    only); dtype: torch.float32 unless given."""
+    dt = X_BF16 if dtype is not None and dtype == _torch().bfloat16 else X_F32
+    r = _lib_handle().fp8_gemm_kernel_name(m, n, k, dt, int(gated))
+    if r is None:
+        raise ValueError("fp8_gemm_kernel_name: invalid sizes")
+    return r.decode()
+
+
+def fp8_gemm_gated_quantize_kernel_name(m: int, f: int, k: int) -> str:
+    """The kernel that makes the first columns of fp8_gemm_gated_quantize's result (host only)."""
+    r = _lib_handle().fp8_gemm_gated_quantize_kernel_name(m, f, k)
+    if r is None:
+        raise ValueError("fp8_gemm_gated_quantize_kernel_name: invalid sizes")
+    return r.decode()
 
 
 # ------------------------------------------------------------------ what a head's logits say

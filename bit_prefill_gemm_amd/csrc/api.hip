@@ -855,13 +855,30 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 bool act_ok(bpg_activation act) { return act >= BPG_ACT_NONE && act <= BPG_ACT_GELU_TANH; }
 
+bool fp8_shape(int64_t m, int64_t n, int64_t k)
+{
+    return m >= 0 && m <= kMaxFp8Rows && n >= 1 && n <= kMaxFp8Rows && k >= 1 && k % 32 == 0 &&
+           k <= kMaxGemmK;
+}
+
+// what a plan goes by (no pointer is followed)
+bpg::Fp8Problem shape_problem(int64_t m, int64_t n, int64_t k, bool gated)
+{
+    static const uint8_t any = 0;
+    bpg::Fp8Problem p{};
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.up = gated ? &any : nullptr;
+    return p;
+}
+
 // up_codes, up_scales: the second matrix (gated), else null
 bpg_status check_fp8(const void *codes, const float *scales, int64_t m, const void *w_codes,
                      const float *w_scales, bool gated, const void *up_codes,
                      const float *up_scales, int64_t n, int64_t k)
 {
-    if (m < 0 || m > kMaxFp8Rows || n < 1 || n > kMaxFp8Rows || k < 1 || k % 32 != 0 ||
-        k > kMaxGemmK)
+    if (!fp8_shape(m, n, k))
         return BPG_ERR_SHAPE;
     if (!w_codes || !w_scales || (gated && (!up_codes || !up_scales)) ||
         (m > 0 && (!codes || !scales)))
@@ -966,9 +983,26 @@ bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
 
 size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k)
 {
-    if (m < 0 || m > kMaxFp8Rows || f < 1 || f > kMaxFp8Rows || k < 1)
+    if (!fp8_shape(m, f, k) || f % 32 != 0)
         return 0;
-    return bpg::fp8_gated_quantize_bytes(m, f, k);
+    return bpg::fp8_gated_quantize_bytes(shape_problem(m, f, k, true));
+}
+
+const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt, int gated)
+{
+    if (!fp8_shape(m, n, k) || !dtype_ok(y_dt))
+        return nullptr;
+    bpg::Fp8Problem p = shape_problem(m, n, k, gated != 0);
+    p.y_bf16 = y_dt == BPG_X_BF16;
+    p.exact = !p.y_bf16;
+    return bpg::fp8_kernel_name(bpg::plan_fp8_gemm(p).part[0].kernel);
+}
+
+const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
+{
+    if (!fp8_shape(m, f, k) || f % 32 != 0)
+        return nullptr;
+    return bpg::fp8_kernel_name(bpg::plan_fp8_codes(shape_problem(m, f, k, true)).part[0].kernel);
 }
 
 bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64_t m,
@@ -986,7 +1020,7 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
         return s;
     if (f % 32 != 0 || m * bpg::fp8_blocks(f) >= ((int64_t)1 << 31))
         return BPG_ERR_SHAPE;
-    const size_t need = m > 0 ? bpg::fp8_gated_quantize_bytes(m, f, k) : 0;
+    const size_t need = fp8_gemm_gated_quantize_bytes(m, f, k);
     if (m > 0 && (!out_codes || !out_scales || (need > 0 && !workspace)))
         return BPG_ERR_NULL;
     if (!aligned16(out_codes) || !aligned4(out_scales) || !aligned16(workspace))

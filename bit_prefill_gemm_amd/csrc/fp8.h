@@ -38,20 +38,22 @@ struct Fp8Problem {
 };
 hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t stream);
 // The gated product (p.y, ldy, y_bf16 unused) as codes [m][n] and scales
-// [m][blocks of n]; workspace: fp8_gated_quantize_bytes(m, n, k) bytes.
-size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t k);
+// [m][blocks of n]; workspace: fp8_gated_quantize_bytes(p) bytes.
+size_t fp8_gated_quantize_bytes(const Fp8Problem &p);
 hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
                                      void *workspace, hipStream_t stream);
-// The kernels over LDS tiles (fp8_tile.hip): which of them makes which columns.
+
+// Which kernels make which columns, from the shape alone (fp8_tile.hip); the
+// launches above go by it.
 enum Fp8Kernel {
     kFp8None = 0,
-    kFp8Stream,          // operands straight to registers (fp8_stream.hip)
+    kFp8Stream,          // few rows: each wave streams its part of K (fp8_stream.hip)
     kFp8Tile256x256,     // rows x columns (gated: columns of both matrices)
     kFp8Tile128x128Pair, // two workgroups a CU
     kFp8Tile128x128,     // one, with loads further ahead
     kFp8Tile64x128,
     kFp8Tile64x64,       // two halves of K a workgroup
-    kFp8Tile64x256,
+    kFp8Tile64x256,      // a gated product's codes
 };
 struct Fp8Part {
     int kernel;
@@ -59,12 +61,14 @@ struct Fp8Part {
 };
 struct Fp8Plan {
     Fp8Part part[2]; // the second may have no columns
+    bool staged;     // fp32 values in a workspace, quantized behind it
 };
-Fp8Plan plan_fp8_tiles(const Fp8Problem &p);
-Fp8Plan plan_fp8_tile_codes(const Fp8Problem &p);
-hipError_t launch_fp8_tiles(const Fp8Problem &p, hipStream_t stream);
-hipError_t launch_fp8_tile_codes(const Fp8Problem &p, uint8_t *codes, float *scales,
-                                 hipStream_t stream);
+Fp8Plan plan_fp8_gemm(const Fp8Problem &p);
+Fp8Plan plan_fp8_codes(const Fp8Problem &p);
+const char *fp8_kernel_name(int kernel);
+
+constexpr int kFp8StreamRows = 32; // at most
+hipError_t launch_fp8_stream(const Fp8Problem &p, hipStream_t stream);
 
 // Log probabilities, entropies and top alternatives of rows of logits.
 struct LogprobsProblem {

@@ -16,7 +16,6 @@ namespace bpg {
 namespace {
 
 constexpr int kWaves = 8;
-constexpr int kStreamRows = 32;
 
 // XL: loads of 8 rows of x per block, so 8 XL rows at most.
 template <int XL, bool GATED> struct Ring {
@@ -181,32 +180,9 @@ template <bool EXACT> hipError_t stream(const Fp8Problem &p, hipStream_t s)
 
 } // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
+hipError_t launch_fp8_stream(const Fp8Problem &p, hipStream_t s)
 {
-    if (p.m == 0)
-        return hipSuccess;
-    if (p.m > kStreamRows)
-        return launch_fp8_tiles(p, s);
     return p.exact ? stream<true>(p, s) : stream<false>(p, s);
-}
-
-size_t fp8_gated_quantize_bytes(int64_t m, int64_t n, int64_t)
-{
-    return m > kStreamRows ? 0 : (size_t)m * (size_t)n * sizeof(float);
-}
-
-hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
-                                     void *workspace, hipStream_t s)
-{
-    if (p.m > kStreamRows)
-        return launch_fp8_tile_codes(p, codes, scales, s);
-    Fp8Problem values = p;
-    values.y = workspace;
-    values.ldy = p.n;
-    const hipError_t e = launch_fp8_gemm(values, s);
-    if (e != hipSuccess)
-        return e;
-    return launch_fp8_quantize(workspace, false, p.m, p.n, p.n, false, codes, scales, s);
 }
 
 } // namespace bpg

@@ -24,7 +24,10 @@ struct Tile {
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
 };
 
-template <class T, bool GATED, bool EXACT, bool QUANT>
+// What a tile's results are stored as.
+enum Store { kBf16, kF32, kCodes };
+
+template <class T, bool GATED, bool EXACT, Store STORE>
 __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const Fp8Problem p, int64_t col_first, int64_t cols, uint8_t *out_codes, float *out_scales)
 {
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     // a lane of whole rows: straight from the registers it would be 32 bytes of
     // each of 16 rows.  The 16-byte pieces of a row are stored in the order
     // piece ^ row, as above.
-    constexpr int kValue = QUANT ? 1 : EXACT ? 4 : 2, kPerPiece = 16 / kValue;
+    constexpr int kValue = STORE == kCodes ? 1 : STORE == kF32 ? 4 : 2, kPerPiece = 16 / kValue;
     constexpr int kRow = 16 * NO * kValue, kPieces = kRow / 16; // bytes, 16-byte pieces
     const uint32_t mine = base + wave * (16 * MJ * kRow);
     static_assert(T::kWaves * 16 * MJ * kRow + 4 * T::NW * T::kRowsX <= kGroup);
@@ -382,9 +385,9 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
             }
         }
     };
-    if constexpr (QUANT) {
+    if constexpr (STORE == kCodes) {
         // a block of 128 columns: the waves of a row tile share its maximum
-        static_assert(!QUANT || kCols == 128);
+        static_assert(STORE != kCodes || (kCols == 128 && KS == 1));
         const uint32_t tops = base + kGroup - 4 * T::NW * T::kRowsX;
         uint32_t top[MJ];
 #pragma unroll
@@ -427,7 +430,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 #pragma unroll
             for (int i = 0; i < NO; i++) {
                 const v4f v = acc[i][j];
-                if constexpr (EXACT)
+                if constexpr (STORE == kF32)
                     put(i, j, v);
                 else
                     put(i, j, v2u{bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
@@ -444,14 +447,14 @@ typedef Tile<2, 2, 4, 2, 1, 4, true> Tile64x128;
 typedef Tile<2, 2, 2, 2, 2, 4, true> Tile64x64; // two halves of K
 typedef Tile<4, 4, 4, 1, 1, 3> Tile64x256;
 
-template <class T, bool GATED, bool EXACT, bool QUANT>
+template <class T, bool GATED, bool EXACT, Store STORE>
 hipError_t launch_tile(const Fp8Problem &p, const Fp8Part &part, uint8_t *codes, float *scales,
                        hipStream_t s)
 {
     constexpr int kCols = T::kRowsW / (GATED ? 2 : 1);
     const int64_t tiles =
         (p.m + T::kRowsX - 1) / T::kRowsX * ((part.cols + kCols - 1) / kCols);
-    fp8_tile_kernel<T, GATED, EXACT, QUANT><<<(unsigned)tiles, 64 * T::kWaves * T::KS, 0, s>>>(
+    fp8_tile_kernel<T, GATED, EXACT, STORE><<<(unsigned)tiles, 64 * T::kWaves * T::KS, 0, s>>>(
         p, part.first, part.cols, codes, scales);
     return hipGetLastError();
 }
@@ -459,8 +462,9 @@ hipError_t launch_tile(const Fp8Problem &p, const Fp8Part &part, uint8_t *codes,
 template <class T, bool EXACT>
 hipError_t launch_values(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
 {
-    return p.up ? launch_tile<T, true, EXACT, false>(p, part, nullptr, nullptr, s)
-                : launch_tile<T, false, EXACT, false>(p, part, nullptr, nullptr, s);
+    constexpr Store STORE = EXACT ? kF32 : kBf16;
+    return p.up ? launch_tile<T, true, EXACT, STORE>(p, part, nullptr, nullptr, s)
+                : launch_tile<T, false, EXACT, STORE>(p, part, nullptr, nullptr, s);
 }
 
 // What a tile costs, in us on an MI355X: `fixed`, and per block of K with few
@@ -474,20 +478,26 @@ struct Cost {
 constexpr Cost kFast[] = {
     {kFp8Tile256x256, 256, 256, 256, 5.0f, 1.24f, 1.60f},
     {kFp8Tile128x128Pair, 128, 128, 512, 3.5f, 0.52f, 1.05f},
-    {kFp8Tile128x128, 128, 128, 256, 4.0f, 0.46f, 0.60f},
-    {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.36f, 0.38f},
-    {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.235f, 0.235f},
+    {kFp8Tile128x128, 128, 128, 256, 4.0f, 0.46f, 0.75f},
+    {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.36f, 0.46f},
+    {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.25f, 0.30f},
 };
 constexpr Cost kExact[] = {
     {kFp8Tile128x128Pair, 128, 128, 512, 3.5f, 1.20f, 1.75f},
     {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.62f, 0.62f},
     {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.38f, 0.36f},
 };
-// a gated product's codes: blocks of 128 columns, so tiles of 128 and 128
-constexpr Cost kCodes[] = {
+// a gated product's codes: blocks of 128 columns, so tiles of 128 and 128 ...
+constexpr Cost kToCodes[] = {
     {kFp8Tile256x256, 256, 256, 256, 5.0f, 1.24f, 1.60f},
     {kFp8Tile64x256, 64, 256, 256, 4.0f, 0.65f, 0.75f},
 };
+// ... or fp32 values in smaller ones, quantized by another launch
+constexpr Cost kStaged[] = {
+    {kFp8Tile64x128, 64, 128, 256, 3.0f, 0.36f, 0.46f},
+    {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.25f, 0.30f},
+};
+constexpr float kLaunch = 2.0f; // another launch behind one
 
 int64_t tiles_of(const Cost &c, int64_t m, int64_t cols, int g)
 {
@@ -504,7 +514,7 @@ float time_of(const Cost &c, int64_t tiles, int64_t blocks)
     return t;
 }
 
-// The quickest of `costs` for `cols` columns.
+// The quickest of `costs` for `cols` columns, and its time.
 template <int N>
 float best_of(const Cost (&costs)[N], const Fp8Problem &p, int64_t cols, int *kernel)
 {
@@ -519,14 +529,14 @@ float best_of(const Cost (&costs)[N], const Fp8Problem &p, int64_t cols, int *ke
     return best;
 }
 
-template <int N> Fp8Plan plan(const Cost (&costs)[N], const Fp8Problem &p)
+template <int N> float plan(const Cost (&costs)[N], const Fp8Problem &p, Fp8Plan *plan)
 {
-    Fp8Plan plan{};
-    plan.part[0].cols = p.n;
-    const float whole = best_of(costs, p, p.n, &plan.part[0].kernel);
+    *plan = Fp8Plan{};
+    plan->part[0].cols = p.n;
+    const float whole = best_of(costs, p, p.n, &plan->part[0].kernel);
     // The largest tiles (the first of the list) for as many columns as fill the
     // chip in whole rounds, and the quickest for the rest: 1024 x 5120 x 17408
-    // gated is 2.1 rounds, 208 us as three and 183 us as two and a rest.
+    // gated is 2.1 rounds, 208 us as three and 192 us as two and a rest.
     const Cost &c = costs[0];
     const int64_t each = c.cols / (p.up ? 2 : 1), down = (p.m + c.rows - 1) / c.rows;
     const int64_t rounds = tiles_of(c, p.m, p.n, p.up ? 2 : 1) / c.slots;
@@ -535,13 +545,14 @@ template <int N> Fp8Plan plan(const Cost (&costs)[N], const Fp8Problem &p)
         Fp8Plan split{};
         split.part[0] = {c.kernel, 0, cols};
         split.part[1] = {0, cols, p.n - cols};
-        constexpr float kLaunch = 2.0f;
         const float t = time_of(c, cols / each * down, fp8_blocks(p.k)) + kLaunch +
                         best_of(costs, p, p.n - cols, &split.part[1].kernel);
-        if (t < whole)
-            return split;
+        if (t < whole) {
+            *plan = split;
+            return t;
+        }
     }
-    return plan;
+    return whole;
 }
 
 hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
@@ -553,6 +564,11 @@ hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
         default: return launch_values<Tile64x64, true>(p, part, s);
         }
     }
+    if (!p.y_bf16) { // the values of a staged gated product
+        return part.kernel == kFp8Tile64x128
+                   ? launch_tile<Tile64x128, true, false, kF32>(p, part, nullptr, nullptr, s)
+                   : launch_tile<Tile64x64, true, false, kF32>(p, part, nullptr, nullptr, s);
+    }
     switch (part.kernel) {
     case kFp8Tile256x256: return launch_values<Tile256x256, false>(p, part, s);
     case kFp8Tile128x128Pair: return launch_values<Tile128x128Pair, false>(p, part, s);
@@ -562,32 +578,115 @@ hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
     }
 }
 
+// Few rows, and few enough columns for a workgroup per 16 of them: 32 rows x
+// 5120 take 11.9 us either way, x 1024 6.7 (tiles 11.9), x 17408 34 (tiles 27).
+bool streams(const Fp8Problem &p)
+{
+    return p.m <= 16 || (p.m <= kFp8StreamRows && p.n * (p.up ? 2 : 1) <= 8192);
+}
+
+Fp8Plan streamed(const Fp8Problem &p)
+{
+    Fp8Plan plan{};
+    plan.part[0] = {kFp8Stream, 0, p.n};
+    return plan;
+}
+
 } // namespace
 
-Fp8Plan plan_fp8_tiles(const Fp8Problem &p) { return p.exact ? plan(kExact, p) : plan(kFast, p); }
-
-Fp8Plan plan_fp8_tile_codes(const Fp8Problem &p) { return plan(kCodes, p); }
-
-hipError_t launch_fp8_tiles(const Fp8Problem &p, hipStream_t s)
+Fp8Plan plan_fp8_gemm(const Fp8Problem &p)
 {
-    const Fp8Plan plan = plan_fp8_tiles(p);
+    if (p.m == 0)
+        return Fp8Plan{};
+    if (streams(p))
+        return streamed(p);
+    Fp8Plan values;
+    if (p.exact)
+        plan(kExact, p, &values);
+    else
+        plan(kFast, p, &values);
+    return values;
+}
+
+Fp8Plan plan_fp8_codes(const Fp8Problem &p)
+{
+    if (p.m == 0)
+        return Fp8Plan{};
+    Fp8Plan codes, values{};
+    if (streams(p)) {
+        values = streamed(p);
+        values.staged = true;
+        return values;
+    }
+    const float direct = plan(kToCodes, p, &codes);
+    // the values are written and read by the quantizer's launch, at 4 TB/s
+    values.staged = true;
+    values.part[0].cols = p.n;
+    const float staged = best_of(kStaged, p, p.n, &values.part[0].kernel) + kLaunch +
+                         (float)(p.m * p.n) * (9.0f / 4e6f);
+    return staged < direct ? values : codes;
+}
+
+const char *fp8_kernel_name(int kernel)
+{
+    switch (kernel) {
+    case kFp8Stream: return "stream";
+    case kFp8Tile256x256: return "tile 256x256";
+    case kFp8Tile128x128Pair: return "tile 128x128 pair";
+    case kFp8Tile128x128: return "tile 128x128";
+    case kFp8Tile64x128: return "tile 64x128";
+    case kFp8Tile64x64: return "tile 64x64";
+    case kFp8Tile64x256: return "tile 64x256";
+    default: return "none";
+    }
+}
+
+namespace {
+
+hipError_t launch_plan(const Fp8Problem &p, const Fp8Plan &plan, hipStream_t s)
+{
     for (const Fp8Part &part : plan.part) {
-        const hipError_t e = part.cols > 0 ? launch_part(p, part, s) : hipSuccess;
+        if (part.cols == 0)
+            continue;
+        const hipError_t e =
+            part.kernel == kFp8Stream ? launch_fp8_stream(p, s) : launch_part(p, part, s);
         if (e != hipSuccess)
             return e;
     }
     return hipSuccess;
 }
 
-hipError_t launch_fp8_tile_codes(const Fp8Problem &p, uint8_t *codes, float *scales, hipStream_t s)
+} // namespace
+
+hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
 {
-    const Fp8Plan plan = plan_fp8_tile_codes(p);
+    return launch_plan(p, plan_fp8_gemm(p), s);
+}
+
+size_t fp8_gated_quantize_bytes(const Fp8Problem &p)
+{
+    return plan_fp8_codes(p).staged ? (size_t)p.m * (size_t)p.n * sizeof(float) : 0;
+}
+
+hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float *scales,
+                                     void *workspace, hipStream_t s)
+{
+    const Fp8Plan plan = plan_fp8_codes(p);
+    if (plan.staged) {
+        Fp8Problem values = p;
+        values.y = workspace;
+        values.ldy = p.n;
+        const hipError_t e = launch_plan(values, plan, s);
+        if (e != hipSuccess)
+            return e;
+        return launch_fp8_quantize(workspace, false, p.m, p.n, p.n, false, codes, scales, s);
+    }
     for (const Fp8Part &part : plan.part) {
         hipError_t e = hipSuccess;
         if (part.cols > 0 && part.kernel == kFp8Tile256x256)
-            e = launch_tile<Tile256x256, true, false, true>(p, part, codes, scales, s);
+            e = launch_tile<Tile256x256, true, false, kCodes>(p, part, codes, scales, s);
         else if (part.cols > 0)
-            e = launch_tile<Tile64x256, true, false, true>(p, part, codes, scales, s);
+            e = launch_tile<Tile64x256, true, false, kCodes>(p, part, codes, scales, s);
         if (e != hipSuccess)
             return e;
     }

@@ -568,6 +568,16 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
                                    void *stream);
 
 /*
+ * Routing queries, host only: the name of the kernel that makes the first
+ * columns of fp8_gemm's or (gated) fp8_gemm_gated's result, and of
+ * fp8_gemm_gated_quantize's: "stream", "tile 256x256", "tile 128x128 pair",
+ * "tile 128x128", "tile 64x128", "tile 64x64" or "tile 64x256"; "none" for no
+ * rows, NULL for sizes that the call refuses.
+ */
+const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt, int gated);
+const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k);
+
+/*
  * token_logprobs: what a head's logits say of each position.  Per row l of
  * `vocab` logits, p = softmax(l):
  *   logprobs[r] = log p(tokens[r]); 0 where tokens[r] is negative (a position
