@@ -27,10 +27,8 @@
 namespace bpg {
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr int kEach = 16;                    // logits a thread holds at once
-constexpr int kStep = kThreads * kEach;      // logits of a step of a workgroup
-constexpr int kSteps = 32;                   // at most, per workgroup
+constexpr int kEach = 16;  // logits a thread holds at once
+constexpr int kSteps = 32; // of a workgroup, at most
 constexpr int kCandidates = 1024;
 constexpr int kMaxParts = 64;
 constexpr float kLog2e = 1.44269504f;
@@ -65,37 +63,90 @@ __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > 
 __device__ __forceinline__ float clamped(float d) { return fmaxf(d, -150.0f); }
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
-__device__ __forceinline__ Part join(Part a, Part b)
+// a DPP move of both halves; lanes without a source keep `old`
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_double(double old, double v)
 {
-    const float m = fmaxf(a.m, b.m);
-    const float da = clamped(a.m - m), db = clamped(b.m - m);
-    const double ea = exp_of(da), eb = exp_of(db);
-    return Part{m, a.odd | b.odd, a.s * ea + b.s * eb,
-                (a.t + da * a.s) * ea + (b.t + db * b.s) * eb};
+    const uint64_t o = __builtin_bit_cast(uint64_t, old), u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32), (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
+// the sum over a wave, in its last lane: shifts by 1, 2, 4, 8 within 16 lanes,
+// then the last lane of 16 to the next 16, of 32 to the next 32
+__device__ __forceinline__ double sum_to_last(double v)
+{
+    v += dpp_double<0x111, 0xf>(0.0, v);
+    v += dpp_double<0x112, 0xf>(0.0, v);
+    v += dpp_double<0x114, 0xf>(0.0, v);
+    v += dpp_double<0x118, 0xf>(0.0, v);
+    v += dpp_double<0x142, 0xa>(0.0, v);
+    v += dpp_double<0x143, 0xc>(0.0, v);
+    return v;
+}
+
+template <int CTRL> __device__ __forceinline__ float max_dpp(float v)
+{
+    return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                        (int)__float_as_uint(v), (int)__float_as_uint(v), CTRL, 0xf, 0xf, false)));
+}
+
+// the maximum over a wave, in every lane
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = max_dpp<0x128>(v);
+    v = max_dpp<0x124>(v);
+    v = max_dpp<0x122>(v);
+    v = max_dpp<0x121>(v);
+    v = max_dpp<0x142>(v);
+    v = max_dpp<0x143>(v);
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+// a part's sums about another maximum
+__device__ __forceinline__ void rescale(Part &p, float m)
+{
+    const float d = clamped(p.m - m);
+    const double e = exp_of(d);
+    p.t = (p.t + d * p.s) * e;
+    p.s *= e;
+    p.m = m;
+}
+
+// all lanes' parts as one, in the last lane
 __device__ __forceinline__ Part over_wave(Part p)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        Part o;
-        o.m = __shfl_xor(p.m, d);
-        o.odd = __shfl_xor(p.odd, d);
-        o.s = __shfl_xor(p.s, d);
-        o.t = __shfl_xor(p.t, d);
-        p = join(p, o);
-    }
+    rescale(p, wave_max(p.m));
+    p.s = sum_to_last(p.s);
+    p.t = sum_to_last(p.t);
+    p.odd = __ballot(p.odd != 0) != 0;
     return p;
+}
+
+// parts of one row (in memory or LDS) as one
+__device__ __forceinline__ Part over_parts(const Part *parts, int count)
+{
+    Part all{-INFINITY, 0, 0.0, 0.0};
+    for (int i = 0; i < count; i++)
+        all.m = fmaxf(all.m, parts[i].m);
+    for (int i = 0; i < count; i++) {
+        Part q = parts[i];
+        rescale(q, all.m);
+        all.s += q.s;
+        all.t += q.t;
+        all.odd |= q.odd;
+    }
+    return all;
 }
 
 // Sixteen logits of a thread in a step: groups of one 16-byte load each, the
 // threads' groups side by side.
-template <bool BF16> struct Step {
+template <bool BF16, int THREADS> struct Step {
     static constexpr int kGroups = BF16 ? 2 : 4, kPer = kEach / kGroups;
     v4u raw[kGroups];
     static __device__ __forceinline__ int64_t id(int64_t at, int q)
     {
-        return at + (int64_t)q * (kThreads * kPer) + threadIdx.x * kPer;
+        return at + (int64_t)q * (THREADS * kPer) + threadIdx.x * kPer;
     }
     static __device__ __forceinline__ const uint8_t *address(const void *row, int64_t i)
     {
@@ -175,9 +226,14 @@ __device__ __forceinline__ Token token_of(const LogprobsProblem &p, int64_t r, c
     return Token{id < 0 || id >= p.vocab ? NAN : logit<BF16>(row, id), id < 0};
 }
 
+__device__ __forceinline__ double log_sum(const Part &all)
+{
+    return all.odd || all.m == -INFINITY ? NAN : log(all.s);
+}
+
 __device__ __forceinline__ void write_row(const LogprobsProblem &p, int64_t r, const Part &all, Token token)
 {
-    const double log_s = all.odd || all.m == -INFINITY ? NAN : log(all.s);
+    const double log_s = log_sum(all);
     if (p.entropy)
         p.entropy[r] = (float)(log_s - all.t / all.s);
     if (p.tokens)
@@ -190,22 +246,28 @@ __device__ __forceinline__ const void *row_of(const LogprobsProblem &p, int64_t 
     return static_cast<const uint8_t *>(p.logits) + r * p.ldl * (BF16 ? 2 : 4);
 }
 
-__device__ __forceinline__ void write_top(const LogprobsProblem &p, int64_t at, uint64_t word, const Part &all)
-{
-    const double log_s = all.odd || all.m == -INFINITY ? NAN : log(all.s);
-    p.ids[at] = (int32_t)(~(uint32_t)word);
-    p.top[at] = (float)((double)(logit_of(word) - all.m) - log_s);
-}
-
-// rank < k of `count` different words: emit(rank, word)
+// Writes rank and word of the words among the k largest of `count` different
+// ones, which begin at a multiple of 16 bytes and have room for eight more.
 template <int THREADS, class F>
-__device__ __forceinline__ void rank_words(const uint64_t *words, int count, int k, F &&emit)
+__device__ __forceinline__ void rank_words(uint64_t *words, int count, int k, F &&emit)
 {
+    typedef uint64_t Pair __attribute__((ext_vector_type(2)));
+    if (threadIdx.x < 8)
+        words[count + threadIdx.x] = 0; // below every logit
+    if (THREADS > 64)
+        __syncthreads();
     for (int i = threadIdx.x; i < count; i += THREADS) {
         const uint64_t mine = words[i];
         int rank = 0;
-        for (int j = 0; j < count; j++)
-            rank += words[j] > mine;
+        for (int j = 0; j < count; j += 8) {
+            Pair o[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                o[u] = *reinterpret_cast<const Pair *>(words + j + 2 * u);
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                rank += (o[u][0] > mine) + (o[u][1] > mine);
+        }
         if (rank < k)
             emit(rank, mine);
     }
@@ -213,28 +275,31 @@ __device__ __forceinline__ void rank_words(const uint64_t *words, int count, int
 
 // workgroup (row, part): logits [part * length, ...) of its row.  TOP: with
 // alternatives.
-template <bool BF16, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProblem p, int parts,
-                                                            int64_t length, Part *out_parts,
-                                                            uint64_t *out_words)
+template <bool BF16, bool TOP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProblem p, int parts,
+                                                              int64_t length, Part *out_parts,
+                                                              uint64_t *out_words)
 {
-    __shared__ Part wave_parts[kWaves];
+    constexpr int kThreads = 64 * WAVES, kStep = kThreads * kEach;
+    typedef Step<BF16, kThreads> Logits;
+    __shared__ Part wave_parts[WAVES];
     __shared__ uint16_t tops[TOP ? kSteps : 1][kThreads];
-    __shared__ float groups[kWaves][64];
-    __shared__ uint64_t words[TOP ? kCandidates : 1], best[kWaves];
+    __shared__ float groups[WAVES][64], reach;
+    __shared__ __attribute__((aligned(16))) uint64_t words[TOP ? kCandidates + 8 : 1];
+    __shared__ uint64_t best[WAVES];
     __shared__ int count;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t r = blockIdx.x / parts, part = blockIdx.x % parts;
     const void *row = row_of<BF16>(p, r);
     const int64_t begin = part * length, end = min(begin + length, p.vocab);
-
     Token token{NAN, true};
     if (parts == 1 && threadIdx.x == 0)
         token = token_of<BF16>(p, r, row);
 
     // ---- the sums
     Part mine{-INFINITY, 0, 0.0, 0.0};
-    Step<BF16> now, next;
+    Logits now, next;
     now.load(row, begin, end);
     int steps = 0;
     for (int64_t at = begin; at < end; at += kStep, steps++) {
@@ -252,7 +317,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProble
             odd |= __builtin_isunordered(v[i], v[i + 1]);
         if (TOP)
             tops[steps][threadIdx.x] = above(top == top ? top : -INFINITY);
-        const float m = fmaxf(mine.m, top), dm = clamped(mine.m - m);
+        const float m = fmaxf(mine.m, top);
         float e[kEach], t[kEach];
 #pragma unroll
         for (int i = 0; i < kEach; i++) {
@@ -260,65 +325,69 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProble
             e[i] = exp_of(d);
             t[i] = d * e[i];
         }
-        const double c = exp_of(dm);
-        mine.t = (mine.t + dm * mine.s) * c + (double)sum_of(t);
-        mine.s = mine.s * c + (double)sum_of(e);
-        mine.m = m;
+        rescale(mine, m);
+        mine.s += (double)sum_of(e);
+        mine.t += (double)sum_of(t);
         mine.odd |= odd || top == INFINITY;
         now = next;
     }
     const float top = mine.m; // -inf: the sums are 0 (-inf - -inf is clamped)
     mine = over_wave(mine);
-    if (lane == 0)
+    if (WAVES > 1 && lane == 63)
         wave_parts[wave] = mine;
     if (TOP) {
         groups[wave][lane] = top;
         if (threadIdx.x == 0)
             count = 0;
     }
-    __syncthreads();
-    Part all = wave_parts[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; w++)
-        all = join(all, wave_parts[w]);
-    if (threadIdx.x == 0) {
-        if (parts == 1)
-            write_row(p, r, all, token);
-        else
-            out_parts[blockIdx.x] = all;
+    if (WAVES > 1)
+        __syncthreads();
+    // the first wave goes on; the others come back to read their logits again
+    float least = 0;
+    if (wave == 0) {
+        Part all;
+        if constexpr (WAVES > 1) {
+            all = over_parts(wave_parts, WAVES);
+        } else {
+            all.m = mine.m;
+            all.odd = mine.odd;
+            all.s = __shfl(mine.s, 63);
+            all.t = __shfl(mine.t, 63);
+        }
+        if (threadIdx.x == 0) {
+            if (parts == 1)
+                write_row(p, r, all, token);
+            else
+                out_parts[blockIdx.x] = all;
+        }
+        mine = all;
     }
     if constexpr (!TOP)
         return;
 
     // ---- the alternatives
     const int k = (int)min((int64_t)p.topk, end - begin);
-    if (parts > 1 && (int)threadIdx.x >= k && (int)threadIdx.x < p.topk)
-        out_words[(int64_t)blockIdx.x * p.topk + threadIdx.x] = 0; // none: below every logit
-    auto emit = [&](int rank, uint64_t word) {
-        if (parts == 1)
-            write_top(p, r * p.topk + rank, word, all);
-        else
-            out_words[(int64_t)blockIdx.x * p.topk + rank] = word;
-    };
-    if (all.m == -INFINITY) { // the first ones
-        if ((int)threadIdx.x < k)
-            emit(threadIdx.x, word_of(-INFINITY, (uint32_t)(begin + threadIdx.x)));
-        return;
-    }
-    // the k-th largest of 64 groups' maxima, in every wave
-    float g = groups[0][lane];
+    if (wave == 0) {
+        // the k-th largest of 64 groups' maxima
+        float g = groups[0][lane];
 #pragma unroll
-    for (int w = 1; w < kWaves; w++)
-        g = fmaxf(g, groups[w][lane]);
-    int rank = 0;
+        for (int w = 1; w < WAVES; w++)
+            g = fmaxf(g, groups[w][lane]);
+        int rank = 0;
 #pragma unroll
-    for (int i = 0; i < 64; i++) {
-        const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
-        rank += o > g || (o == g && i < lane);
+        for (int i = 0; i < 64; i++) {
+            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
+            rank += o > g || (o == g && i < lane);
+        }
+        const uint64_t which = __ballot(rank == k - 1);
+        least = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), __builtin_ctzll(which)));
+        if (WAVES > 1 && threadIdx.x == 0)
+            reach = least;
     }
-    const uint64_t which = __ballot(rank == k - 1);
-    const float least =
-        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), __builtin_ctzll(which)));
+    if constexpr (WAVES > 1) {
+        __syncthreads();
+        least = reach;
+    }
     if (top >= least) {
         for (int s = 0; s < steps; s++) {
             const int64_t at = begin + (int64_t)s * kStep;
@@ -329,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProble
             now.values(v);
 #pragma unroll
             for (int i = 0; i < kEach; i++) {
-                const int64_t id = Step<BF16>::id(at, i / Step<BF16>::kPer) + i % Step<BF16>::kPer;
+                const int64_t id = Logits::id(at, i / Logits::kPer) + i % Logits::kPer;
                 const float l = v[i] == v[i] ? v[i] : -INFINITY;
                 if (l >= least && id < end) {
                     const int slot = atomicAdd(&count, 1); // the order decides nothing
@@ -340,8 +409,24 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProble
         }
     }
     __syncthreads();
-    if (count <= kCandidates) {
-        rank_words<kThreads>(words, count, k, emit);
+    const bool few = count <= kCandidates;
+    if (few && wave > 0)
+        return;
+    double log_s = 0;
+    if (wave == 0 && parts == 1)
+        log_s = log_sum(mine);
+    auto emit = [&](int rank, uint64_t word) {
+        if (parts > 1) {
+            out_words[(int64_t)blockIdx.x * p.topk + rank] = word;
+            return;
+        }
+        p.ids[r * p.topk + rank] = (int32_t)(~(uint32_t)word);
+        p.top[r * p.topk + rank] = (float)((double)(logit_of(word) - mine.m) - log_s);
+    };
+    if (parts > 1 && (int)threadIdx.x >= k && (int)threadIdx.x < p.topk)
+        out_words[(int64_t)blockIdx.x * p.topk + threadIdx.x] = 0; // none: below every logit
+    if (few) {
+        rank_words<64>(words, count, k, emit);
         return;
     }
     uint64_t last = ~(uint64_t)0;
@@ -359,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(const LogprobsProble
             best[wave] = found;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWaves; w++)
+        for (int w = 0; w < WAVES; w++)
             found = larger(found, best[w]);
         last = found;
         if (threadIdx.x == 0)
@@ -374,71 +459,120 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
                                                                      const Part *in_parts,
                                                                      const uint64_t *in_words)
 {
-    __shared__ uint64_t words[kMaxParts * 64];
+    __shared__ __attribute__((aligned(16))) uint64_t words[kMaxParts * 64 + 8];
+    __shared__ Part sums[kMaxParts];
+    __shared__ uint64_t reach[2];
+    __shared__ int count;
     const int64_t r = blockIdx.x;
-    Part all = in_parts[r * parts];
-    for (int i = 1; i < parts; i++)
-        all = join(all, in_parts[r * parts + i]);
-    if (threadIdx.x == 0)
-        write_row(p, r, all, token_of<BF16>(p, r, row_of<BF16>(p, r)));
-    const int count = parts * p.topk;
-    for (int i = threadIdx.x; i < count; i += kJoinThreads)
-        words[i] = in_words[r * count + i];
+    Token token{NAN, true};
+    if (threadIdx.x == 0) {
+        token = token_of<BF16>(p, r, row_of<BF16>(p, r));
+        count = 0;
+    }
+    if ((int)threadIdx.x < parts)
+        sums[threadIdx.x] = in_parts[r * parts + threadIdx.x];
+    // Every part's words fall.  At least topk words are not below the largest
+    // of the parts' last, nor below the smallest of their (topk / parts)-th.
+    const int k = p.topk, each = (k + parts - 1) / parts;
+    const uint64_t *in = in_words + r * parts * k;
+    if (k > 0 && threadIdx.x < 64) {
+        uint64_t last = 0, share = ~(uint64_t)0;
+        for (int i = threadIdx.x; i < parts; i += 64) {
+            last = larger(last, in[i * k + k - 1]);
+            share = min(share, in[i * k + each - 1]);
+        }
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) {
+            last = larger(last, __shfl_xor(last, d));
+            share = min(share, (uint64_t)__shfl_xor(share, d));
+        }
+        if (threadIdx.x == 0)
+            reach[0] = larger(larger(last, share), 1);
+    }
     __syncthreads();
-    rank_words<kJoinThreads>(words, count, p.topk, [&](int rank, uint64_t word) {
-        write_top(p, r * p.topk + rank, word, all);
+    const Part all = over_parts(sums, parts);
+    if (threadIdx.x == 0)
+        write_row(p, r, all, token);
+    if (k == 0)
+        return;
+    for (int i = threadIdx.x; i < parts * k; i += kJoinThreads) {
+        const uint64_t w = in[i];
+        if (w >= reach[0])
+            words[atomicAdd(&count, 1)] = w; // the order decides nothing
+    }
+    __syncthreads();
+    const double log_s = log_sum(all);
+    rank_words<kJoinThreads>(words, count, k, [&](int rank, uint64_t word) {
+        p.ids[r * k + rank] = (int32_t)(~(uint32_t)word);
+        p.top[r * k + rank] = (float)((double)(logit_of(word) - all.m) - log_s);
     });
 }
 
-// Parts of a row: one where the rows fill the chip (256 CUs), else about 1024
-// workgroups; a part is a whole number of steps, 32 at most.
-int parts_of(int64_t rows, int64_t vocab, int64_t *length)
+// How a row is split: waves of a workgroup, and parts of `length` logits.  One
+// part where the rows fill the chip (256 CUs), else about 1024 workgroups; a
+// part is a whole number of steps, 32 at most.
+struct Split {
+    int waves, parts;
+    int64_t length;
+};
+
+Split split_of(int64_t rows, int64_t vocab)
 {
-    const int64_t steps = (vocab + kStep - 1) / kStep;
+    Split s;
+    s.waves = vocab <= 4096 ? 1 : vocab <= 65536 && rows > 128 ? 4 : 8;
+    const int64_t step = 64 * s.waves * kEach, steps = (vocab + step - 1) / step;
     int64_t parts = rows > 128 ? 1 : (1024 + rows - 1) / (rows > 0 ? rows : 1);
     parts = std::min<int64_t>(std::min<int64_t>(parts, steps), kMaxParts);
+    if (s.waves == 1)
+        parts = 1;
     parts = std::max<int64_t>(parts, (steps + kSteps - 1) / kSteps);
-    const int64_t each = (steps + parts - 1) / parts;
-    *length = each * kStep;
-    return (int)((vocab + *length - 1) / *length);
+    s.length = (steps + parts - 1) / parts * step;
+    s.parts = (int)((vocab + s.length - 1) / s.length);
+    return s;
+}
+
+template <bool BF16, bool TOP>
+void launch_parts(const LogprobsProblem &p, const Split &s, Part *sums, uint64_t *words, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)(p.rows * s.parts);
+    if (s.waves == 1)
+        logprobs_kernel<BF16, TOP, 1><<<grid, 64, 0, stream>>>(p, s.parts, s.length, sums, words);
+    else if (s.waves == 4)
+        logprobs_kernel<BF16, TOP, 4><<<grid, 256, 0, stream>>>(p, s.parts, s.length, sums, words);
+    else
+        logprobs_kernel<BF16, TOP, 8><<<grid, 512, 0, stream>>>(p, s.parts, s.length, sums, words);
 }
 
 } // namespace
 
 size_t logprobs_bytes(int64_t rows, int64_t vocab, int topk)
 {
-    int64_t length;
-    const int parts = parts_of(rows, vocab, &length);
-    return parts == 1 ? 0 : (size_t)rows * parts * (sizeof(Part) + (size_t)topk * sizeof(uint64_t));
+    const int64_t parts = split_of(rows, vocab).parts;
+    return parts == 1 ? 0 : (size_t)(rows * parts) * (sizeof(Part) + (size_t)topk * sizeof(uint64_t));
 }
 
 hipError_t launch_logprobs(const LogprobsProblem &p, void *workspace, hipStream_t stream)
 {
     if (p.rows == 0)
         return hipSuccess;
-    int64_t length;
-    const int parts = parts_of(p.rows, p.vocab, &length);
+    const Split s = split_of(p.rows, p.vocab);
     Part *sums = static_cast<Part *>(workspace);
-    uint64_t *words = reinterpret_cast<uint64_t *>(sums + p.rows * parts);
-    const unsigned grid = (unsigned)(p.rows * parts);
-#define BPG_LOGPROBS(BF16, TOP)                                                                    \
-    logprobs_kernel<BF16, TOP><<<grid, kThreads, 0, stream>>>(p, parts, length, sums, words)
+    uint64_t *words = reinterpret_cast<uint64_t *>(sums + p.rows * s.parts);
     if (p.bf16 && p.topk > 0)
-        BPG_LOGPROBS(true, true);
+        launch_parts<true, true>(p, s, sums, words, stream);
     else if (p.bf16)
-        BPG_LOGPROBS(true, false);
+        launch_parts<true, false>(p, s, sums, words, stream);
     else if (p.topk > 0)
-        BPG_LOGPROBS(false, true);
+        launch_parts<false, true>(p, s, sums, words, stream);
     else
-        BPG_LOGPROBS(false, false);
-#undef BPG_LOGPROBS
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts == 1)
+        launch_parts<false, false>(p, s, sums, words, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || s.parts == 1)
         return e;
     if (p.bf16)
-        logprobs_join_kernel<true><<<(unsigned)p.rows, kJoinThreads, 0, stream>>>(p, parts, sums, words);
+        logprobs_join_kernel<true><<<(unsigned)p.rows, kJoinThreads, 0, stream>>>(p, s.parts, sums, words);
     else
-        logprobs_join_kernel<false><<<(unsigned)p.rows, kJoinThreads, 0, stream>>>(p, parts, sums, words);
+        logprobs_join_kernel<false><<<(unsigned)p.rows, kJoinThreads, 0, stream>>>(p, s.parts, sums, words);
     return hipGetLastError();
 }
 
