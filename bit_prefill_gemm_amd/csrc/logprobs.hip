@@ -31,15 +31,18 @@ constexpr int kEach = 16;  // logits a thread holds at once
 constexpr int kSteps = 32; // of a workgroup, at most
 constexpr int kCandidates = 1024;
 constexpr int kMaxParts = 64;
-constexpr float kLog2e = 1.44269504f;
+constexpr float kLog2e = 1.44269504f; // log2 e to 2^-26; divided by again at the end
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// What a part of a row amounts to.
+// What a part of a row amounts to: sums of 2^x and x 2^x, x = l log2 e - ref.
+// The reference is m log2 e, or the float next to it: x is then one FMA, with one
+// rounding relative to x, however large the logits are.
 struct Part {
+    double ref;
+    double s, t;  // 0 where m is -inf
     float m;      // the largest logit, -inf if there is none
-    uint32_t odd; // a NaN or +inf among them
-    double s, t;  // the sums, 0 where m is -inf
+    uint32_t odd; // a NaN or +inf among them (s may be NaN instead)
 };
 
 // An order of the logits and their ids in one word: larger words are larger
@@ -59,9 +62,10 @@ __device__ __forceinline__ float logit_of(uint64_t word)
 
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
-// e^d, d <= 0 or NaN (from -inf - -inf: no logit yet); 0 below -150
-__device__ __forceinline__ float clamped(float d) { return fmaxf(d, -150.0f); }
-__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+__device__ __forceinline__ double reference(float m)
+{
+    return fabsf(m) < INFINITY ? (double)m * kLog2e : 0.0;
+}
 
 // a DPP move of both halves; lanes without a source keep `old`
 template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_double(double old, double v)
@@ -103,20 +107,22 @@ __device__ __forceinline__ float wave_max(float v)
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// a part's sums about another maximum
-__device__ __forceinline__ void rescale(Part &p, float m)
+// a part's sums about a maximum that is not smaller
+__device__ __forceinline__ void rescale(Part &p, float m, double ref)
 {
-    const float d = clamped(p.m - m);
-    const double e = exp_of(d);
+    const double d = p.m == -INFINITY ? 0.0 : p.ref - ref;
+    const double e = __builtin_amdgcn_exp2f((float)d);
     p.t = (p.t + d * p.s) * e;
     p.s *= e;
     p.m = m;
+    p.ref = ref;
 }
 
 // all lanes' parts as one, in the last lane
 __device__ __forceinline__ Part over_wave(Part p)
 {
-    rescale(p, wave_max(p.m));
+    const float m = wave_max(p.m);
+    rescale(p, m, reference(m));
     p.s = sum_to_last(p.s);
     p.t = sum_to_last(p.t);
     p.odd = __ballot(p.odd != 0) != 0;
@@ -126,12 +132,13 @@ __device__ __forceinline__ Part over_wave(Part p)
 // parts of one row (in memory or LDS) as one
 __device__ __forceinline__ Part over_parts(const Part *parts, int count)
 {
-    Part all{-INFINITY, 0, 0.0, 0.0};
+    Part all{0.0, 0.0, 0.0, -INFINITY, 0};
     for (int i = 0; i < count; i++)
         all.m = fmaxf(all.m, parts[i].m);
+    all.ref = reference(all.m);
     for (int i = 0; i < count; i++) {
         Part q = parts[i];
-        rescale(q, all.m);
+        rescale(q, all.m, all.ref);
         all.s += q.s;
         all.t += q.t;
         all.odd |= q.odd;
@@ -226,18 +233,24 @@ __device__ __forceinline__ Token token_of(const LogprobsProblem &p, int64_t r, c
     return Token{id < 0 || id >= p.vocab ? NAN : logit<BF16>(row, id), id < 0};
 }
 
+// log2 S, NaN for a row without a distribution
 __device__ __forceinline__ double log_sum(const Part &all)
 {
-    return all.odd || all.m == -INFINITY ? NAN : log(all.s);
+    return all.odd || all.m == -INFINITY ? NAN : log2(all.s);
 }
 
-__device__ __forceinline__ void write_row(const LogprobsProblem &p, int64_t r, const Part &all, Token token)
+__device__ __forceinline__ float log_probability(const Part &all, double log_s, float logit)
 {
-    const double log_s = log_sum(all);
+    return (float)(((double)logit * kLog2e - all.ref - log_s) * (1.0 / kLog2e));
+}
+
+__device__ __forceinline__ void write_row(const LogprobsProblem &p, int64_t r, const Part &all, double log_s,
+                                          Token token)
+{
     if (p.entropy)
-        p.entropy[r] = (float)(log_s - all.t / all.s);
+        p.entropy[r] = (float)((log_s - all.t / all.s) * (1.0 / kLog2e));
     if (p.tokens)
-        p.logprobs[r] = token.none ? 0.0f : (float)((double)(token.logit - all.m) - log_s);
+        p.logprobs[r] = token.none ? 0.0f : log_probability(all, log_s, token.logit);
 }
 
 template <bool BF16>
@@ -298,7 +311,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         token = token_of<BF16>(p, r, row);
 
     // ---- the sums
-    Part mine{-INFINITY, 0, 0.0, 0.0};
+    Part mine{0.0, 0.0, 0.0, -INFINITY, 0};
     Logits now, next;
     now.load(row, begin, end);
     int steps = 0;
@@ -307,31 +320,42 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
             next.load(row, at + kStep, end);
         float v[kEach];
         now.values(v);
-        float top = v[0];
-        bool odd = false;
+        float top = v[0], low = v[0];
 #pragma unroll
-        for (int i = 1; i < kEach; i++)
-            top = fmaxf(top, v[i]); // drops NaN
-#pragma unroll
-        for (int i = 0; i < kEach; i += 2)
-            odd |= __builtin_isunordered(v[i], v[i + 1]);
+        for (int i = 1; i < kEach; i++) { // NaN is dropped
+            top = fmaxf(top, v[i]);
+            low = fminf(low, v[i]);
+        }
         if (TOP)
             tops[steps][threadIdx.x] = above(top == top ? top : -INFINITY);
         const float m = fmaxf(mine.m, top);
-        float e[kEach], t[kEach];
+        float e[kEach], t[4] = {0, 0, 0, 0};
+        if (__builtin_amdgcn_ballot_w64(!(low > -1e38f && top < 1e38f)) == 0) {
+            // nothing is masked: a NaN makes the sums NaN
+            const float ref = m * kLog2e;
+            rescale(mine, m, ref);
 #pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const float d = clamped(v[i] - m);
-            e[i] = exp_of(d);
-            t[i] = d * e[i];
+            for (int i = 0; i < kEach; i++) {
+                const float x = __builtin_fmaf(v[i], kLog2e, -ref);
+                e[i] = __builtin_amdgcn_exp2f(x);
+                t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
+            }
+        } else {
+            // x held to -250 and above, where 2^x is 0; NaN is dropped, and told
+            rescale(mine, m, reference(m));
+#pragma unroll
+            for (int i = 0; i < kEach; i++) {
+                const float x = fmaxf((v[i] - m) * kLog2e, -250.0f);
+                e[i] = __builtin_amdgcn_exp2f(x);
+                t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
+                mine.odd |= !(v[i] < INFINITY);
+            }
         }
-        rescale(mine, m);
         mine.s += (double)sum_of(e);
         mine.t += (double)sum_of(t);
-        mine.odd |= odd || top == INFINITY;
         now = next;
     }
-    const float top = mine.m; // -inf: the sums are 0 (-inf - -inf is clamped)
+    const float top = mine.m;
     mine = over_wave(mine);
     if (WAVES > 1 && lane == 63)
         wave_parts[wave] = mine;
@@ -344,19 +368,21 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         __syncthreads();
     // the first wave goes on; the others come back to read their logits again
     float least = 0;
+    double log_s = 0;
     if (wave == 0) {
         Part all;
         if constexpr (WAVES > 1) {
             all = over_parts(wave_parts, WAVES);
         } else {
-            all.m = mine.m;
-            all.odd = mine.odd;
+            all = mine;
             all.s = __shfl(mine.s, 63);
             all.t = __shfl(mine.t, 63);
         }
+        if (parts == 1)
+            log_s = log_sum(all);
         if (threadIdx.x == 0) {
             if (parts == 1)
-                write_row(p, r, all, token);
+                write_row(p, r, all, log_s, token);
             else
                 out_parts[blockIdx.x] = all;
         }
@@ -373,20 +399,30 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
 #pragma unroll
         for (int w = 1; w < WAVES; w++)
             g = fmaxf(g, groups[w][lane]);
+        // the k-th of them, or a little less: the lowest bits give way to the
+        // lane, which makes the keys different
+        const uint32_t key = (uint32_t)(word_of(g, 0) >> 32 & ~(uint64_t)63) | (uint32_t)lane;
         int rank = 0;
 #pragma unroll
-        for (int i = 0; i < 64; i++) {
-            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), i));
-            rank += o > g || (o == g && i < lane);
-        }
+        for (int i = 0; i < 64; i++)
+            rank += (uint32_t)__builtin_amdgcn_readlane((int)key, i) > key;
         const uint64_t which = __ballot(rank == k - 1);
-        least = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), __builtin_ctzll(which)));
+        const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(which));
+        least = logit_of((uint64_t)max(kth & ~63u, 0x007fffffu) << 32); // -inf at least
+        if (mine.m == -INFINITY)
+            least = NAN; // nothing reaches it
         if (WAVES > 1 && threadIdx.x == 0)
             reach = least;
     }
     if constexpr (WAVES > 1) {
         __syncthreads();
         least = reach;
+    }
+    if (least != least) { // a row of -inf: the first ones
+        if ((int)threadIdx.x < k)
+            words[threadIdx.x] = word_of(-INFINITY, (uint32_t)(begin + threadIdx.x));
+        if (threadIdx.x == 0)
+            count = k;
     }
     if (top >= least) {
         for (int s = 0; s < steps; s++) {
@@ -412,16 +448,13 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     const bool few = count <= kCandidates;
     if (few && wave > 0)
         return;
-    double log_s = 0;
-    if (wave == 0 && parts == 1)
-        log_s = log_sum(mine);
     auto emit = [&](int rank, uint64_t word) {
         if (parts > 1) {
             out_words[(int64_t)blockIdx.x * p.topk + rank] = word;
             return;
         }
         p.ids[r * p.topk + rank] = (int32_t)(~(uint32_t)word);
-        p.top[r * p.topk + rank] = (float)((double)(logit_of(word) - mine.m) - log_s);
+        p.top[r * p.topk + rank] = log_probability(mine, log_s, logit_of(word));
     };
     if (parts > 1 && (int)threadIdx.x >= k && (int)threadIdx.x < p.topk)
         out_words[(int64_t)blockIdx.x * p.topk + threadIdx.x] = 0; // none: below every logit
@@ -491,8 +524,9 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
     }
     __syncthreads();
     const Part all = over_parts(sums, parts);
+    const double log_s = log_sum(all);
     if (threadIdx.x == 0)
-        write_row(p, r, all, token);
+        write_row(p, r, all, log_s, token);
     if (k == 0)
         return;
     for (int i = threadIdx.x; i < parts * k; i += kJoinThreads) {
@@ -501,10 +535,9 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(const Logpr
             words[atomicAdd(&count, 1)] = w; // the order decides nothing
     }
     __syncthreads();
-    const double log_s = log_sum(all);
     rank_words<kJoinThreads>(words, count, k, [&](int rank, uint64_t word) {
         p.ids[r * k + rank] = (int32_t)(~(uint32_t)word);
-        p.top[r * k + rank] = (float)((double)(logit_of(word) - all.m) - log_s);
+        p.top[r * k + rank] = log_probability(all, log_s, logit_of(word));
     });
 }
 
@@ -519,7 +552,7 @@ struct Split {
 Split split_of(int64_t rows, int64_t vocab)
 {
     Split s;
-    s.waves = vocab <= 4096 ? 1 : vocab <= 65536 && rows > 128 ? 4 : 8;
+    s.waves = vocab <= 4096 ? 1 : vocab <= 131072 && rows > 512 ? 4 : 8;
     const int64_t step = 64 * s.waves * kEach, steps = (vocab + step - 1) / step;
     int64_t parts = rows > 128 ? 1 : (1024 + rows - 1) / (rows > 0 ? rows : 1);
     parts = std::min<int64_t>(std::min<int64_t>(parts, steps), kMaxParts);
