@@ -11,7 +11,7 @@
 // One pass over the logits: a thread holds 16 at a time, takes their maximum,
 // rescales its sums to it and adds the 16 terms (in fp32 among the 16, in fp64
 // from one 16 to the next).  For the alternatives it leaves each 16's maximum in
-// LDS.  The k-th largest of 64 groups' maxima is then below or at the k-th
+// LDS.  The k-th largest of 64 (or 128) groups' maxima is then below or at the k-th
 // largest logit, and few logits reach it (64 ln (64 / (64 - k)) on shuffled
 // rows: 24 for k = 20), so only the 16s that do are read again.  Where more than
 // kCandidates reach it (rows of equal logits, or with fewer than k above -inf)
@@ -394,21 +394,42 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     // ---- the alternatives
     const int k = (int)min((int64_t)p.topk, end - begin);
     if (wave == 0) {
-        // the k-th largest of 64 groups' maxima
-        float g = groups[0][lane];
+        // the k-th largest of 64 groups' maxima, of 128 for many alternatives, or
+        // a little less: the lowest bits give way to the group, which makes the
+        // keys different
+        auto key_of = [](float g, int group) {
+            return (uint32_t)(word_of(g, 0) >> 32 & ~(uint64_t)127) | (uint32_t)group;
+        };
+        const int kinds = WAVES > 1 && k > 32 ? 2 : 1;
+        float even = groups[0][lane], odd = -INFINITY;
 #pragma unroll
-        for (int w = 1; w < WAVES; w++)
-            g = fmaxf(g, groups[w][lane]);
-        // the k-th of them, or a little less: the lowest bits give way to the
-        // lane, which makes the keys different
-        const uint32_t key = (uint32_t)(word_of(g, 0) >> 32 & ~(uint64_t)63) | (uint32_t)lane;
-        int rank = 0;
+        for (int w = 1; w < WAVES; w++) {
+            if (kinds == 2 && w % 2)
+                odd = fmaxf(odd, groups[w][lane]);
+            else
+                even = fmaxf(even, groups[w][lane]);
+        }
+        const uint32_t key = key_of(even, lane), other = key_of(odd, 64 + lane);
+        int rank = 0, rank_other = 0;
 #pragma unroll
         for (int i = 0; i < 64; i++)
             rank += (uint32_t)__builtin_amdgcn_readlane((int)key, i) > key;
-        const uint64_t which = __ballot(rank == k - 1);
-        const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(which));
-        least = logit_of((uint64_t)max(kth & ~63u, 0x007fffffu) << 32); // -inf at least
+        if (kinds == 2) {
+#pragma unroll
+            for (int i = 0; i < 64; i++) {
+                const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)key, i);
+                const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)other, i);
+                rank += b > key;
+                rank_other += (a > other) + (b > other);
+            }
+        } else {
+            rank_other = -1;
+        }
+        const uint64_t which = __ballot(rank == k - 1), where = __ballot(rank_other == k - 1);
+        const uint32_t kth =
+            which ? (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(which))
+                  : (uint32_t)__builtin_amdgcn_readlane((int)other, __builtin_ctzll(where));
+        least = logit_of((uint64_t)max(kth & ~127u, 0x007fffffu) << 32); // -inf at least
         if (mine.m == -INFINITY)
             least = NAN; // nothing reaches it
         if (WAVES > 1 && threadIdx.x == 0)
