@@ -31,7 +31,7 @@ ENTRY_POINTS = ("bpg_status_str", "rotate_pack_weights_bytes", "rotate_pack_weig
                 "w4a4_gemm_bf16", "w4a4_grouped_gemm_bf16", "w4a4_gemm_kernel_name",
                 "w4a4_grouped_gemm_kernel_name", "rmsnorm_quantize_act", "dequantize_act",
                 "w4a4_gemm_epilogue", "w4a4_gemm_epilogue_kernel_name", "moe_route_topk",
-                "quantize_fp8", "fp8_gemm", "fp8_gemm_gated", "fp8_gemm_gated_quantize_bytes",
+                "quantize_fp8", "fp8_gemm_bytes", "fp8_gemm", "fp8_gemm_gated", "fp8_gemm_gated_quantize_bytes",
                 "fp8_gemm_gated_quantize", "fp8_gemm_kernel_name",
                 "fp8_gemm_gated_quantize_kernel_name", "token_logprobs_bytes", "token_logprobs")
 
@@ -136,7 +136,9 @@ def _lib_handle():
     lib.quantize_fp8.restype = _int
     lib.quantize_fp8.argtypes = [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _vp]
     lib.fp8_gemm.restype = _int
-    lib.fp8_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64, _vp]
+    lib.fp8_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64, _vp, _size, _vp]
+    lib.fp8_gemm_bytes.restype = _size
+    lib.fp8_gemm_bytes.argtypes = [_i64, _i64, _i64, _int]
     lib.fp8_gemm_gated.restype = _int
     lib.fp8_gemm_gated.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _int,
                                    _i64, _vp]

@@ -906,7 +906,8 @@ bpg::Fp8Problem fp8_problem(const void *codes, const float *scales, int64_t m, c
     return p;
 }
 
-bpg_status fp8_product(bpg::Fp8Problem &p, void *y, bpg_x_dtype y_dt, int64_t ldy, void *stream)
+bpg_status fp8_product(bpg::Fp8Problem &p, void *y, bpg_x_dtype y_dt, int64_t ldy, void *workspace,
+                       size_t workspace_bytes, void *stream)
 {
     if (!dtype_ok(y_dt))
         return BPG_ERR_DTYPE;
@@ -914,16 +915,21 @@ bpg_status fp8_product(bpg::Fp8Problem &p, void *y, bpg_x_dtype y_dt, int64_t ld
         return BPG_ERR_SHAPE;
     if (p.m > 0 && !y)
         return BPG_ERR_NULL;
-    if (!aligned_to(y, y_dt))
-        return BPG_ERR_ALIGN;
-    const bpg_status s = check_device();
-    if (s != BPG_OK)
-        return s;
     p.y = y;
     p.ldy = ldy;
     p.y_bf16 = y_dt == BPG_X_BF16;
     p.exact = !p.y_bf16;
-    return launch_status(bpg::launch_fp8_gemm(p, static_cast<hipStream_t>(stream)));
+    const size_t need = bpg::fp8_gemm_bytes(p);
+    if (need > 0 && !workspace)
+        return BPG_ERR_NULL;
+    if (!aligned_to(y, y_dt) || !aligned16(workspace))
+        return BPG_ERR_ALIGN;
+    if (workspace_bytes < need)
+        return BPG_ERR_BUFFER;
+    const bpg_status s = check_device();
+    if (s != BPG_OK)
+        return s;
+    return launch_status(bpg::launch_fp8_gemm(p, workspace, static_cast<hipStream_t>(stream)));
 }
 
 } // namespace
@@ -953,7 +959,7 @@ bpg_status quantize_fp8(const void *x, bpg_x_dtype dt, int64_t m, int64_t k, int
 
 bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const void *w_codes,
                     const float *w_scales, int64_t n, int64_t k, void *y, bpg_x_dtype y_dt,
-                    int64_t ldy, void *stream)
+                    int64_t ldy, void *workspace, size_t workspace_bytes, void *stream)
 {
     const bpg_status s =
         check_fp8(codes, scales, m, w_codes, w_scales, false, nullptr, nullptr, n, k);
@@ -961,7 +967,7 @@ bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const voi
         return s;
     bpg::Fp8Problem p =
         fp8_problem(codes, scales, m, w_codes, w_scales, nullptr, nullptr, n, k);
-    return fp8_product(p, y, y_dt, ldy, stream);
+    return fp8_product(p, y, y_dt, ldy, workspace, workspace_bytes, stream);
 }
 
 bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
@@ -978,7 +984,7 @@ bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
     bpg::Fp8Problem p =
         fp8_problem(codes, scales, m, gate_codes, gate_scales, up_codes, up_scales, f, k);
     p.act = act;
-    return fp8_product(p, y, y_dt, ldy, stream);
+    return fp8_product(p, y, y_dt, ldy, nullptr, 0, stream);
 }
 
 size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k)
@@ -986,6 +992,16 @@ size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k)
     if (!fp8_shape(m, f, k) || f % 32 != 0)
         return 0;
     return bpg::fp8_gated_quantize_bytes(shape_problem(m, f, k, true));
+}
+
+size_t fp8_gemm_bytes(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt)
+{
+    if (!fp8_shape(m, n, k) || !dtype_ok(y_dt))
+        return 0;
+    bpg::Fp8Problem p = shape_problem(m, n, k, false);
+    p.y_bf16 = y_dt == BPG_X_BF16;
+    p.exact = !p.y_bf16;
+    return bpg::fp8_gemm_bytes(p);
 }
 
 const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt, int gated)

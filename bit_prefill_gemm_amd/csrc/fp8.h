@@ -36,7 +36,8 @@ struct Fp8Problem {
     bool exact;            // products added in fp32 (fp8_mma.h)
     int act;               // bpg_activation (gated)
 };
-hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t stream);
+size_t fp8_gemm_bytes(const Fp8Problem &p); // of the workspace
+hipError_t launch_fp8_gemm(const Fp8Problem &p, void *workspace, hipStream_t stream);
 // The gated product (p.y, ldy, y_bf16 unused) as codes [m][n] and scales
 // [m][blocks of n]; workspace: fp8_gated_quantize_bytes(p) bytes.
 size_t fp8_gated_quantize_bytes(const Fp8Problem &p);
@@ -58,6 +59,7 @@ enum Fp8Kernel {
 struct Fp8Part {
     int kernel;
     int64_t first, cols;
+    int splits; // parts of K, joined by another launch; 0 or 1: one
 };
 struct Fp8Plan {
     Fp8Part part[2]; // the second may have no columns

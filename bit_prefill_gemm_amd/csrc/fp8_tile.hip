@@ -29,7 +29,8 @@ enum Store { kBf16, kF32, kCodes };
 
 template <class T, bool GATED, bool EXACT, Store STORE>
 __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
-    const Fp8Problem p, int64_t col_first, int64_t cols, uint8_t *out_codes, float *out_scales)
+    const Fp8Problem p, int64_t col_first, int64_t cols, int k_each, uint8_t *out_codes,
+    float *out_scales)
 {
     constexpr int NI = T::NI, MJ = T::MJ, S = T::S, KS = T::KS, G = GATED ? 2 : 1;
     constexpr int kCols = T::kRowsW / G;
@@ -76,8 +77,10 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     // first half of w's row tiles; and their second half.
     constexpr int kLoadsX = T::kRowsX / 8 / T::kWaves, kLoadsW = T::kRowsW / 16 / T::kWaves;
     constexpr int kFirst = kLoadsX + kLoadsW, kSecond = kLoadsW;
-    // a group's block b is block b + before of K
-    const int rounds = (blocks + KS - 1) / KS, before = group * rounds;
+    // a group's block b is block b + before of K; blockIdx.y: which k_each blocks
+    // of K the workgroup takes
+    const int k_first = blockIdx.y * k_each, k_end = min(k_first + k_each, blocks);
+    const int rounds = (k_end - k_first + KS - 1) / KS, before = k_first + group * rounds;
     auto at_of = [&](int b) { return (uint32_t)(b + before) * kFp8Block; };
     auto load_w = [&](uint32_t to, int b, uint32_t l, int half, int u) {
         constexpr int kHalf = 8 * NI, kParts = kHalf / 8; // rows and loads of a wave's half
@@ -86,9 +89,9 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
         const int col = GATED ? owner * kHalf + row : in;
         load16(GATED && half ? us : ws, to + kX + in * 128, l, (uint32_t)(col * k) + at_of(b));
     };
-    // pieces past K are read from past the buffer: zeros
+    // pieces past K or past the workgroup's blocks are read from past the buffer: zeros
     auto lane_from = [&](int b) {
-        return at_of(b) + piece < k ? lane_at : kPastBuffer;
+        return b + before < k_end && at_of(b) + piece < k ? lane_at : kPastBuffer;
     };
     auto load_first = [&](int stage, int b, int u) {
         const uint32_t to = base + stage * kStage, l = lane_from(b);
@@ -114,9 +117,9 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     float w_lanes[G], w_scale[G];
     auto load_w_scales = [&](int b) {
         const int at = b + lane + before;
-        w_lanes[0] = at < blocks ? p.w_scales[wb + at] : 0.0f;
+        w_lanes[0] = at < k_end ? p.w_scales[wb + at] : 0.0f;
         if constexpr (GATED)
-            w_lanes[1] = at < blocks ? p.up_scales[wb + at] : 0.0f;
+            w_lanes[1] = at < k_end ? p.up_scales[wb + at] : 0.0f;
         // wait here, not where they are used: that is in the loop below, and the
         // wait would be for its direct loads too
 #pragma unroll
@@ -162,8 +165,8 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 #pragma unroll
         for (int j = 0; j < MJ; j++) {
             sx[j] = lds_read<float>(at, 256 * j);
-            if (KS > 1) // blocks past K: what lies there is no scale
-                sx[j] = b + before < blocks ? sx[j] : 0.0f;
+            if (KS > 1) // blocks past the end: what lies there is no scale
+                sx[j] = b + before < k_end ? sx[j] : 0.0f;
         }
     };
     // The additions of a tile follow its matrix instruction kLag tiles behind,
@@ -354,7 +357,9 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     constexpr int kValue = STORE == kCodes ? 1 : STORE == kF32 ? 4 : 2, kPerPiece = 16 / kValue;
     constexpr int kRow = 16 * NO * kValue, kPieces = kRow / 16; // bytes, 16-byte pieces
     const uint32_t mine = base + wave * (16 * MJ * kRow);
-    static_assert(T::kWaves * 16 * MJ * kRow + 4 * T::NW * T::kRowsX <= kGroup);
+    // (A part of K's sums of the largest tiles do not fit: 64 bytes of each row.)
+    constexpr bool kFits = T::kWaves * 16 * MJ * kRow + 4 * T::NW * T::kRowsX <= kGroup;
+    static_assert(kFits || STORE == kF32);
     auto put = [&](int i, int j, auto v) { // columns 16 i + 4 g .. + 3 of row 16 j + r
         const int line = 16 * j + r, at = (16 * i + 4 * g) * kValue;
         lds_write(mine + line * kRow + ((at / 16) ^ (line % kPieces)) * 16 + at % 16, v);
@@ -424,6 +429,18 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
             }
         }
         store(out_codes, p.n);
+    } else if constexpr (!kFits) {
+        float *y = static_cast<float *>(p.y) + blockIdx.y * (p.m * p.ldy);
+#pragma unroll
+        for (int j = 0; j < MJ; j++) {
+            const int64_t line = m0 + 16 * (wm * MJ + j) + r;
+#pragma unroll
+            for (int i = 0; i < NO; i++) {
+                const int64_t n = col0 + 16 * i + 4 * g; // p.n and p.ldy are multiples of 4
+                if (line < p.m && n < p.n)
+                    *reinterpret_cast<v4f *>(y + line * p.ldy + n) = acc[i][j];
+            }
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < MJ; j++)
@@ -436,7 +453,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
                     put(i, j, v2u{bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
                                   bf16_bits(v[2]) | bf16_bits(v[3]) << 16});
             }
-        store(p.y, p.ldy);
+        store(static_cast<uint8_t *>(p.y) + blockIdx.y * (p.m * p.ldy * kValue), p.ldy);
     }
 }
 
@@ -454,8 +471,10 @@ hipError_t launch_tile(const Fp8Problem &p, const Fp8Part &part, uint8_t *codes,
     constexpr int kCols = T::kRowsW / (GATED ? 2 : 1);
     const int64_t tiles =
         (p.m + T::kRowsX - 1) / T::kRowsX * ((part.cols + kCols - 1) / kCols);
-    fp8_tile_kernel<T, GATED, EXACT, STORE><<<(unsigned)tiles, 64 * T::kWaves * T::KS, 0, s>>>(
-        p, part.first, part.cols, codes, scales);
+    const int64_t blocks = fp8_blocks(p.k), splits = part.splits > 1 ? part.splits : 1;
+    fp8_tile_kernel<T, GATED, EXACT, STORE>
+        <<<dim3((unsigned)tiles, (unsigned)splits), 64 * T::kWaves * T::KS, 0, s>>>(
+            p, part.first, part.cols, (int)((blocks + splits - 1) / splits), codes, scales);
     return hipGetLastError();
 }
 
@@ -555,6 +574,21 @@ template <int N> float plan(const Cost (&costs)[N], const Fp8Problem &p, Fp8Plan
     return whole;
 }
 
+// y = the splits' sums [splits][m][n], in their order, as bf16
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float *sums, int splits, int64_t m,
+                                                       int64_t n, uint16_t *y, int64_t ldy)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; // n is a multiple of 4
+    if (i >= m * n)
+        return;
+    v4f sum = *reinterpret_cast<const v4f *>(sums + i);
+    for (int q = 1; q < splits; q++)
+        sum += *reinterpret_cast<const v4f *>(sums + q * m * n + i);
+    const v2u v{bf16_bits(sum[0]) | bf16_bits(sum[1]) << 16,
+                bf16_bits(sum[2]) | bf16_bits(sum[3]) << 16};
+    __builtin_memcpy(__builtin_assume_aligned(y + i / n * ldy + i % n, 2), &v, 8);
+}
+
 hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
 {
     if (p.exact) {
@@ -601,10 +635,28 @@ Fp8Plan plan_fp8_gemm(const Fp8Problem &p)
     if (streams(p))
         return streamed(p);
     Fp8Plan values;
-    if (p.exact)
+    if (p.exact) {
         plan(kExact, p, &values);
-    else
-        plan(kFast, p, &values);
+        return values;
+    }
+    const float whole = plan(kFast, p, &values);
+    if (p.up || p.n % 4 != 0)
+        return values;
+    // The largest tiles over a part of K each, where there are few of them: the
+    // sums are written and read again, at 5 TB/s.  1024 x 17408 x 5120, 80 tiles:
+    // 143 us by halves of them, 97 over three parts.
+    float best = whole;
+    const Cost &c = kFast[0];
+    const int64_t tiles = tiles_of(c, p.m, p.n, 1), blocks = fp8_blocks(p.k);
+    for (int splits = 2; splits <= 8 && tiles * splits <= 2 * c.slots && 8 * splits <= blocks; splits++) {
+        const float t = time_of(c, tiles * splits, (blocks + splits - 1) / splits) + kLaunch +
+                        (float)(p.m * p.n) * (float)(8 * splits + 2) / 5e6f;
+        if (t < best) {
+            best = t;
+            values = Fp8Plan{};
+            values.part[0] = {c.kernel, 0, p.n, splits};
+        }
+    }
     return values;
 }
 
@@ -658,9 +710,28 @@ hipError_t launch_plan(const Fp8Problem &p, const Fp8Plan &plan, hipStream_t s)
 
 } // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Problem &p, hipStream_t s)
+size_t fp8_gemm_bytes(const Fp8Problem &p)
 {
-    return launch_plan(p, plan_fp8_gemm(p), s);
+    const int64_t splits = plan_fp8_gemm(p).part[0].splits;
+    return splits > 1 ? (size_t)(splits * p.m * p.n) * sizeof(float) : 0;
+}
+
+hipError_t launch_fp8_gemm(const Fp8Problem &p, void *workspace, hipStream_t s)
+{
+    const Fp8Plan plan = plan_fp8_gemm(p);
+    const int splits = plan.part[0].splits;
+    if (splits < 2)
+        return launch_plan(p, plan, s);
+    Fp8Problem sums = p;
+    sums.y = workspace;
+    sums.ldy = p.n;
+    const hipError_t e =
+        launch_tile<Tile256x256, false, false, kF32>(sums, plan.part[0], nullptr, nullptr, s);
+    if (e != hipSuccess)
+        return e;
+    fp8_join_kernel<<<(unsigned)((p.m * p.n / 4 + 255) / 256), 256, 0, s>>>(
+        static_cast<const float *>(workspace), splits, p.m, p.n, static_cast<uint16_t *>(p.y), p.ldy);
+    return hipGetLastError();
 }
 
 size_t fp8_gated_quantize_bytes(const Fp8Problem &p)

@@ -758,6 +758,9 @@ PyObject *fp8_product(const char *where, PyObject *const *a, bool gated)
         const c10::Device device =
             one_device(where, {&o.codes, &o.scales, &o.w, &o.w_scales, &o.up, &o.up_scales, &y});
         const c10::DeviceGuard guard(device);
+        // on the current stream, like the call: free for the next one behind it
+        const int64_t bytes = gated ? 0 : (int64_t)::fp8_gemm_bytes(o.m, o.n, o.k, y_dt);
+        const at::Tensor workspace = bytes ? make({bytes}, at::kByte, o.codes) : at::Tensor();
         check_status(where, unlocked([&] {
                          const int64_t ldy = row_stride(y, 1);
                          if (gated)
@@ -768,7 +771,8 @@ PyObject *fp8_product(const char *where, PyObject *const *a, bool gated)
                                  stream_of(device));
                          return ::fp8_gemm(address(o.codes), address<float>(o.scales), o.m,
                                            address(o.w), address<float>(o.w_scales), o.n, o.k,
-                                           address(y), y_dt, ldy, stream_of(device));
+                                           address(y), y_dt, ldy, address(workspace), (size_t)bytes,
+                                           stream_of(device));
                      }));
         return made ? wrap(y) : (Py_INCREF(given), given);
     });

@@ -537,11 +537,15 @@ bpg_status quantize_fp8(const void *x, bpg_x_dtype dt, int64_t m, int64_t k, int
  * instruction, which takes eight consecutive k at a time and may drop from each
  * product what is below 2^-12 of the largest of the eight: an error of at most
  * 2^-9 of the sum over the eights of their largest product, typically 2e-5 of y.
- * Errors: NULL, SHAPE, ALIGN, DTYPE, DEVICE, LAUNCH.
+ * workspace is device memory of fp8_gemm_bytes(m, n, k, y_dt) bytes at least (may
+ * be 0), 16-byte aligned, written and read by the call's kernels only: calls that
+ * can run at one time need one each.
+ * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
  */
+size_t fp8_gemm_bytes(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt);
 bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const void *w_codes,
                     const float *w_scales, int64_t n, int64_t k, void *y, bpg_x_dtype y_dt,
-                    int64_t ldy, void *stream);
+                    int64_t ldy, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * fp8_gemm_gated: the gated feed-forward block's y = act(x . gate^T) *
@@ -549,10 +553,8 @@ bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const voi
  * and up are [f][k] codes with scales of their own, y [m][ldy], ldy >= f.
  * fp8_gemm_gated_quantize: the same values in fp32, products as with y bf16,
  * written as quantize_fp8 does: codes [m][f], scales [m][ceil(f/128)], f a
- * multiple of 32: what fp8_gemm reads for the down projection.  workspace is
- * device memory of fp8_gemm_gated_quantize_bytes(m, f, k) bytes at least (may be
- * 0), 16-byte aligned, written and read by the call's kernels only: calls that
- * can run at one time need one each.
+ * multiple of 32: what fp8_gemm reads for the down projection.  workspace as
+ * fp8_gemm's, of fp8_gemm_gated_quantize_bytes(m, f, k) bytes at least.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
  */
 bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,

@@ -48,8 +48,8 @@ def test_quantize_abi_valid_calls_reach_the_device_check(args):
     assert quantize(**args) == DEVICE
 
 
-def product(codes=P, scales=P, m=4, w=P, ws=P, n=70, k=160, y=P, dt=0, ldy=70):
-    return bb.lib().fp8_gemm(codes, scales, m, w, ws, n, k, y, dt, ldy, NUL)
+def product(codes=P, scales=P, m=4, w=P, ws=P, n=70, k=160, y=P, dt=0, ldy=70, work=P, size=1 << 62):
+    return bb.lib().fp8_gemm(codes, scales, m, w, ws, n, k, y, dt, ldy, work, size, NUL)
 
 
 PRODUCT = [
@@ -63,7 +63,7 @@ PRODUCT = [
 ]
 
 
-@pytest.mark.parametrize("args,status", PRODUCT)
+@pytest.mark.parametrize("args,status", PRODUCT + [(dict(work=MIS), ALIGN)])
 def test_product_abi_refusals(args, status):
     assert product(**args) == status
 
@@ -75,6 +75,23 @@ def test_product_abi_refusals(args, status):
 ])
 def test_product_abi_valid_calls_reach_the_device_check(args):
     assert product(**args) == DEVICE
+
+
+@pytest.mark.parametrize("m,n,k,dt", [(4, 70, 160, 0), (512, 5120, 17408, 1), (1024, 5120, 17408, 1),
+                                      (300, 300, 4096, 1), (0, 64, 64, 1)])
+def test_product_workspace(m, n, k, dt):
+    need = bb.lib().fp8_gemm_bytes(m, n, k, dt)
+    args = dict(m=m, n=n, k=k, dt=dt, ldy=n)
+    if need:
+        assert product(size=need - 1, **args) == BUFFER
+        assert product(size=need, work=NUL, **args) == NULL
+    if not torch.cuda.is_available():
+        assert product(size=need, **args) == DEVICE
+        if not need:
+            assert product(size=0, work=NUL, **args) == DEVICE
+    assert need or (n, k, dt) != (5120, 17408, 1)
+    for bad in ((-1, n, k, dt), (m, 0, k, dt), (m, n, 31, dt), (m, n, k, 2)):
+        assert bb.lib().fp8_gemm_bytes(*bad) == 0
 
 
 def gated(codes=P, scales=P, m=4, w=P, ws=P, u=P, us=P, n=96, k=160, act=2, y=P, dt=0, ldy=96):

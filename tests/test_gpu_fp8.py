@@ -121,7 +121,7 @@ def test_quantize_empty(torch):
 # ------------------------------------------------------------------ products
 
 # every kernel and both sides of its limits; odd rows and columns, K that ends inside a block
-SHAPES = [(1, 1, 32), (1, 16, 96), (1, 128, 128), (2, 300, 160), (15, 129, 352), (16, 512, 1024),
+SHAPES = [(300, 256, 8192), (260, 516, 4128), (1, 1, 32), (1, 16, 96), (1, 128, 128), (2, 300, 160), (15, 129, 352), (16, 512, 1024),
           (17, 100, 256), (31, 640, 544), (33, 257, 128), (64, 384, 2080), (65, 130, 160),
           (128, 256, 512), (130, 1061, 352), (200, 512, 1152), (257, 300, 416), (300, 1536, 288),
           (513, 257, 800), (1000, 2048, 256), (33, 5120, 5120), (1, 17408, 1024)]
