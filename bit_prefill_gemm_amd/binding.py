@@ -792,8 +792,8 @@ def fp8_gemm_gated_quantize(codes, scales, gate: Fp8Weights, up: Fp8Weights,
 
 
 def fp8_gemm_kernel_name(m: int, n: int, k: int, dtype=None, gated: bool = False) -> str:
-    """The kernel that makes the first columns of fp8_gemm's (or fp8_gemm_gated's) result (host
-    only); dtype: torch.float32 unless given."""
+    """The kernel that fp8_gemm (or fp8_gemm_gated) runs (host only; see include/bpg.h); dtype:
+    torch.float32 unless given."""
     dt = X_BF16 if dtype is not None and dtype == _torch().bfloat16 else X_F32
     r = _lib_handle().fp8_gemm_kernel_name(m, n, k, dt, int(gated))
     if r is None:
@@ -802,7 +802,7 @@ def fp8_gemm_kernel_name(m: int, n: int, k: int, dtype=None, gated: bool = False
 
 
 def fp8_gemm_gated_quantize_kernel_name(m: int, f: int, k: int) -> str:
-    """The kernel that makes the first columns of fp8_gemm_gated_quantize's result (host only)."""
+    """The kernel that fp8_gemm_gated_quantize runs (host only; see include/bpg.h)."""
     r = _lib_handle().fp8_gemm_gated_quantize_kernel_name(m, f, k)
     if r is None:
         raise ValueError("fp8_gemm_gated_quantize_kernel_name: invalid sizes")

@@ -849,7 +849,8 @@ namespace {
 
 // rows of activations or weights: what a launch's grid and 32-bit row numbers hold
 constexpr int64_t kMaxFp8Rows = (int64_t)1 << 22;
-constexpr int64_t kMaxVocab = (int64_t)1 << 24;
+constexpr int64_t kMaxFp8Results = (int64_t)1 << 40;
+constexpr int64_t kMaxVocab = (int64_t)1 << 24, kMaxLogits = (int64_t)1 << 40;
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -857,8 +858,8 @@ bool act_ok(bpg_activation act) { return act >= BPG_ACT_NONE && act <= BPG_ACT_G
 
 bool fp8_shape(int64_t m, int64_t n, int64_t k)
 {
-    return m >= 0 && m <= kMaxFp8Rows && n >= 1 && n <= kMaxFp8Rows && k >= 1 && k % 32 == 0 &&
-           k <= kMaxGemmK;
+    return m >= 0 && m <= kMaxFp8Rows && n >= 1 && n <= kMaxFp8Rows && m * n <= kMaxFp8Results &&
+           k >= 1 && k % 32 == 0 && k <= kMaxGemmK;
 }
 
 // what a plan goes by (no pointer is followed)
@@ -1011,14 +1012,14 @@ const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_
     bpg::Fp8Problem p = shape_problem(m, n, k, gated != 0);
     p.y_bf16 = y_dt == BPG_X_BF16;
     p.exact = !p.y_bf16;
-    return bpg::fp8_kernel_name(bpg::plan_fp8_gemm(p).part[0].kernel);
+    return bpg::fp8_plan_name(bpg::plan_fp8_gemm(p));
 }
 
 const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
 {
     if (!fp8_shape(m, f, k) || f % 32 != 0)
         return nullptr;
-    return bpg::fp8_kernel_name(bpg::plan_fp8_codes(shape_problem(m, f, k, true)).part[0].kernel);
+    return bpg::fp8_plan_name(bpg::plan_fp8_codes(shape_problem(m, f, k, true)));
 }
 
 bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64_t m,
@@ -1057,7 +1058,7 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
 size_t token_logprobs_bytes(int64_t rows, int64_t vocab, int64_t topk)
 {
     if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || topk < 0 ||
-        topk > kMaxTopk)
+        topk > kMaxTopk || rows * vocab > kMaxLogits)
         return 0;
     return bpg::logprobs_bytes(rows, vocab, (int)topk);
 }
@@ -1071,7 +1072,7 @@ bpg_status token_logprobs(const void *logits, bpg_x_dtype dt, int64_t rows, int6
         return BPG_ERR_DTYPE;
     if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || ldl < vocab ||
         ldl > ((int64_t)1 << 40) || topk < 0 || topk > kMaxTopk || topk > vocab ||
-        rows * topk >= ((int64_t)1 << 31))
+        rows * topk >= ((int64_t)1 << 31) || rows * vocab > kMaxLogits)
         return BPG_ERR_SHAPE;
     const size_t need = rows > 0 ? bpg::logprobs_bytes(rows, vocab, (int)topk) : 0;
     if (rows > 0 && (!logits || (tokens && !logprobs) || (topk > 0 && (!ids || !top)) ||

@@ -67,7 +67,7 @@ struct Fp8Plan {
 };
 Fp8Plan plan_fp8_gemm(const Fp8Problem &p);
 Fp8Plan plan_fp8_codes(const Fp8Problem &p);
-const char *fp8_kernel_name(int kernel);
+const char *fp8_plan_name(const Fp8Plan &plan);
 
 constexpr int kFp8StreamRows = 32; // at most
 hipError_t launch_fp8_stream(const Fp8Problem &p, hipStream_t stream);

@@ -679,18 +679,32 @@ Fp8Plan plan_fp8_codes(const Fp8Problem &p)
     return staged < direct ? values : codes;
 }
 
-const char *fp8_kernel_name(int kernel)
+const char *fp8_plan_name(const Fp8Plan &plan)
 {
-    switch (kernel) {
-    case kFp8Stream: return "stream";
-    case kFp8Tile256x256: return "tile 256x256";
-    case kFp8Tile128x128Pair: return "tile 128x128 pair";
-    case kFp8Tile128x128: return "tile 128x128";
-    case kFp8Tile64x128: return "tile 64x128";
-    case kFp8Tile64x64: return "tile 64x64";
-    case kFp8Tile64x256: return "tile 64x256";
-    default: return "none";
-    }
+    static const char *const one[] = {"none",           "stream",      "tile 256x256",
+                                      "tile 128x128 pair", "tile 128x128", "tile 64x128",
+                                      "tile 64x64",     "tile 64x256"};
+    // the first columns' kernel is the one with the largest tiles there
+    static const char *const behind[] = {"",
+                                         "",
+                                         "tile 256x256, then tile 256x256",
+                                         "tile 256x256, then tile 128x128 pair",
+                                         "tile 256x256, then tile 128x128",
+                                         "tile 256x256, then tile 64x128",
+                                         "tile 256x256, then tile 64x64",
+                                         "tile 256x256, then tile 64x256"};
+    static const char *const pairs[] = {"",
+                                        "",
+                                        "",
+                                        "tile 128x128 pair, then tile 128x128 pair",
+                                        "",
+                                        "tile 128x128 pair, then tile 64x128",
+                                        "tile 128x128 pair, then tile 64x64",
+                                        ""};
+    const Fp8Part &first = plan.part[0], &rest = plan.part[1];
+    if (rest.cols > 0)
+        return (first.kernel == kFp8Tile256x256 ? behind : pairs)[rest.kernel];
+    return first.splits > 1 ? "tile 256x256 over parts of K" : one[first.kernel];
 }
 
 namespace {

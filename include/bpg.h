@@ -513,7 +513,7 @@ bpg_status moe_combine(const float *dn, int64_t lddn, int64_t rows, const int32_
  * block of a row or column holds what is left.  Codes are [rows][k] bytes,
  * scales [rows][KB] (activations) or [NB][KB] (weights) fp32, KB = ceil(k/128),
  * NB = ceil(n/128); a code c under scale d stands for c d.  K is a multiple of
- * 32, at most 2^22; N is any positive number; x, codes and weight scales are
+ * 32, at most 2^22; N is positive, M and N at most 2^22, M N 2^40; x, codes and weight scales are
  * 16-byte aligned, scales of activations 4-byte; y and its rows are aligned to
  * y's type.  Neither output may overlap another or an input.
  *
@@ -570,11 +570,11 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
                                    void *stream);
 
 /*
- * Routing queries, host only: the name of the kernel that makes the first
- * columns of fp8_gemm's or (gated) fp8_gemm_gated's result, and of
- * fp8_gemm_gated_quantize's: "stream", "tile 256x256", "tile 128x128 pair",
- * "tile 128x128", "tile 64x128", "tile 64x64" or "tile 64x256"; "none" for no
- * rows, NULL for sizes that the call refuses.
+ * Routing queries, host only: the kernel of fp8_gemm or (gated) fp8_gemm_gated,
+ * and of fp8_gemm_gated_quantize: "stream", "tile RxC" (rows by columns; gated:
+ * columns of both matrices), "tile 128x128 pair", "tile 256x256 over parts of K",
+ * or "A, then B" where the columns that fill the GPU in whole rounds and the rest
+ * have a kernel each; "none" for no rows, NULL for sizes that the call refuses.
  */
 const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_dt, int gated);
 const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k);
@@ -600,7 +600,8 @@ const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
  *              least (may be 0), 16-byte aligned; calls that can run at one time
  *              need one each
  * Neither output may overlap another or an input.
- * Limits: 1 <= vocab <= 2^24, 0 <= topk <= min(vocab, 64), rows * topk < 2^31.
+ * Limits: 1 <= vocab <= 2^24, 0 <= topk <= min(vocab, 64), rows * topk < 2^31,
+ * rows * vocab <= 2^40.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
  */
 typedef enum { BPG_I32 = 0, BPG_I64 = 1 } bpg_index_dtype;

@@ -186,6 +186,43 @@ def test_logprobs_workspace(rows, vocab, topk):
         assert bb.lib().token_logprobs_bytes(*bad) == 0
 
 
+# ------------------------------------------------------------------ routing
+
+def test_kernel_names_refuse_what_the_calls_refuse():
+    lib = bb.lib()
+    for bad in ((-1, 64, 64, 0, 0), (4, 0, 64, 0, 0), (4, 64, 48, 0, 0), (4, 64, 64, 2, 0),
+                (1 << 22, 1 << 22, 64, 0, 1)):
+        assert lib.fp8_gemm_kernel_name(*bad) is None
+    for bad in ((-1, 64, 64), (4, 33, 64), (4, 64, 0)):
+        assert lib.fp8_gemm_gated_quantize_kernel_name(*bad) is None
+    assert bb.fp8_gemm_kernel_name(0, 64, 64) == "none"
+    assert bb.fp8_gemm_gated_quantize_kernel_name(0, 64, 64) == "none"
+    with pytest.raises(ValueError):
+        bb.fp8_gemm_kernel_name(4, 64, 31)
+
+
+def test_every_kernel_has_a_tested_shape():
+    """The shapes of the GPU tests reach every kernel in every form."""
+    from test_gpu_fp8 import GATED, GATED_ODD, SHAPES
+    half = torch.bfloat16
+    name = bb.fp8_gemm_kernel_name
+    largest, pair = "tile 256x256", "tile 128x128 pair"
+    small = {"stream", pair, "tile 64x128", "tile 64x64"}
+    assert small | {largest, "tile 128x128", largest + " over parts of K"} <= {
+        name(*s, half) for s in SHAPES}
+    assert any(name(*s, half).startswith(largest + ", then") for s in SHAPES)
+    assert small <= {name(*s) for s in SHAPES}
+    assert any(name(*s).startswith(pair + ", then") for s in SHAPES)
+    gated = GATED + GATED_ODD
+    assert small | {largest, "tile 128x128"} <= {name(*s, half, gated=True) for s in gated}
+    assert any(name(*s, half, gated=True).startswith(largest + ", then") for s in gated)
+    assert small <= {name(*s, gated=True) for s in gated}
+    codes = {(bb.fp8_gemm_gated_quantize_kernel_name(*s),
+              bb.lib().fp8_gemm_gated_quantize_bytes(*s) > 0) for s in GATED}
+    assert {("stream", True), ("tile 64x64", True), ("tile 64x128", True), ("tile 64x256", False),
+            (largest, False), (largest + ", then tile 64x256", False)} <= codes
+
+
 # ------------------------------------------------------------------ binding
 
 def codes_of(m, k):

@@ -124,7 +124,9 @@ def test_quantize_empty(torch):
 SHAPES = [(300, 256, 8192), (260, 516, 4128), (1, 1, 32), (1, 16, 96), (1, 128, 128), (2, 300, 160), (15, 129, 352), (16, 512, 1024),
           (17, 100, 256), (31, 640, 544), (33, 257, 128), (64, 384, 2080), (65, 130, 160),
           (128, 256, 512), (130, 1061, 352), (200, 512, 1152), (257, 300, 416), (300, 1536, 288),
-          (513, 257, 800), (1000, 2048, 256), (33, 5120, 5120), (1, 17408, 1024)]
+          (513, 257, 800), (1000, 2048, 256), (33, 5120, 5120), (1, 17408, 1024),
+          (65, 4100, 160), (200, 4100, 160), (1500, 1300, 160), (1500, 1300, 2080), (2050, 4100, 160),
+          (1030, 17410, 544)]
 
 
 def small_codes(torch, g, m, k, top=3):
@@ -306,7 +308,10 @@ def act64(torch, g, act):
 
 GATED = [(1, 32, 32), (1, 1024, 5120), (2, 160, 96), (16, 288, 352), (17, 96, 160), (33, 416, 512),
          (65, 128, 1024), (77, 1056, 2080), (130, 640, 416), (200, 1280, 256), (300, 992, 544),
-         (513, 160, 288), (1024, 512, 256)]
+         (513, 160, 288), (1024, 512, 256), (65, 4096, 160), (65, 5120, 1056), (200, 4096, 160),
+         (200, 4096, 2080), (1030, 2048, 160), (1500, 2688, 160), (2050, 4096, 160)]
+
+GATED_ODD = [(5, 33, 64), (100, 1061, 160), (300, 129, 96), (200, 4100, 2080), (1030, 4100, 288), (1500, 2700, 160)]
 
 
 def gated_case(torch, m, f, k, seed):
@@ -336,7 +341,7 @@ def gated_reference(torch, c, s, gate, up, act, exact):
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-@pytest.mark.parametrize("m,f,k", GATED + [(5, 33, 64), (100, 1061, 160), (300, 129, 96)])
+@pytest.mark.parametrize("m,f,k", GATED + GATED_ODD)
 def test_gated(torch, m, f, k, dtype, act):
     dt = getattr(torch, dtype)
     c, s, gate, up = gated_case(torch, m, f, k, m + f + k)
@@ -371,7 +376,7 @@ def test_gated_quantize(torch, m, f, k, act):
 
 def test_gated_exact_relu(torch):
     """Whole codes: every kernel's gate and up columns are where they belong, bit for bit."""
-    for m, f, k in GATED + [(5, 33, 64), (300, 129, 96)]:
+    for m, f, k in GATED + GATED_ODD:
         g = generator(torch, m + f)
         c, s = small_codes(torch, g, m, k, 1), power_scales(torch, g, m, blocks(k))
 
