@@ -16,10 +16,11 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
 // weights) by 16 MJ rows.  Gated, the first half of a wave's NI row tiles are
 // rows of the gate and the second half the same rows of the up projection.
-template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_, bool ONE_ = false>
+template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_, int P_ = 0>
 struct Tile {
     static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_, KS = KS_, S = S_;
-    static constexpr bool ONE = ONE_;
+    static constexpr int P = P_; // loading waves of a group, 0: the others load
+    static constexpr int kLoaders = P ? P : NW_ * MW_, kThreads = 64 * KS_ * (NW_ * MW_ + P_);
     static constexpr int kWaves = NW * MW; // of a group
     static constexpr int kRowsW = 16 * NI * NW, kRowsX = 16 * MJ * MW;
 };
@@ -28,7 +29,7 @@ struct Tile {
 enum Store { kBf16, kF32, kCodes };
 
 template <class T, bool GATED, bool EXACT, Store STORE>
-__global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
+__global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
     const Fp8Problem p, int64_t col_first, int64_t cols, int k_each, uint8_t *out_codes,
     float *out_scales)
 {
@@ -39,8 +40,11 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     constexpr int kGroup = S * kStage + 2 * kScales;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[KS * kGroup];
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % T::kWaves;
-    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / T::kWaves;
+    // the waves that multiply come first, then those that load (P of a group)
+    const int number = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool loads = T::P > 0 && number >= T::kWaves * KS;
+    const int wave = loads ? (number - T::kWaves * KS) % T::kLoaders : number % T::kWaves;
+    const int group = loads ? (number - T::kWaves * KS) / T::kLoaders : number / T::kWaves;
     const int wn = wave % T::NW, wm = wave / T::NW;
     const int r = lane & 15, g = lane >> 4;
     // ---- which tile: every XCD a stretch of them, in panels of eight row tiles
@@ -71,11 +75,12 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const v4i ss = buffer_of(p.scales, m0, p.m, (int64_t)blocks * 4, T::kRowsX);
     // scales: 64 rows of 16 bytes an instruction, every fourth block
     constexpr int kScaleWaves = T::kRowsX / 64;
-    static_assert(kScaleWaves <= T::kWaves);
+    static_assert(kScaleWaves <= T::kLoaders);
     const uint32_t slane = (uint32_t)((64 * wave + lane) * blocks) * 4;
     // What a stage brings comes in two groups: x, the scales and each wave's
     // first half of w's row tiles; and their second half.
-    constexpr int kLoadsX = T::kRowsX / 8 / T::kWaves, kLoadsW = T::kRowsW / 16 / T::kWaves;
+    constexpr int kLoadsX = T::kRowsX / 8 / T::kLoaders, kLoadsW = T::kRowsW / 16 / T::kLoaders;
+    static_assert(kLoadsX * 8 * T::kLoaders == T::kRowsX && kLoadsW * 16 * T::kLoaders == T::kRowsW);
     constexpr int kFirst = kLoadsX + kLoadsW, kSecond = kLoadsW;
     // a group's block b is block b + before of K; blockIdx.y: which k_each blocks
     // of K the workgroup takes
@@ -84,7 +89,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     auto at_of = [&](int b) { return (uint32_t)(b + before) * kFp8Block; };
     auto load_w = [&](uint32_t to, int b, uint32_t l, int half, int u) {
         constexpr int kHalf = 8 * NI, kParts = kHalf / 8; // rows and loads of a wave's half
-        const int i = wave + T::kWaves * u, owner = i / kParts, row = i % kParts * 8;
+        const int i = wave + T::kLoaders * u, owner = i / kParts, row = i % kParts * 8;
         const int in = owner * 2 * kHalf + half * kHalf + row;
         const int col = GATED ? owner * kHalf + row : in;
         load16(GATED && half ? us : ws, to + kX + in * 128, l, (uint32_t)(col * k) + at_of(b));
@@ -96,7 +101,7 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     auto load_first = [&](int stage, int b, int u) {
         const uint32_t to = base + stage * kStage, l = lane_from(b);
         if (u < kLoadsX) {
-            const int i = wave + T::kWaves * u;
+            const int i = wave + T::kLoaders * u;
             load16(xs, to + 1024 * i, l, (uint32_t)(8 * i * k) + at_of(b));
         } else {
             load_w(to, b, l, 0, u - kLoadsX);
@@ -148,8 +153,8 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
     const uint32_t s_at = opaque(base + S * kStage + (wm * MJ * 16 + r) * 16);
     // w's row tiles are read kAhead tiles before their use
     constexpr int kAhead = 2;
-    constexpr int XS = T::ONE ? 2 : 1; // sets of x
-    static_assert(!T::ONE || S % 2 == 0);
+    constexpr int XS = T::P > 0 ? 2 : 1; // sets of x
+    static_assert(T::P == 0 || S % 2 == 0);
     Operand<EXACT> x[XS][MJ], w[kAhead];
     float sx[MJ], sv[G][MJ];
     auto read_w = [&](int stage, int i) {
@@ -216,29 +221,19 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
                     w_scale[q] = __uint_as_float(
                         __builtin_amdgcn_readlane(__float_as_uint(w_lanes[q]), b - b0));
             }
-            if (T::ONE ? i == 0 : i == kTurn + 1)
+            if (T::P == 0 && i == kTurn + 1)
                 load_scales((b & ~3) + 4, (b & 3) == 0);
-            if (T::ONE && i <= kLast) {
-                constexpr int kAll = kFirst + kSecond, kRowLoads = (kAll + kLast) / (kLast + 1);
-#pragma unroll
-                for (int u = i * kRowLoads; u < min((i + 1) * kRowLoads, kAll); u++) {
-                    if (u < kFirst)
-                        load_first((stage + S - 1) % S, b + S - 1, u);
-                    else
-                        load_second((stage + S - 1) % S, b + S - 1, u - kFirst);
-                }
-            }
-            if (T::ONE && i == NI - 1) {
+            if (T::P > 0 && i == NI - 1) {
 #pragma unroll
                 for (int j = 0; j < MJ; j++)
                     read_x(after, j);
             }
-            if (!T::ONE && i > kTurn && i <= kLast) {
+            if (T::P == 0 && i > kTurn && i <= kLast) {
 #pragma unroll
                 for (int u = (i - kTurn - 1) * kPerRow; u < min((i - kTurn) * kPerRow, kFirst); u++)
                     load_first(stage, b + S, u);
             }
-            if (!T::ONE && i == kLast + 1) {
+            if (T::P == 0 && i == kLast + 1) {
 #pragma unroll
                 for (int u = 0; u < kSecond; u++)
                     load_second(stage, b + S, u);
@@ -248,12 +243,12 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
                 const int t = i * MJ + j;
                 d[t % kRing] = dot(row, x[stage % XS][j]);
                 additions(t - kLag);
-                if (!T::ONE && i == NI - 1)
+                if (T::P == 0 && i == NI - 1)
                     read_x(after, j);
             }
-            if ((!T::ONE && i == kTurn) || i == kLast) {
+            if ((T::P == 0 && i == kTurn) || i == kLast) {
                 __builtin_amdgcn_sched_barrier(0);
-                arrived_all<(T::ONE ? S - 2 : S - 1) * (kFirst + kSecond)>();
+                arrived_all<(T::P > 0) ? 63 : (S - 1) * (kFirst + kSecond)>();
             }
             if (i < kLast)
                 read_w(stage, i + kAhead);
@@ -272,20 +267,50 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
         }
     };
 
-    load_scales(0, true);
+    // Waves of their own load, at three stages' distance: a wave that does both
+    // waits for the load unit while it could multiply.  One barrier a block: block
+    // b + 1 is there, and block b's w and the x behind it are read by everybody.
+    if (loads) {
+        constexpr int kAll = kFirst + kSecond;
+        auto load_all = [&](int stage, int b) {
 #pragma unroll
-    for (int q = 0; q < (T::ONE ? S - 1 : S); q++) {
+            for (int u = 0; u < kFirst; u++)
+                load_first(stage, b, u);
 #pragma unroll
-        for (int u = 0; u < kFirst; u++)
-            load_first(q, q, u);
-        if (!T::ONE && q == S - 1)
-            arrived_all<(S - 1) * (kFirst + kSecond)>();
+            for (int u = 0; u < kSecond; u++)
+                load_second(stage, b, u);
+        };
+        load_scales(0, true);
 #pragma unroll
-        for (int u = 0; u < kSecond; u++)
-            load_second(q, q, u);
+        for (int q = 0; q < S - 1; q++)
+            load_all(q, q);
+        arrived_all<(S - 2) * kAll>();
+        for (int b = 0; b < rounds; b++) {
+            load_scales((b & ~3) + 4, (b & 3) == 0);
+            load_all((b + S - 1) % S, b + S - 1);
+            arrived_all<(S - 2) * kAll>();
+        }
+        arrived_all<0>();
+        if (KS > 1)
+            __syncthreads();
+        return;
     }
-    if (T::ONE)
-        arrived_all<(S - 2) * (kFirst + kSecond)>();
+    if constexpr (T::P > 0) {
+        arrived_all<63>();
+    } else {
+        load_scales(0, true);
+#pragma unroll
+        for (int q = 0; q < S; q++) {
+#pragma unroll
+            for (int u = 0; u < kFirst; u++)
+                load_first(q, q, u);
+            if (q == S - 1)
+                arrived_all<(S - 1) * (kFirst + kSecond)>();
+#pragma unroll
+            for (int u = 0; u < kSecond; u++)
+                load_second(q, q, u);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kAhead; i++)
         read_w(0, i);
@@ -458,10 +483,10 @@ __global__ __launch_bounds__(64 * T::kWaves * T::KS, 2) void fp8_tile_kernel(
 }
 
 typedef Tile<8, 4, 2, 4, 1, 2> Tile256x256;
-typedef Tile<4, 4, 2, 2, 1, 4, true> Tile128x128;
+typedef Tile<4, 4, 2, 2, 1, 4, 4> Tile128x128;
 typedef Tile<4, 4, 2, 2, 1, 2> Tile128x128Pair; // two workgroups a CU
-typedef Tile<2, 2, 4, 2, 1, 4, true> Tile64x128;
-typedef Tile<2, 2, 2, 2, 2, 4, true> Tile64x64; // two halves of K
+typedef Tile<2, 2, 4, 2, 1, 4, 4> Tile64x128;
+typedef Tile<2, 2, 2, 2, 2, 4, 2> Tile64x64; // two halves of K
 typedef Tile<4, 4, 4, 1, 1, 3> Tile64x256;
 
 template <class T, bool GATED, bool EXACT, Store STORE>
@@ -473,7 +498,7 @@ hipError_t launch_tile(const Fp8Problem &p, const Fp8Part &part, uint8_t *codes,
         (p.m + T::kRowsX - 1) / T::kRowsX * ((part.cols + kCols - 1) / kCols);
     const int64_t blocks = fp8_blocks(p.k), splits = part.splits > 1 ? part.splits : 1;
     fp8_tile_kernel<T, GATED, EXACT, STORE>
-        <<<dim3((unsigned)tiles, (unsigned)splits), 64 * T::kWaves * T::KS, 0, s>>>(
+        <<<dim3((unsigned)tiles, (unsigned)splits), T::kThreads, 0, s>>>(
             p, part.first, part.cols, (int)((blocks + splits - 1) / splits), codes, scales);
     return hipGetLastError();
 }
