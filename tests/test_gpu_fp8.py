@@ -118,6 +118,21 @@ def test_quantize_empty(torch):
     assert codes.shape == (0, 64) and scales.shape == (0, 1)
 
 
+def test_quantize_more_rows_than_a_grid_holds(torch):
+    """2^29 blocks and some: 2^32 threads, over several launches."""
+    m, k = (1 << 29) + 77, 32
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    near = [slice(at, at + 64) for at in (0, (1 << 28) - 32, (1 << 29) - 32, m - 64)]
+    for i, s in enumerate(near):
+        x[s] = inputs(torch, 64, k, "normal", i).bfloat16().cuda()
+    codes, scales = bb.quantize_fp8(x)
+    for s in near:
+        q, d = plain_codes(torch, x[s].float().cpu(), 1)
+        assert torch.equal(scales[s].cpu(), d)
+        assert torch.equal(codes[s].view(torch.uint8).cpu(), q)
+    assert int(torch.count_nonzero(scales)) == 64 * len(near) - 19  # the last two overlap
+
+
 # ------------------------------------------------------------------ products
 
 # every kernel and both sides of its limits; odd rows and columns, K that ends inside a block

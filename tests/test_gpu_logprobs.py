@@ -204,3 +204,17 @@ def test_logits_past_4_gib(torch):
     assert torch.equal(ids[:, 1].long(), (at == 0).long())
     want = -math.log1p((vocab - 1) * math.exp(-20.0))
     assert (lp.double() - want).abs().max() <= U * 30 and torch.equal(lp, top[:, 0])
+
+
+def test_more_rows_than_a_grid_holds(torch):
+    """2^26 waves and some: 2^32 threads, over several launches."""
+    rows = (1 << 26) + 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.empty(rows, 2, dtype=torch.bfloat16, device="cuda").normal_(0, 3, generator=g)
+    tokens = torch.arange(rows, dtype=torch.int32, device="cuda") % 2
+    out = bb.token_logprobs(logits, tokens, topk=1)
+    for at in (0, (1 << 22) - 100, (1 << 25) - 100, (1 << 26) - 100, rows - 200):
+        s = slice(at, at + 200)
+        check(torch, logits[s], tokens[s], 1)
+        for a, b in zip(out, bb.token_logprobs(logits[s], tokens[s], topk=1)):
+            assert torch.equal(a[s], b)
