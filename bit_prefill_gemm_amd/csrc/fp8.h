@@ -1,6 +1,6 @@
 // fp8.h -- launchers of the 8-bit floating-point route (fp8_quantize.hip,
-// fp8_stream.hip) and of the log probabilities of tokens (logprobs.hip).  Not
-// part of the public interface (see include/bpg.h).
+// fp8_stream.hip, fp8_tile.hip) and of the log probabilities of tokens
+// (logprobs.hip).  Not part of the public interface (see include/bpg.h).
 #pragma once
 
 #include <hip/hip_runtime.h>

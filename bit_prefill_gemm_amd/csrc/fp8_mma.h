@@ -4,8 +4,8 @@
 // Both operands of v_mfma_f32_16x16x128_f8f6f4 take a lane's row (lane % 16)
 // and 32 codes of it; which k the 4 x 32 codes of the lanes of a row are does
 // not matter as long as both operands agree.  Here lane group g = lane / 16
-// holds bytes 16g..16g+15 and 64+16g..64+16g+15 of a block of 128, so that one
-// load of 16 bytes per lane covers 64 bytes of each row without a gap.  Result
+// holds bytes 16g..16g+15 and 64+16g..64+16g+15 of a block of 128: two 16-byte
+// reads from LDS, whose quarter waves meet different banks (fp8_lds.h).  Result
 // register i of a lane is row 4g + i of the first operand, row lane % 16 of the
 // second.
 //

@@ -1,11 +1,19 @@
-// fp8_stream.hip -- products of e4m3 codes whose operands go straight from
-// memory to registers (gfx950).
+// fp8_stream.hip -- products of e4m3 codes with few rows (gfx950).
 //
 //   y[m][n] = sum over blocks b of sx[m][b] sw[n / 128][b] * dot(x block, w block)
 //
-// and, gated, act(y_gate) * y_up.  A workgroup makes 16 columns of w (16 of
-// each matrix, gated) by 16 MT rows of x; its eight waves take the blocks of K
-// in turn and add their partial results through LDS, in wave order.
+// and, gated, act(y_gate) * y_up.  All that is read once is w, so this is a
+// stream of it: a workgroup makes 16 columns (16 of each matrix, gated) of all
+// rows, and each of its eight waves takes a part of K, whose blocks it brings to
+// a ring of its own in LDS by direct loads, two blocks on the way.  No wave waits
+// for another before the end, where their sums are added in wave order.
+//
+// Bound by memory where there are many columns (1 x 17408 x 5120, 89 MB: 19.7 us,
+// 4.5 TB/s; gated to codes 42.9 us, 4.2 TB/s) and by the time to fill and drain
+// where there are few (1 x 5120 x 5120: 7.9 us, 3.3 TB/s; 1 x 1024 x 5120: 4.6 us).
+// Blocks of K dealt to the waves in turn, straight to registers, took 20.7 us for
+// the first and 14.2 instead of 8.7 for 16 x 5120 x 5120, where a load of x or w
+// in the operands' shape keeps the load unit for 47 clocks (fp8_lds.h).
 #include "fp8.h"
 
 #include "epilogue.h"
@@ -36,7 +44,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Proble
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t k = p.k;
     const int blocks = (int)fp8_blocks(k), per = (blocks + kWaves - 1) / kWaves;
     const int first = min(wave * per, blocks), end = min(first + per, blocks);
@@ -46,8 +54,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Proble
     const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
     const v4i w0 = buffer_of(p.w, n0, p.n, k, 16);
     const v4i w1 = GATED ? buffer_of(p.up, n0, p.n, k, 16) : w0;
-    const v4i x = buffer_of(p.codes, m0, p.m, k, 8 * XL);
-    const v4i xs = buffer_of(p.scales, m0, p.m, (int64_t)blocks * 4, 8 * XL);
+    const v4i x = buffer_of(p.codes, 0, p.m, k, 8 * XL);
+    const v4i xs = buffer_of(p.scales, 0, p.m, (int64_t)blocks * 4, 8 * XL);
     const uint32_t slane = (uint32_t)(lane * blocks) * 4;
     auto load = [&](int slot, int b) {
         const uint32_t to = base + slot * R::kSlot, at = (uint32_t)b * kFp8Block;
@@ -64,13 +72,14 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Proble
             load16(x, to + 2048 * G + 1024 * u, l, (uint32_t)(8 * u * k) + at);
     };
     auto load_scales = [&](int c) { // of the wave's blocks 4 c .. 4 c + 3
-        load16_lanes((uint64_t)~0u >> (32 - 16 * MT), xs, base + D * R::kSlot + (c & 1) * 256 * MT, slane,
-                     (uint32_t)(first + 4 * c) * 4);
+        load16_lanes((uint64_t)~0u >> (32 - 16 * MT), xs,
+                     base + D * R::kSlot + (c & 1) * 256 * MT, slane, (uint32_t)(first + 4 * c) * 4);
     };
     const int64_t wb = n0 / kFp8Block * blocks;
     // scalar loads: vector ones would be counted with the direct loads
     typedef const __attribute__((address_space(4))) float *Scalars;
-    const Scalars s0 = (Scalars)(p.w_scales + wb), s1 = (Scalars)(GATED ? p.up_scales + wb : p.w_scales);
+    const Scalars s0 = (Scalars)(p.w_scales + wb);
+    const Scalars s1 = (Scalars)(GATED ? p.up_scales + wb : p.w_scales);
     float w_next[G];
     auto w_scales = [&](int b) {
         b = min(b, blocks - 1);
@@ -104,8 +113,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Proble
 #pragma unroll
         for (int j = 0; j < MT; j++) {
             c[j] = operand(2048 * (G + j));
-            sx[j] = lds_read<float>(base + D * R::kSlot + (i / 4 & 1) * 256 * MT + (i & 3) * 4 + r * 16,
-                                    256 * j);
+            sx[j] = lds_read<float>(
+                base + D * R::kSlot + (i / 4 & 1) * 256 * MT + (i & 3) * 4 + r * 16, 256 * j);
         }
         read_done();
         load(slot, b + D);
@@ -157,7 +166,7 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_stream_kernel(const Fp8Proble
         ep_activate(p.act, t);
         sum[0] = v4f{t[0], t[1], t[2], t[3]} * sum[G - 1];
     }
-    const int64_t row = m0 + 16 * j + r, n = n0 + 4 * g;
+    const int64_t row = 16 * j + r, n = n0 + 4 * g;
     if (row < p.m && n < p.n)
         store4(p.y, p.y_bf16, vec, row * p.ldy + n, (int)min((int64_t)4, p.n - n), sum[0]);
 }
@@ -175,7 +184,9 @@ template <int XL, bool EXACT> hipError_t launch(const Fp8Problem &p, hipStream_t
 
 template <bool EXACT> hipError_t stream(const Fp8Problem &p, hipStream_t s)
 {
-    return p.m <= 8 ? launch<1, EXACT>(p, s) : p.m <= 16 ? launch<2, EXACT>(p, s) : launch<4, EXACT>(p, s);
+    return p.m <= 8    ? launch<1, EXACT>(p, s)
+           : p.m <= 16 ? launch<2, EXACT>(p, s)
+                       : launch<4, EXACT>(p, s);
 }
 
 } // namespace

@@ -16,6 +16,20 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // A workgroup's tile: NW x MW waves, each of 16 NI columns of y (rows of the
 // weights) by 16 MJ rows.  Gated, the first half of a wave's NI row tiles are
 // rows of the gate and the second half the same rows of the up projection.
+// KS groups of such waves take a part of K each; S stages of one block of K are
+// in LDS, and P waves of a group do nothing but load them (0: the others do).
+//
+// What the tiles reach (bf16 results): 256x256 2400 TF at 8192 x 17408 x 5120
+// (602 to 620 us; the library's product of the same size under one scale for
+// everything 2500 TF), 128x128 1190 TF at 512 x 5120 x 5120 (22.5 us, 160
+// workgroups).  A block of 256x256 takes 2700 clocks of the matrix unit's 2048,
+// one of 128x128 1080 of 512.  What bounds them is the vector unit beside the
+// matrix unit: the block scales cost four additions per instruction, and while a
+// matrix instruction reads its operands (16 clocks) no other one is issued, so
+// that two waves of a SIMD need 37 clocks for 32 and one, alone, 45; the rest is
+// barriers and the first and last block.  32 x 32 instructions (half the reads,
+// but twice the registers per operand, so fewer of them in flight) took 663 us
+// at the first size and 22.9 at the second.
 template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_, int P_ = 0>
 struct Tile {
     static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_, KS = KS_, S = S_;
@@ -62,10 +76,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
     const int64_t k = p.k;
     const int blocks = (int)fp8_blocks(k);
 
-    // ---- direct loads.  Lane l of an instruction brings a 16-byte piece of row
-    //      l / 8: piece l % 8 of the row in LDS, which is piece (l % 8) ^ (l / 8)
-    //      of the row in memory, so that the 16 rows that a quarter wave reads at
-    //      one piece lie in different banks.
+    // ---- direct loads, eight rows an instruction (fp8_lds.h)
     const uint32_t base = lds_address(lds) + group * kGroup;
     const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;
     const uint32_t lane_at = (uint32_t)((lane >> 3) * k) + piece;
@@ -108,8 +119,9 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
         }
     };
     auto load_scales = [&](int b, bool now) { // of blocks b..b+3
-        load16_lanes(now && wave < kScaleWaves ? ~(uint64_t)0 : 0, ss, base + S * kStage + (b / 4 & 1) * kScales + 1024 * wave,
-                  slane, (uint32_t)(b + before) * 4);
+        load16_lanes(now && wave < kScaleWaves ? ~(uint64_t)0 : 0, ss,
+                     base + S * kStage + (b / 4 & 1) * kScales + 1024 * wave, slane,
+                     (uint32_t)(b + before) * 4);
     };
     auto load_second = [&](int stage, int b, int u) {
         load_w(base + stage * kStage, b, lane_from(b), 1, u);
@@ -175,9 +187,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
         }
     };
     // The additions of a tile follow its matrix instruction kLag tiles behind,
-    // into the next block's: the first ones add zeros.
+    // into the next block's: the first ones add zeros.  Row tile 0's, which take
+    // the block's scales, are never left for the next block.
     constexpr int kTiles = NI * MJ, kRing = 4;
-    constexpr int kLag = kRing - 1 < kTiles - MJ ? kRing - 1 : kTiles - MJ; // row tile 0's are never left for the next block
+    constexpr int kLag = kRing - 1 < kTiles - MJ ? kRing - 1 : kTiles - MJ;
     static_assert(kTiles % kRing == 0);
     v4f d[kRing];
 #pragma unroll
@@ -200,14 +213,14 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
         add_scaled(acc[i][j], d[t % kRing], sv[i / (NI / G)][j]);
     };
 
-    // One block of K from stage b & 1.  x and the first kAhead row tiles of w
-    // have been read; on the way the other stage arrives and this one is loaded
-    // anew:
+    // One block of K from its stage.  x and the first kAhead row tiles of w have
+    // been read; on the way the next stage arrives and, where these waves load,
+    // this one is loaded anew:
     //   at row tile kTurn: the second half of w is there, and x, the scales and
-    //     the first half are read by everybody: block b + 2's follow;
+    //     the first half are read by everybody: block b + S's follow;
     //   at row tile kLast: the next block's x, scales and first half are there,
     //     and this one's second half is read by everybody.
-    // Each load has about one and a half blocks' time to arrive.
+    // With two stages each load has about one and a half blocks' time to arrive.
     auto block = [&](auto stage_of, int b0, int b) {
         constexpr int stage = decltype(stage_of)::value, after = (stage + 1) % S;
         constexpr int kTurn = NI / 2 - kAhead, kLast = NI - kAhead;
@@ -267,9 +280,10 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
         }
     };
 
-    // Waves of their own load, at three stages' distance: a wave that does both
-    // waits for the load unit while it could multiply.  One barrier a block: block
-    // b + 1 is there, and block b's w and the x behind it are read by everybody.
+    // Waves of their own load, S - 1 blocks ahead: a wave that does both waits for
+    // the load unit while it could multiply (64x128, 256 x 5120 x 5120: 17.9 us,
+    // so 16.5).  One barrier a block, behind its last read of w: block b + 1 is
+    // there, and block b's stage is free.
     if (loads) {
         constexpr int kAll = kFirst + kSecond;
         auto load_all = [&](int stage, int b) {
@@ -513,7 +527,7 @@ hipError_t launch_values(const Fp8Problem &p, const Fp8Part &part, hipStream_t s
 
 // What a tile costs, in us on an MI355X: `fixed`, and per block of K with few
 // tiles on the chip (`light`) and with as many as it holds at once (`full`,
-// `slots` of them).  Measured at 5120 x 5120 to 17408 x 5120 with 128 to 8192
+// `slots` of them).  Fitted to 5120 x 5120 to 17408 x 5120 with 128 to 8192
 // rows; products whose codes are widened take longer.
 struct Cost {
     int kernel, rows, cols, slots;
@@ -669,7 +683,7 @@ Fp8Plan plan_fp8_gemm(const Fp8Problem &p)
         return values;
     // The largest tiles over a part of K each, where there are few of them: the
     // sums are written and read again, at 5 TB/s.  1024 x 17408 x 5120, 80 tiles:
-    // 143 us by halves of them, 97 over three parts.
+    // 143 us by halves of them, 103 over three parts.
     float best = whole;
     const Cost &c = kFast[0];
     const int64_t tiles = tiles_of(c, p.m, p.n, 1), blocks = fp8_blocks(p.k);

@@ -1,7 +1,8 @@
 // native.cpp -- the Python entry points of the operators between the products
 // (rmsnorm_quantize_act, dequantize_act, w4a4_gemm_epilogue, moe_route_topk),
 // of the 8-bit floating-point route (quantize_fp8, fp8_gemm, fp8_gemm_gated,
-// fp8_gemm_gated_quantize) and of token_logprobs, compiled: their tensor checks, output allocation and the call of the C ABI
+// fp8_gemm_gated_quantize) and of token_logprobs, compiled: their tensor checks,
+// output allocation and the call of the C ABI
 // (include/bpg.h).  Host code only; every step of the operators runs in
 // libbpg.so's kernels.
 //
