@@ -137,21 +137,30 @@ __device__ __forceinline__ Part over_wave(Part p)
     return p;
 }
 
-// parts of one row (in memory or LDS) as one
+__device__ __forceinline__ double last_lane(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// the last lane's part in every lane
+__device__ __forceinline__ Part everywhere(Part p)
+{
+    p.s = last_lane(p.s);
+    p.t = last_lane(p.t);
+    return p;
+}
+
+// parts of one row in LDS as one, a lane each (64 at most), in every lane
 __device__ __forceinline__ Part over_parts(const Part *parts, int count)
 {
-    Part all{0.0, 0.0, 0.0, -INFINITY, 0};
-    for (int i = 0; i < count; i++)
-        all.m = fmaxf(all.m, parts[i].m);
-    all.ref = reference(all.m);
-    for (int i = 0; i < count; i++) {
-        Part q = parts[i];
-        rescale(q, all.m, all.ref);
-        all.s += q.s;
-        all.t += q.t;
-        all.odd |= q.odd;
-    }
-    return all;
+    Part p{0.0, 0.0, 0.0, -INFINITY, 0};
+    const int lane = threadIdx.x & 63;
+    if (lane < count)
+        p = parts[lane];
+    return everywhere(over_wave(p));
 }
 
 // Sixteen logits of a thread in a step: groups of one 16-byte load each, the
@@ -378,14 +387,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     float least = 0;
     double log_s = 0;
     if (wave == 0) {
-        Part all;
-        if constexpr (WAVES > 1) {
-            all = over_parts(wave_parts, WAVES);
-        } else {
-            all = mine;
-            all.s = __shfl(mine.s, 63);
-            all.t = __shfl(mine.t, 63);
-        }
+        const Part all = WAVES > 1 ? over_parts(wave_parts, WAVES) : everywhere(mine);
         if (parts == 1)
             log_s = log_sum(all);
         if (threadIdx.x == 0) {
