@@ -8,9 +8,9 @@
 // are the largest logits, equal ones by the lowest id; a NaN counts as -inf
 // there.  A row with a NaN or +inf, or of -inf only, has no distribution: NaN.
 //
-// One pass over the logits: a thread holds 16 at a time, takes their maximum,
-// rescales its sums to it and adds the 16 terms (in fp32 among the 16, in fp64
-// from one 16 to the next).  For the alternatives it leaves each 16's maximum in
+// One pass over the logits: a thread holds 16 at a time and has 16 more on the
+// way, takes their maximum, rescales its sums to it and adds the 16 terms (in fp32
+// among the 16, in fp64 from one 16 to the next).  For the alternatives it leaves each 16's maximum in
 // LDS.  The k-th largest of 64 (or 128) groups' maxima is then below or at the k-th
 // largest logit, and few logits reach it (64 ln (64 / (64 - k)) on shuffled
 // rows: 24 for k = 20), so only the 16s that do are read again.  Where more than
@@ -20,14 +20,15 @@
 // Few rows are split into parts of 8192 logits or more, a workgroup each, and
 // another launch joins them.
 //
-// Bound by memory where there are many rows: 4096 x 131072 bf16, 1.07 GB, 202 us
-// (5.3 TB/s), fp32 2048 x 131072 190 us (5.7 TB/s).  Few or short rows are bound by
+// Bound by memory where there are many rows: 4096 x 131072 bf16, 1.07 GB, 189 us
+// (5.7 TB/s; 196 with an alternative), fp32 2048 x 131072 181 us (5.9 TB/s).  Few or short rows are bound by
 // the chain of their steps: the sums over a workgroup, the k-th of the groups'
-// maxima, the ranks, the join (1 x 131072 with 20 alternatives 13 us, 333 x 50001
-// with 5 19.5 us, 16 x 262144 with 64 27 us).
+// maxima, the ranks, the join (1 x 131072 with 20 alternatives 12 us, 333 x 50001
+// with 5 19 us, 16 x 262144 with 64 26 us).
 #include "fp8.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace bpg {
@@ -164,31 +165,42 @@ __device__ __forceinline__ Part over_parts(const Part *parts, int count)
 }
 
 // Sixteen logits of a thread in a step: groups of one 16-byte load each, the
-// threads' groups side by side.
+// threads' groups side by side.  Rows of more than one wave are loaded without a
+// branch, so that loads of later steps can be on the way: a group that would
+// pass the end is the last whole one instead, less what is not its own.
 template <bool BF16, int THREADS> struct Step {
     static constexpr int kGroups = BF16 ? 2 : 4, kPer = kEach / kGroups;
+    static constexpr bool kWhole = THREADS > 64; // of a row of kPer logits or more
     v4u raw[kGroups];
     static __device__ __forceinline__ int64_t id(int64_t at, int q)
     {
         return at + (int64_t)q * (THREADS * kPer) + threadIdx.x * kPer;
     }
+    // logit e of group q of the step that begins at `at`: is it the group's own?
+    static __device__ __forceinline__ bool own(int64_t at, int q, int e, int64_t end)
+    {
+        return kWhole ? id_of(at, q, e, end) >= id(at, q) : id(at, q) + e < end;
+    }
+    static __device__ __forceinline__ int64_t id_of(int64_t at, int q, int e, int64_t end)
+    {
+        return (kWhole ? min(id(at, q), end - kPer) : id(at, q)) + e;
+    }
     static __device__ __forceinline__ const uint8_t *address(const void *row, int64_t i)
     {
         return static_cast<const uint8_t *>(row) + i * (BF16 ? 2 : 4);
     }
-    // the step that begins at logit `at`; -inf past `end`
     __device__ __forceinline__ void load(const void *row, int64_t at, int64_t end)
     {
 #pragma unroll
         for (int q = 0; q < kGroups; q++) {
-            const int64_t i = id(at, q);
-            if (i + kPer <= end) {
+            const int64_t i = id_of(at, q, 0, end);
+            if (kWhole || i + kPer <= end) {
                 __builtin_memcpy(&raw[q], __builtin_assume_aligned(address(row, i), BF16 ? 2 : 4), 16);
                 continue;
             }
 #pragma unroll
             for (int e = 0; e < kPer; e++) {
-                uint32_t v = BF16 ? 0xff80u : 0xff800000u;
+                uint32_t v = BF16 ? 0xff80u : 0xff800000u; // -inf
                 if (i + e < end)
                     v = BF16 ? *reinterpret_cast<const uint16_t *>(address(row, i + e))
                              : *reinterpret_cast<const uint32_t *>(address(row, i + e));
@@ -199,12 +211,18 @@ template <bool BF16, int THREADS> struct Step {
             }
         }
     }
-    __device__ __forceinline__ void values(float (&v)[kEach]) const
+    // -inf for those that are not the thread's own
+    __device__ __forceinline__ void values(float (&v)[kEach], int64_t at, int64_t end) const
     {
 #pragma unroll
         for (int i = 0; i < kEach; i++) {
             const uint32_t w = raw[i / kPer][BF16 ? i % kPer / 2 : i % kPer];
             v[i] = __uint_as_float(!BF16 ? w : i & 1 ? w & 0xffff0000u : w << 16);
+        }
+        if (kWhole && at + THREADS * kEach > end) {
+#pragma unroll
+            for (int i = 0; i < kEach; i++)
+                v[i] = own(at, i / kPer, i % kPer, end) ? v[i] : -INFINITY;
         }
     }
 };
@@ -329,48 +347,56 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
 
     // ---- the sums
     Part mine{0.0, 0.0, 0.0, -INFINITY, 0};
-    Logits now, next;
-    now.load(row, begin, end);
     int steps = 0;
-    for (int64_t at = begin; at < end; at += kStep, steps++) {
-        if (at + kStep < end)
-            next.load(row, at + kStep, end);
+    auto step = [&](const Logits &now, int64_t at) {
         float v[kEach];
-        now.values(v);
-        float top = v[0], low = v[0];
+        now.values(v, at, end);
+        float top = v[0];
 #pragma unroll
-        for (int i = 1; i < kEach; i++) { // NaN is dropped
+        for (int i = 1; i < kEach; i++) // NaN is dropped
             top = fmaxf(top, v[i]);
-            low = fminf(low, v[i]);
-        }
         if (TOP)
             tops[steps][threadIdx.x] = above(top == top ? top : -INFINITY);
         const float m = fmaxf(mine.m, top);
+        const float ref = m * kLog2e;
         float e[kEach], t[4] = {0, 0, 0, 0};
-        if (__builtin_amdgcn_ballot_w64(!(low > -1e38f && top < 1e38f)) == 0) {
-            // nothing is masked: a NaN makes the sums NaN
-            const float ref = m * kLog2e;
-            rescale(mine, m, ref);
 #pragma unroll
-            for (int i = 0; i < kEach; i++) {
-                const float x = __builtin_fmaf(v[i], kLog2e, -ref);
-                e[i] = __builtin_amdgcn_exp2f(x);
-                t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
-            }
-        } else {
+        for (int i = 0; i < kEach; i++) {
+            const float x = __builtin_fmaf(v[i], kLog2e, -ref);
+            e[i] = __builtin_amdgcn_exp2f(x);
+            t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
+        }
+        double by = ref;
+        if (__ballot(!(sum_of(t) > -FLT_MAX)) != 0) {
+            // something is masked (x is -inf or NaN, x 2^x NaN), or no number: again,
             // x held to -250 and above, where 2^x is 0; NaN is dropped, and told
-            rescale(mine, m, reference(m));
+            by = reference(m);
 #pragma unroll
             for (int i = 0; i < kEach; i++) {
                 const float x = fmaxf((v[i] - m) * kLog2e, -250.0f);
                 e[i] = __builtin_amdgcn_exp2f(x);
-                t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
+                t[i % 4] = __builtin_fmaf(x, e[i], i < 4 ? 0.0f : t[i % 4]);
                 mine.odd |= !(v[i] < INFINITY);
             }
         }
+        rescale(mine, m, by);
         mine.s += (double)sum_of(e);
         mine.t += (double)sum_of(t);
-        now = next;
+        steps++;
+    };
+    constexpr int kRing = WAVES > 1 ? 2 : 1; // steps in registers, all but one on the way
+    Logits ring[kRing];
+#pragma unroll
+    for (int u = 0; u < kRing - 1; u++)
+        ring[u].load(row, begin + u * kStep, end);
+    for (int64_t at = begin; at < end; at += kRing * kStep) {
+#pragma unroll
+        for (int u = 0; u < kRing; u++) {
+            const int64_t here = at + u * kStep;
+            ring[(u + kRing - 1) % kRing].load(row, here + (kRing - 1) * kStep, end);
+            if (here < end)
+                step(ring[u], here);
+        }
     }
     const float top = mine.m;
     mine = over_wave(mine);
@@ -460,14 +486,16 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
             const int64_t at = begin + (int64_t)s * kStep;
             if (__uint_as_float((uint32_t)tops[s][threadIdx.x] << 16) < least)
                 continue;
-            now.load(row, at, end);
+            Logits again;
+            again.load(row, at, end);
             float v[kEach];
-            now.values(v);
+            again.values(v, at, end);
 #pragma unroll
             for (int i = 0; i < kEach; i++) {
-                const int64_t id = Logits::id(at, i / Logits::kPer) + i % Logits::kPer;
+                const int q = i / Logits::kPer, e = i % Logits::kPer;
+                const int64_t id = Logits::id_of(at, q, e, end);
                 const float l = v[i] == v[i] ? v[i] : -INFINITY;
-                if (l >= least && id < end) {
+                if (l >= least && Logits::own(at, q, e, end)) {
                     const int slot = atomicAdd(&count, 1); // the order decides nothing
                     if (slot < kCandidates)
                         words[slot] = word_of(l, (uint32_t)id);
