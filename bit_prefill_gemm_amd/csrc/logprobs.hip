@@ -24,7 +24,7 @@
 // (5.7 TB/s; 196 with an alternative), fp32 2048 x 131072 181 us (5.9 TB/s).  Few or short rows are bound by
 // the chain of their steps: the sums over a workgroup, the k-th of the groups'
 // maxima, the ranks, the join (1 x 131072 with 20 alternatives 12 us, 333 x 50001
-// with 5 19 us, 16 x 262144 with 64 26 us).
+// with 5 19 us, masked or not, 16 x 262144 with 64 26 us).
 #include "fp8.h"
 
 #include <algorithm>
@@ -47,9 +47,8 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 // rounding relative to x, however large the logits are.
 struct Part {
     double ref;
-    double s, t;  // 0 where m is -inf
-    float m;      // the largest logit, -inf if there is none
-    uint32_t odd; // a NaN or +inf among them (s may be NaN instead)
+    double s, t; // 0 where m is -inf; NaN with a NaN or +inf among them
+    float m;     // the largest logit, -inf if there is none
 };
 
 // An order of the logits and their ids in one word: larger words are larger
@@ -134,7 +133,6 @@ __device__ __forceinline__ Part over_wave(Part p)
     rescale(p, m, reference(m));
     p.s = sum_to_last(p.s);
     p.t = sum_to_last(p.t);
-    p.odd = __ballot(p.odd != 0) != 0;
     return p;
 }
 
@@ -157,7 +155,7 @@ __device__ __forceinline__ Part everywhere(Part p)
 // parts of one row in LDS as one, a lane each (64 at most), in every lane
 __device__ __forceinline__ Part over_parts(const Part *parts, int count)
 {
-    Part p{0.0, 0.0, 0.0, -INFINITY, 0};
+    Part p{0.0, 0.0, 0.0, -INFINITY};
     const int lane = threadIdx.x & 63;
     if (lane < count)
         p = parts[lane];
@@ -271,7 +269,7 @@ __device__ __forceinline__ Token token_of(const LogprobsProblem &p, int64_t r, c
 // log2 S, NaN for a row without a distribution
 __device__ __forceinline__ double log_sum(const Part &all)
 {
-    return all.odd || all.m == -INFINITY ? NAN : log2(all.s);
+    return all.m == -INFINITY ? NAN : log2(all.s);
 }
 
 __device__ __forceinline__ float log_probability(const Part &all, double log_s, float logit)
@@ -346,8 +344,9 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         token = token_of<BF16>(p, r, row);
 
     // ---- the sums
-    Part mine{0.0, 0.0, 0.0, -INFINITY, 0};
+    Part mine{0.0, 0.0, 0.0, -INFINITY};
     int steps = 0;
+    bool masked = false;
     auto step = [&](const Logits &now, int64_t at) {
         float v[kEach];
         now.values(v, at, end);
@@ -360,24 +359,29 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         const float m = fmaxf(mine.m, top);
         const float ref = m * kLog2e;
         float e[kEach], t[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const float x = __builtin_fmaf(v[i], kLog2e, -ref);
-            e[i] = __builtin_amdgcn_exp2f(x);
-            t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
-        }
         double by = ref;
-        if (__ballot(!(sum_of(t) > -FLT_MAX)) != 0) {
-            // something is masked (x is -inf or NaN, x 2^x NaN), or no number: again,
-            // x held to -250 and above, where 2^x is 0; NaN is dropped, and told
-            by = reference(m);
+        bool again = masked; // logits of -inf or next to it
+        if (!masked) { // x is -inf or NaN where it is, and x 2^x NaN
 #pragma unroll
             for (int i = 0; i < kEach; i++) {
-                const float x = fmaxf((v[i] - m) * kLog2e, -250.0f);
+                const float x = __builtin_fmaf(v[i], kLog2e, -ref);
+                e[i] = __builtin_amdgcn_exp2f(x);
+                t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
+            }
+            again = __ballot(!(sum_of(t) > -FLT_MAX)) != 0;
+        }
+        if (again) { // x held to -250 and above, where 2^x is 0; NaN stays
+            by = reference(m);
+            const float from = m == -INFINITY ? 0.0f : m;
+            float low = v[0];
+#pragma unroll
+            for (int i = 0; i < kEach; i++) {
+                low = fminf(low, v[i]);
+                const float x = __builtin_elementwise_maximum((v[i] - from) * kLog2e, -250.0f);
                 e[i] = __builtin_amdgcn_exp2f(x);
                 t[i % 4] = __builtin_fmaf(x, e[i], i < 4 ? 0.0f : t[i % 4]);
-                mine.odd |= !(v[i] < INFINITY);
             }
+            masked = __ballot(!(low > -1e38f)) != 0; // the next 16 are likely to be, too
         }
         rescale(mine, m, by);
         mine.s += (double)sum_of(e);
