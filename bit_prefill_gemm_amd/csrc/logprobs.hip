@@ -40,11 +40,15 @@ constexpr int kCandidates = 1024;
 constexpr int kMaxParts = 64;
 constexpr float kLog2e = 1.44269504f; // log2 e to 2^-26; divided by again at the end
 
+// Up to here m log2 e is at most 1 from the float next to it, which the sums are
+// taken about; far beyond, 2^x of the largest logit itself would leave fp32.
+constexpr float kFarRef = 16777216.0f;
+
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // What a part of a row amounts to: sums of 2^x and x 2^x, x = l log2 e - ref.
-// The reference is m log2 e, or the float next to it: x is then one FMA, with one
-// rounding relative to x, however large the logits are.
+// The reference is m log2 e, or up to kFarRef the float next to it: x is then one
+// FMA, with one rounding relative to x.
 struct Part {
     double ref;
     double s, t; // 0 where m is -inf; NaN with a NaN or +inf among them
@@ -368,7 +372,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
                 e[i] = __builtin_amdgcn_exp2f(x);
                 t[i % 4] = __builtin_fmaf(x, e[i], t[i % 4]);
             }
-            again = __ballot(!(sum_of(t) > -FLT_MAX)) != 0;
+            again = __ballot(!(sum_of(t) > -FLT_MAX) || fabsf(ref) > kFarRef) != 0;
         }
         if (again) { // x held to -250 and above, where 2^x is 0; NaN stays
             by = reference(m);

@@ -115,6 +115,26 @@ def test_alternatives(torch, vocab, topk):
             check(torch, logits, tokens, topk)
 
 
+@pytest.mark.parametrize("kind", ["huge", "stretches", "tail"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab", [(3, 900), (5, 32768), (300, 40001), (2, 262144)])
+def test_wide_ranges_and_stretches(torch, rows, vocab, dtype, kind):
+    """Logits up to half the largest, of both signs; masked stretches between open ones; a
+    vocabulary padded with -inf."""
+    x, tokens = make(torch, rows, vocab, torch.float32, "normal", vocab)
+    at = torch.arange(vocab, device="cuda")
+    if kind == "huge":
+        by = torch.tensor([1e38, 1e30, 1e7, 1e8, 1e12], device="cuda")
+        x *= by.repeat(rows // 5 + 1)[:rows, None]
+        x = x.clamp(-1.65e38, 1.65e38)  # log probabilities stay in fp32's range
+    elif kind == "stretches":
+        x[:, at // 700 % 3 == 1] = -math.inf
+        x[:, at // 9000 % 2 == 1] = torch.finfo(torch.float32).min
+    else:
+        x[:, vocab * 3 // 5:] = -math.inf
+    check(torch, x.to(getattr(torch, dtype)), tokens, 9)
+
+
 def test_many_rows(torch):
     for rows, vocab in ((70001, 33), (4099, 2000)):
         logits, tokens = make(torch, rows, vocab, torch.float32, "normal", 1)
