@@ -8,6 +8,9 @@ Bars:
   kernel: the results equal the whole-number ones bit for bit;
 - products of ordinary codes lie within the rounding bounds derived below.
 """
+import math
+import threading
+
 import numpy as np
 import pytest
 
@@ -202,6 +205,22 @@ def test_product_exact(torch, m, n, k, dtype):
         ref = mm64(torch, wide_values(torch, c, s, 1), wide_values(torch, w.codes, w.scales, 128))
         assert torch.equal(got, ref.to(dt)), torch.nonzero(got != ref.to(dt))[:4]
         check_around(torch, got, buf, how)
+
+
+# more blocks of K than a wave holds scales of at once (60), in one piece and in parts
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("m,n", [(1, 40), (20, 136), (40, 64), (70, 1300), (130, 300), (300, 520),
+                                 (520, 5000), (700, 1100), (1024, 2048), (2050, 4100)])
+@pytest.mark.parametrize("k", [61 * 128, 120 * 128 + 32])
+def test_product_exact_long_k(torch, m, n, k, dtype):
+    """Codes of 1, 0 and -1 under scales of 1/4 to 4: at most 15392 * 256 steps of 1/16."""
+    dt = getattr(torch, dtype)
+    g = generator(torch, m + n + k)
+    c, s = small_codes(torch, g, m, k, 1), power_scales(torch, g, m, blocks(k))
+    w = bb.Fp8Weights(small_codes(torch, g, n, k, 1), power_scales(torch, g, blocks(n), blocks(k)))
+    ref = mm64(torch, wide_values(torch, c, s, 1), wide_values(torch, w.codes, w.scales, 128)).to(dt)
+    got = bb.fp8_gemm(c, s, w, dtype=dt)
+    assert torch.equal(got, ref), torch.nonzero(got != ref)[:4]
 
 
 def real_codes(torch, g, m, k, rows, outliers):
@@ -502,6 +521,80 @@ def test_block_on_streams(torch):
     for turn, parts in enumerate(got):
         for a, b in zip(parts, want[turn % 3]):
             assert torch.equal(a, b)
+
+
+PARTS = [(300, 256, 8192), (300, 520, 120 * 128 + 32)]  # over parts of K, through a workspace
+
+
+def test_parts_of_k_from_graphs_and_threads(torch):
+    """Calls that need a workspace: two graphs' replays, then two threads on streams of their own,
+    with eager calls between, give the same bits."""
+    for m, n, k in PARTS:
+        assert "parts of K" in bb.fp8_gemm_kernel_name(m, n, k, torch.bfloat16)
+        g = generator(torch, m)
+        c, s = real_codes(torch, g, m, k, 1, False)
+        w = [bb.Fp8Weights(*real_codes(torch, g, n, k, 128, False)) for _ in range(2)]
+        want = [bb.fp8_gemm(c, s, v, dtype=torch.bfloat16) for v in w]
+        torch.cuda.synchronize()
+        graphs, outs = [], []
+        for v in w:
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                outs.append(bb.fp8_gemm(c, s, v, dtype=torch.bfloat16))
+            graphs.append(gr)
+        for _ in range(4):
+            for i in range(2):
+                outs[i].fill_(0)
+                graphs[i].replay()
+                again = bb.fp8_gemm(c, s, w[1 - i], dtype=torch.bfloat16)
+                torch.cuda.synchronize()
+                assert torch.equal(outs[i], want[i]) and torch.equal(again, want[1 - i])
+        got = [[], []]
+
+        def work(i):
+            st = torch.cuda.Stream()
+            for _ in range(20):
+                got[i].append(bb.fp8_gemm(c, s, w[i], dtype=torch.bfloat16, stream=st))
+            st.synchronize()
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        for i in range(2):
+            assert len(got[i]) == 20 and all(torch.equal(y, want[i]) for y in got[i])
+
+
+def test_one_matrix_for_both_projections(torch):
+    for m, f, k in ((3, 160, 256), (70, 320, 416), (300, 2048, 288)):
+        g = generator(torch, f)
+        c, s = real_codes(torch, g, m, k, 1, False)
+        w = bb.Fp8Weights(*real_codes(torch, g, f, k, 128, False))
+        other = bb.Fp8Weights(w.codes.clone(), w.scales.clone())
+        for dt in (torch.float32, torch.bfloat16):
+            assert torch.equal(bb.fp8_gemm_gated(c, s, w, w, dtype=dt),
+                               bb.fp8_gemm_gated(c, s, w, other, dtype=dt))
+        for a, b in zip(bb.fp8_gemm_gated_quantize(c, s, w, w),
+                        bb.fp8_gemm_gated_quantize(c, s, w, other)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 150, 544), (40, 260, 672), (70, 1300, 800), (270, 300, 1056),
+                                   (2050, 4100, 416), (300, 256, 8192)])
+def test_nan_scale_stays_in_its_row_and_columns(torch, m, n, k):
+    """A NaN among the scales reaches its row, or its 128 columns: scales of the blocks and rows
+    beside a block are read along with its own."""
+    for dt in (torch.float32, torch.bfloat16):
+        g = generator(torch, k)
+        c, s = real_codes(torch, g, m, k, 1, False)
+        w = bb.Fp8Weights(*real_codes(torch, g, n, k, 128, False))
+        s[1, 0] = math.nan
+        s[m - 2, blocks(k) - 1] = math.nan
+        w.scales[0, blocks(k) // 2] = math.nan
+        y = torch.isnan(bb.fp8_gemm(c, s, w, dtype=dt))
+        want = torch.zeros_like(y)
+        want[1], want[m - 2], want[:, :128] = True, True, True
+        assert torch.equal(y, want)
 
 
 def test_inputs_that_require_gradients(torch):
