@@ -556,6 +556,7 @@ constexpr Cost kStaged[] = {
     {kFp8Tile64x64, 64, 64, 256, 3.0f, 0.25f, 0.30f},
 };
 constexpr float kLaunch = 2.0f; // another launch behind one
+constexpr int kMaxSplits = 16;  // parts of K
 
 int64_t tiles_of(const Cost &c, int64_t m, int64_t cols, int g)
 {
@@ -613,9 +614,43 @@ template <int N> float plan(const Cost (&costs)[N], const Fp8Problem &p, Fp8Plan
     return whole;
 }
 
-// y = the splits' sums [splits][m][n], in their order, as bf16
+// Tiles over a part of K each, where there are few of them: the sums are written
+// and read again, at 5 TB/s.  In us, without and with: rows x K x columns
+// 1024 x 17408 x 5120, 80 tiles of 256x256, 143 and 101; 64 x 17408 x 5120 35 and
+// 25; 96 x 16384 x 1024 29 and 14; fp32 results 256 x 17408 x 5120 79 and 58.
+// Replaces *plan where that is quicker than `best`.
+template <int N>
+void split_k(const Cost (&costs)[N], const Fp8Problem &p, float best, Fp8Plan *plan)
+{
+    const int64_t blocks = fp8_blocks(p.k);
+    const float value = p.y_bf16 ? 2 : 4; // bytes of a result
+    for (const Cost &c : costs) {
+        // one 128x128 a CU, with its loads further ahead, is the quicker of the two
+        // there: 520 x 7808 x 5000 33 us, two a CU 44
+        if (c.kernel == kFp8Tile128x128Pair && !p.exact)
+            continue;
+        const int64_t tiles = tiles_of(c, p.m, p.n, 1);
+        for (int splits = 2; splits <= kMaxSplits && tiles * splits <= 2 * c.slots; splits++) {
+            const int64_t each = (blocks + splits - 1) / splits;
+            if (each < 8)
+                break;
+            if ((splits - 1) * each >= blocks)
+                continue; // the last would have none
+            const float t = time_of(c, tiles * splits, each) + kLaunch +
+                            (float)(p.m * p.n) * ((float)(8 * splits) + value) / 5e6f;
+            if (t < best) {
+                best = t;
+                *plan = Fp8Plan{};
+                plan->part[0] = {c.kernel, 0, p.n, splits};
+            }
+        }
+    }
+}
+
+// y = the splits' sums [splits][m][n], in their order
+template <bool BF16>
 __global__ __launch_bounds__(256) void fp8_join_kernel(const float *sums, int splits, int64_t m,
-                                                       int64_t n, uint16_t *y, int64_t ldy)
+                                                       int64_t n, void *y, int64_t ldy)
 {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; // n is a multiple of 4
     if (i >= m * n)
@@ -623,9 +658,14 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float *sums, int sp
     v4f sum = *reinterpret_cast<const v4f *>(sums + i);
     for (int q = 1; q < splits; q++)
         sum += *reinterpret_cast<const v4f *>(sums + q * m * n + i);
-    const v2u v{bf16_bits(sum[0]) | bf16_bits(sum[1]) << 16,
-                bf16_bits(sum[2]) | bf16_bits(sum[3]) << 16};
-    __builtin_memcpy(__builtin_assume_aligned(y + i / n * ldy + i % n, 2), &v, 8);
+    const int64_t at = i / n * ldy + i % n;
+    if constexpr (BF16) {
+        const v2u v{bf16_bits(sum[0]) | bf16_bits(sum[1]) << 16,
+                    bf16_bits(sum[2]) | bf16_bits(sum[3]) << 16};
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t *>(y) + at, 2), &v, 8);
+    } else {
+        __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(y) + at, 4), &sum, 16);
+    }
 }
 
 hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
@@ -637,10 +677,21 @@ hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
         default: return launch_values<Tile64x64, true>(p, part, s);
         }
     }
-    if (!p.y_bf16) { // the values of a staged gated product
+    if (!p.y_bf16 && p.up) { // the values of a staged gated product
         return part.kernel == kFp8Tile64x128
                    ? launch_tile<Tile64x128, true, false, kF32>(p, part, nullptr, nullptr, s)
                    : launch_tile<Tile64x64, true, false, kF32>(p, part, nullptr, nullptr, s);
+    }
+    if (!p.y_bf16) { // the sums of parts of K
+        switch (part.kernel) {
+        case kFp8Tile256x256:
+            return launch_tile<Tile256x256, false, false, kF32>(p, part, nullptr, nullptr, s);
+        case kFp8Tile128x128:
+            return launch_tile<Tile128x128, false, false, kF32>(p, part, nullptr, nullptr, s);
+        case kFp8Tile64x128:
+            return launch_tile<Tile64x128, false, false, kF32>(p, part, nullptr, nullptr, s);
+        default: return launch_tile<Tile64x64, false, false, kF32>(p, part, nullptr, nullptr, s);
+        }
     }
     switch (part.kernel) {
     case kFp8Tile256x256: return launch_values<Tile256x256, false>(p, part, s);
@@ -674,28 +725,13 @@ Fp8Plan plan_fp8_gemm(const Fp8Problem &p)
     if (streams(p))
         return streamed(p);
     Fp8Plan values;
-    if (p.exact) {
-        plan(kExact, p, &values);
-        return values;
-    }
-    const float whole = plan(kFast, p, &values);
+    const float whole = p.exact ? plan(kExact, p, &values) : plan(kFast, p, &values);
     if (p.up || p.n % 4 != 0)
         return values;
-    // The largest tiles over a part of K each, where there are few of them: the
-    // sums are written and read again, at 5 TB/s.  1024 x 17408 x 5120, 80 tiles:
-    // 143 us by halves of them, 103 over three parts.
-    float best = whole;
-    const Cost &c = kFast[0];
-    const int64_t tiles = tiles_of(c, p.m, p.n, 1), blocks = fp8_blocks(p.k);
-    for (int splits = 2; splits <= 8 && tiles * splits <= 2 * c.slots && 8 * splits <= blocks; splits++) {
-        const float t = time_of(c, tiles * splits, (blocks + splits - 1) / splits) + kLaunch +
-                        (float)(p.m * p.n) * (float)(8 * splits + 2) / 5e6f;
-        if (t < best) {
-            best = t;
-            values = Fp8Plan{};
-            values.part[0] = {c.kernel, 0, p.n, splits};
-        }
-    }
+    if (p.exact)
+        split_k(kExact, p, whole, &values);
+    else
+        split_k(kFast, p, whole, &values);
     return values;
 }
 
@@ -743,7 +779,15 @@ const char *fp8_plan_name(const Fp8Plan &plan)
     const Fp8Part &first = plan.part[0], &rest = plan.part[1];
     if (rest.cols > 0)
         return (first.kernel == kFp8Tile256x256 ? behind : pairs)[rest.kernel];
-    return first.splits > 1 ? "tile 256x256 over parts of K" : one[first.kernel];
+    static const char *const parts[] = {"",
+                                        "",
+                                        "tile 256x256 over parts of K",
+                                        "tile 128x128 pair over parts of K",
+                                        "tile 128x128 over parts of K",
+                                        "tile 64x128 over parts of K",
+                                        "tile 64x64 over parts of K",
+                                        ""};
+    return (first.splits > 1 ? parts : one)[first.kernel];
 }
 
 namespace {
@@ -778,12 +822,13 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, void *workspace, hipStream_t s)
     Fp8Problem sums = p;
     sums.y = workspace;
     sums.ldy = p.n;
-    const hipError_t e =
-        launch_tile<Tile256x256, false, false, kF32>(sums, plan.part[0], nullptr, nullptr, s);
+    sums.y_bf16 = false;
+    const hipError_t e = launch_part(sums, plan.part[0], s);
     if (e != hipSuccess)
         return e;
-    fp8_join_kernel<<<(unsigned)((p.m * p.n / 4 + 255) / 256), 256, 0, s>>>(
-        static_cast<const float *>(workspace), splits, p.m, p.n, static_cast<uint16_t *>(p.y), p.ldy);
+    (p.y_bf16 ? fp8_join_kernel<true> : fp8_join_kernel<false>)<<<
+        (unsigned)((p.m * p.n / 4 + 255) / 256), 256, 0, s>>>(
+        static_cast<const float *>(workspace), splits, p.m, p.n, p.y, p.ldy);
     return hipGetLastError();
 }
 

@@ -572,7 +572,7 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
 /*
  * Routing queries, host only: the kernel of fp8_gemm or (gated) fp8_gemm_gated,
  * and of fp8_gemm_gated_quantize: "stream", "tile RxC" (rows by columns; gated:
- * columns of both matrices), "tile 128x128 pair", "tile 256x256 over parts of K",
+ * columns of both matrices), "tile 128x128 pair", any of them " over parts of K",
  * or "A, then B" where the columns that fill the GPU in whole rounds and the rest
  * have a kernel each; "none" for no rows, NULL for sizes that the call refuses.
  */

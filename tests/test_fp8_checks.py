@@ -203,13 +203,16 @@ def test_kernel_names_refuse_what_the_calls_refuse():
 
 def test_every_kernel_has_a_tested_shape():
     """The shapes of the GPU tests reach every kernel in every form."""
-    from test_gpu_fp8 import GATED, GATED_ODD, SHAPES
+    from test_gpu_fp8 import GATED, GATED_ODD, LONG, SHAPES
     half = torch.bfloat16
     name = bb.fp8_gemm_kernel_name
     largest, pair = "tile 256x256", "tile 128x128 pair"
     small = {"stream", pair, "tile 64x128", "tile 64x64"}
-    assert small | {largest, "tile 128x128", largest + " over parts of K"} <= {
-        name(*s, half) for s in SHAPES}
+    assert small | {largest, "tile 128x128"} <= {name(*s, half) for s in SHAPES}
+    assert {t + " over parts of K" for t in (largest, "tile 128x128", "tile 64x128", "tile 64x64")} <= {
+        name(*s, half) for s in SHAPES + LONG}
+    assert {t + " over parts of K" for t in (pair, "tile 64x128", "tile 64x64")} <= {
+        name(*s) for s in SHAPES + LONG}
     assert any(name(*s, half).startswith(largest + ", then") for s in SHAPES)
     assert small <= {name(*s) for s in SHAPES}
     assert any(name(*s).startswith(pair + ", then") for s in SHAPES)

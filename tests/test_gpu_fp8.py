@@ -208,10 +208,13 @@ def test_product_exact(torch, m, n, k, dtype):
 
 
 # more blocks of K than a wave holds scales of at once (60), in one piece and in parts
+LONG = [(m, n, k) for m, n in ((1, 40), (20, 136), (40, 64), (70, 1300), (130, 300), (300, 520),
+                               (520, 5000), (700, 1100), (1024, 2048), (2050, 4100))
+        for k in (61 * 128, 120 * 128 + 32)]
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-@pytest.mark.parametrize("m,n", [(1, 40), (20, 136), (40, 64), (70, 1300), (130, 300), (300, 520),
-                                 (520, 5000), (700, 1100), (1024, 2048), (2050, 4100)])
-@pytest.mark.parametrize("k", [61 * 128, 120 * 128 + 32])
+@pytest.mark.parametrize("m,n,k", LONG)
 def test_product_exact_long_k(torch, m, n, k, dtype):
     """Codes of 1, 0 and -1 under scales of 1/4 to 4: at most 15392 * 256 steps of 1/16."""
     dt = getattr(torch, dtype)
