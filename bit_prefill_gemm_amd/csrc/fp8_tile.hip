@@ -475,7 +475,7 @@ __global__ __launch_bounds__(T::kThreads, 2) void fp8_tile_kernel(
             const int64_t line = m0 + 16 * (wm * MJ + j) + r;
 #pragma unroll
             for (int i = 0; i < NO; i++) {
-                const int64_t n = col0 + 16 * i + 4 * g; // p.n and p.ldy are multiples of 4
+                const int64_t n = col0 + 16 * i + 4 * g; // p.ldy is n's next multiple of 4
                 if (line < p.m && n < p.n)
                     *reinterpret_cast<v4f *>(y + line * p.ldy + n) = acc[i][j];
             }
@@ -647,24 +647,37 @@ void split_k(const Cost (&costs)[N], const Fp8Problem &p, float best, Fp8Plan *p
     }
 }
 
-// y = the splits' sums [splits][m][n], in their order
+// columns of a row of a part's sums
+int64_t sums_ld(int64_t n) { return (n + 3) / 4 * 4; }
+
+// y = the splits' sums [splits][m][ld], in their order
 template <bool BF16>
 __global__ __launch_bounds__(256) void fp8_join_kernel(const float *sums, int splits, int64_t m,
-                                                       int64_t n, void *y, int64_t ldy)
+                                                       int64_t n, int64_t ld, void *y, int64_t ldy)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; // n is a multiple of 4
-    if (i >= m * n)
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= m * ld)
         return;
     v4f sum = *reinterpret_cast<const v4f *>(sums + i);
     for (int q = 1; q < splits; q++)
-        sum += *reinterpret_cast<const v4f *>(sums + q * m * n + i);
-    const int64_t at = i / n * ldy + i % n;
+        sum += *reinterpret_cast<const v4f *>(sums + q * m * ld + i);
+    const int64_t col = i % ld, at = i / ld * ldy + col;
     if constexpr (BF16) {
+        uint16_t *to = static_cast<uint16_t *>(y) + at;
         const v2u v{bf16_bits(sum[0]) | bf16_bits(sum[1]) << 16,
                     bf16_bits(sum[2]) | bf16_bits(sum[3]) << 16};
-        __builtin_memcpy(__builtin_assume_aligned(static_cast<uint16_t *>(y) + at, 2), &v, 8);
+        if (col + 4 <= n)
+            __builtin_memcpy(__builtin_assume_aligned(to, 2), &v, 8);
+        else
+            for (int e = 0; e < (int)(n - col); e++)
+                to[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
     } else {
-        __builtin_memcpy(__builtin_assume_aligned(static_cast<float *>(y) + at, 4), &sum, 16);
+        float *to = static_cast<float *>(y) + at;
+        if (col + 4 <= n)
+            __builtin_memcpy(__builtin_assume_aligned(to, 4), &sum, 16);
+        else
+            for (int e = 0; e < (int)(n - col); e++)
+                to[e] = sum[e];
     }
 }
 
@@ -726,7 +739,7 @@ Fp8Plan plan_fp8_gemm(const Fp8Problem &p)
         return streamed(p);
     Fp8Plan values;
     const float whole = p.exact ? plan(kExact, p, &values) : plan(kFast, p, &values);
-    if (p.up || p.n % 4 != 0)
+    if (p.up)
         return values;
     if (p.exact)
         split_k(kExact, p, whole, &values);
@@ -810,7 +823,7 @@ hipError_t launch_plan(const Fp8Problem &p, const Fp8Plan &plan, hipStream_t s)
 size_t fp8_gemm_bytes(const Fp8Problem &p)
 {
     const int64_t splits = plan_fp8_gemm(p).part[0].splits;
-    return splits > 1 ? (size_t)(splits * p.m * p.n) * sizeof(float) : 0;
+    return splits > 1 ? (size_t)(splits * p.m * sums_ld(p.n)) * sizeof(float) : 0;
 }
 
 hipError_t launch_fp8_gemm(const Fp8Problem &p, void *workspace, hipStream_t s)
@@ -821,14 +834,14 @@ hipError_t launch_fp8_gemm(const Fp8Problem &p, void *workspace, hipStream_t s)
         return launch_plan(p, plan, s);
     Fp8Problem sums = p;
     sums.y = workspace;
-    sums.ldy = p.n;
+    sums.ldy = sums_ld(p.n);
     sums.y_bf16 = false;
     const hipError_t e = launch_part(sums, plan.part[0], s);
     if (e != hipSuccess)
         return e;
     (p.y_bf16 ? fp8_join_kernel<true> : fp8_join_kernel<false>)<<<
-        (unsigned)((p.m * p.n / 4 + 255) / 256), 256, 0, s>>>(
-        static_cast<const float *>(workspace), splits, p.m, p.n, p.y, p.ldy);
+        (unsigned)((p.m * sums.ldy / 4 + 255) / 256), 256, 0, s>>>(
+        static_cast<const float *>(workspace), splits, p.m, p.n, sums.ldy, p.y, p.ldy);
     return hipGetLastError();
 }
 

@@ -209,7 +209,8 @@ def test_product_exact(torch, m, n, k, dtype):
 
 # more blocks of K than a wave holds scales of at once (60), in one piece and in parts
 LONG = [(m, n, k) for m, n in ((1, 40), (20, 136), (40, 64), (70, 1300), (130, 300), (300, 520),
-                               (520, 5000), (700, 1100), (1024, 2048), (2050, 4100))
+                               (520, 5000), (700, 1100), (1024, 2048), (2050, 4100), (39, 1),
+                               (130, 301), (259, 1034), (520, 4999))
         for k in (61 * 128, 120 * 128 + 32)]
 
 
@@ -222,8 +223,11 @@ def test_product_exact_long_k(torch, m, n, k, dtype):
     c, s = small_codes(torch, g, m, k, 1), power_scales(torch, g, m, blocks(k))
     w = bb.Fp8Weights(small_codes(torch, g, n, k, 1), power_scales(torch, g, blocks(n), blocks(k)))
     ref = mm64(torch, wide_values(torch, c, s, 1), wide_values(torch, w.codes, w.scales, 128)).to(dt)
-    got = bb.fp8_gemm(c, s, w, dtype=dt)
-    assert torch.equal(got, ref), torch.nonzero(got != ref)[:4]
+    for how in ("new", "odd"):
+        y, buf = output(torch, m, n, dt, how)
+        got = bb.fp8_gemm(c, s, w, y=y, dtype=dt)
+        assert torch.equal(got, ref), torch.nonzero(got != ref)[:4]
+        check_around(torch, got, buf, how)
 
 
 def real_codes(torch, g, m, k, rows, outliers):
