@@ -9,7 +9,7 @@
 // for another before the end, where their sums are added in wave order.
 //
 // Bound by memory where there are many columns (1 x 17408 x 5120, 89 MB: 19.7 us,
-// 4.5 TB/s; gated to codes 42.9 us, 4.2 TB/s) and by the time to fill and drain
+// 4.5 TB/s; gated to codes 43.8 us, 4.1 TB/s) and by the time to fill and drain
 // where there are few (1 x 5120 x 5120: 7.9 us, 3.3 TB/s; 1 x 1024 x 5120: 4.6 us).
 // Blocks of K dealt to the waves in turn, straight to registers, took 20.7 us for
 // the first and 14.2 instead of 8.7 for 16 x 5120 x 5120, where a load of x or w

@@ -858,6 +858,10 @@ hipError_t launch_fp8_gated_quantize(const Fp8Problem &p, uint8_t *codes, float 
         Fp8Problem values = p;
         values.y = workspace;
         values.ldy = p.n;
+        // Few rows wait for memory, so their products may as well be added in fp32:
+        // a value next to a border of e4m3 moves by a whole step if it is a little
+        // off, and one row's down projection does not average that out.
+        values.exact = plan.part[0].kernel == kFp8Stream;
         const hipError_t e = launch_plan(values, plan, s);
         if (e != hipSuccess)
             return e;

@@ -415,6 +415,16 @@ def test_gated_quantize(torch, m, f, k, act):
     assert (err <= step + lim + 4 * U * size).all(), (err / (step + lim)).max()
 
 
+def test_codes_of_few_rows_are_those_of_the_fp32_values(torch):
+    for m, f, k in ((1, 1024, 2080), (16, 640, 544), (30, 96, 5120)):
+        g = generator(torch, m)
+        c, s = real_codes(torch, g, m, k, 1, True)
+        ws = [bb.Fp8Weights(*real_codes(torch, g, f, k, 128, False)) for _ in range(2)]
+        want = bb.quantize_fp8(bb.fp8_gemm_gated(c, s, *ws, dtype=torch.float32))
+        for a, b in zip(bb.fp8_gemm_gated_quantize(c, s, *ws), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_gated_exact_relu(torch):
     """Whole codes: every kernel's gate and up columns are where they belong, bit for bit."""
     for m, f, k in GATED + GATED_ODD:
