@@ -601,7 +601,7 @@ const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
  *              least (may be 0), 16-byte aligned; calls that can run at one time
  *              need one each
  * Neither output may overlap another or an input.
- * Limits: 1 <= vocab <= 2^24, 0 <= topk <= min(vocab, 64), rows * topk < 2^31,
+ * Limits: 1 <= vocab <= 2^24, 0 <= topk <= min(vocab, 64), rows and rows * topk < 2^31,
  * rows * vocab <= 2^40.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
  */
