@@ -1,21 +1,27 @@
 // logprobs.hip -- log probabilities of given tokens, entropies and top
 // alternatives of rows of logits (gfx950).
 //
-//   m = max l, S = sum e^(l - m), T = sum (l - m) e^(l - m)
-//   log p(t) = l_t - m - log S,  entropy = log S - T / S
+//   m = max l, R = sum e^(l - m) without one of the largest, T = sum (l - m) e^(l - m)
+//   log p(t) = l_t - m - log1p(R),  entropy = log1p(R) - T / (1 + R)
 //
-// T <= 0 and S >= 1, so nothing cancels in the entropy.  The top alternatives
-// are the largest logits, equal ones by the lowest id; a NaN counts as -inf
-// there.  A row with a NaN or +inf, or of -inf only, has no distribution: NaN.
+// T <= 0 and R >= 0, so nothing cancels: where one token is nearly certain, its
+// log probability and the entropy keep the digits of R and T.  The top
+// alternatives are the largest logits, equal ones by the lowest id; a NaN counts
+// as -inf there.  A row with a NaN or +inf, or of -inf only, has no distribution:
+// NaN.
 //
 // One pass over the logits: a thread holds 16 at a time and has 16 more on the
 // way, takes their maximum, rescales its sums to it and adds the 16 terms (in fp32
-// among the 16, in fp64 from one 16 to the next).  For the alternatives it leaves each 16's maximum in
-// LDS.  The k-th largest of 64 (or 128) groups' maxima is then below or at the k-th
-// largest logit, and few logits reach it (64 ln (64 / (64 - k)) on shuffled
-// rows: 24 for k = 20), so only the 16s that do are read again.  Where more than
-// kCandidates reach it (rows of equal logits, or with fewer than k above -inf)
-// the alternatives are found one scan of the part each.
+// among the 16, in fp64 from one 16 to the next).  These sums hold the largest
+// logit's own term, with an error of fp32; where R is not well above it, the wave
+// reads the logits of the thread that has the largest again and leaves it out.
+//
+// For the alternatives a thread leaves each 16's maximum in LDS.  The k-th
+// largest of 64 (or 128) groups' maxima is then below or at the k-th largest
+// logit, and few logits reach it (64 ln (64 / (64 - k)) on shuffled rows: 24 for
+// k = 20), so only the 16s that do are read again.  Where more than kCandidates
+// reach it (rows of equal logits, or with fewer than k above -inf) the
+// alternatives are found one scan of the part each.
 //
 // Few rows are split into parts of 8192 logits or more, a workgroup each, and
 // another launch joins them.
@@ -38,7 +44,7 @@ constexpr int kEach = 16;  // logits a thread holds at once
 constexpr int kSteps = 32; // of a workgroup, at most
 constexpr int kCandidates = 1024;
 constexpr int kMaxParts = 64;
-constexpr float kLog2e = 1.44269504f; // log2 e to 2^-26; divided by again at the end
+constexpr float kLog2e = 1.44269504f; // log2 e to 2^-26
 
 // Up to here m log2 e is at most 1 from the float next to it, which the sums are
 // taken about; far beyond, 2^x of the largest logit itself would leave fp32.
@@ -46,14 +52,26 @@ constexpr float kFarRef = 16777216.0f;
 
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// What a part of a row amounts to: sums of 2^x and x 2^x, x = l log2 e - ref.
-// The reference is m log2 e, or up to kFarRef the float next to it: x is then one
-// FMA, with one rounding relative to x.
-struct Part {
+// What a thread has: sums of 2^x and x 2^x, x = l log2 e - ref.  The reference is
+// m log2 e, or up to kFarRef the float next to it: x is then one FMA, with one
+// rounding relative to x.
+struct Sums {
     double ref;
     double s, t; // 0 where m is -inf; NaN with a NaN or +inf among them
     float m;     // the largest logit, -inf if there is none
 };
+
+// What a part of a row amounts to, x = (l - m) log2 e: sums of 2^x over all
+// logits but one of the largest, and of x 2^x.
+struct Part {
+    double s, t; // as above
+    float m;
+};
+
+// The largest logit's own term leaves up to ten roundings of 2^-24 in a thread's
+// s (the sum of 16, the exponential, the reference): from here on that is 2^-18
+// of the rest at most.
+constexpr double kClose = 1.0 / 4;
 
 // An order of the logits and their ids in one word: larger words are larger
 // logits, or the lower id of equal ones.  No logit has word 0.
@@ -119,8 +137,8 @@ __device__ __forceinline__ float wave_max(float v)
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-// a part's sums about a maximum that is not smaller
-__device__ __forceinline__ void rescale(Part &p, float m, double ref)
+// sums about a maximum that is not smaller
+__device__ __forceinline__ void rescale(Sums &p, float m, double ref)
 {
     const double d = p.m == -INFINITY ? 0.0 : p.ref - ref;
     const double e = __builtin_amdgcn_exp2f((float)d);
@@ -128,16 +146,6 @@ __device__ __forceinline__ void rescale(Part &p, float m, double ref)
     p.s *= e;
     p.m = m;
     p.ref = ref;
-}
-
-// all lanes' parts as one, in the last lane
-__device__ __forceinline__ Part over_wave(Part p)
-{
-    const float m = wave_max(p.m);
-    rescale(p, m, reference(m));
-    p.s = sum_to_last(p.s);
-    p.t = sum_to_last(p.t);
-    return p;
 }
 
 __device__ __forceinline__ double last_lane(double v)
@@ -148,22 +156,45 @@ __device__ __forceinline__ double last_lane(double v)
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
-// the last lane's part in every lane
-__device__ __forceinline__ Part everywhere(Part p)
+// the lanes' s and t as one part, in every lane
+__device__ __forceinline__ Part over_lanes(double s, double t, float m)
 {
-    p.s = last_lane(p.s);
-    p.t = last_lane(p.t);
-    return p;
+    return Part{last_lane(sum_to_last(s)), last_lane(sum_to_last(t)), m};
+}
+
+// The threads of a wave as one part, in every lane.  again(lane, m, s, t): adds
+// the terms of one lane's logits, without the largest, to s and t, each lane a
+// share of them.
+template <class F> __device__ __forceinline__ Part over_wave(Sums p, F &&again)
+{
+    const float m = wave_max(p.m);
+    const int owner = __builtin_ctzll(__ballot(p.m == m)); // p.m is no NaN
+    rescale(p, m, reference(m));
+    const bool mine = (int)(threadIdx.x & 63) == owner && m > -INFINITY;
+    const Part all = over_lanes(mine ? p.s - 1.0 : p.s, p.t, m);
+    if (!(all.s < kClose) || m == -INFINITY)
+        return all;
+    double s = mine ? 0.0 : p.s, t = mine ? 0.0 : p.t;
+    again(owner, m, s, t);
+    return over_lanes(s, t, m);
 }
 
 // parts of one row in LDS as one, a lane each (64 at most), in every lane
 __device__ __forceinline__ Part over_parts(const Part *parts, int count)
 {
-    Part p{0.0, 0.0, 0.0, -INFINITY};
+    Part p{0.0, 0.0, -INFINITY};
     const int lane = threadIdx.x & 63;
     if (lane < count)
         p = parts[lane];
-    return everywhere(over_wave(p));
+    const float m = wave_max(p.m);
+    const int owner = __builtin_ctzll(__ballot(p.m == m));
+    if (lane != owner && p.m > -INFINITY) {
+        const double d = ((double)p.m - m) * kLog2e, s = p.s + 1.0;
+        const double e = __builtin_amdgcn_exp2f((float)d);
+        p.t = (p.t + d * s) * e;
+        p.s = s * e;
+    }
+    return over_lanes(p.s, p.t, m);
 }
 
 // Sixteen logits of a thread in a step: groups of one 16-byte load each, the
@@ -174,18 +205,18 @@ template <bool BF16, int THREADS> struct Step {
     static constexpr int kGroups = BF16 ? 2 : 4, kPer = kEach / kGroups;
     static constexpr bool kWhole = THREADS > 64; // of a row of kPer logits or more
     v4u raw[kGroups];
-    static __device__ __forceinline__ int64_t id(int64_t at, int q)
+    static __device__ __forceinline__ int64_t id(int64_t at, int q, int thread)
     {
-        return at + (int64_t)q * (THREADS * kPer) + threadIdx.x * kPer;
+        return at + (int64_t)q * (THREADS * kPer) + thread * kPer;
     }
     // logit e of group q of the step that begins at `at`: is it the group's own?
     static __device__ __forceinline__ bool own(int64_t at, int q, int e, int64_t end)
     {
-        return kWhole ? id_of(at, q, e, end) >= id(at, q) : id(at, q) + e < end;
+        return kWhole ? id_of(at, q, e, end) >= id(at, q, threadIdx.x) : id(at, q, threadIdx.x) + e < end;
     }
     static __device__ __forceinline__ int64_t id_of(int64_t at, int q, int e, int64_t end)
     {
-        return (kWhole ? min(id(at, q), end - kPer) : id(at, q)) + e;
+        return (kWhole ? min(id(at, q, threadIdx.x), end - kPer) : id(at, q, threadIdx.x)) + e;
     }
     static __device__ __forceinline__ const uint8_t *address(const void *row, int64_t i)
     {
@@ -270,22 +301,22 @@ __device__ __forceinline__ Token token_of(const LogprobsProblem &p, int64_t r, c
     return Token{id < 0 || id >= p.vocab ? NAN : logit<BF16>(row, id), id < 0};
 }
 
-// log2 S, NaN for a row without a distribution
+// log S, NaN for a row without a distribution
 __device__ __forceinline__ double log_sum(const Part &all)
 {
-    return all.m == -INFINITY ? NAN : log2(all.s);
+    return all.m == -INFINITY ? NAN : log1p(all.s);
 }
 
 __device__ __forceinline__ float log_probability(const Part &all, double log_s, float logit)
 {
-    return (float)(((double)logit * kLog2e - all.ref - log_s) * (1.0 / kLog2e));
+    return (float)((double)logit - all.m - log_s);
 }
 
 __device__ __forceinline__ void write_row(const LogprobsProblem &p, int64_t r, const Part &all, double log_s,
                                           Token token)
 {
     if (p.entropy)
-        p.entropy[r] = (float)((log_s - all.t / all.s) * (1.0 / kLog2e));
+        p.entropy[r] = (float)(log_s - all.t / (1.0 + all.s) * (1.0 / kLog2e));
     if (p.tokens)
         p.logprobs[r] = token.none ? 0.0f : log_probability(all, log_s, token.logit);
 }
@@ -348,7 +379,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         token = token_of<BF16>(p, r, row);
 
     // ---- the sums
-    Part mine{0.0, 0.0, 0.0, -INFINITY};
+    Sums mine{0.0, 0.0, 0.0, -INFINITY};
     int steps = 0;
     bool masked = false;
     auto step = [&](const Logits &now, int64_t at) {
@@ -407,9 +438,24 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         }
     }
     const float top = mine.m;
-    mine = over_wave(mine);
-    if (WAVES > 1 && lane == 63)
-        wave_parts[wave] = mine;
+    Part all = over_wave(mine, [&](int from, float m, double &s, double &t) {
+        const int thread = 64 * wave + from;
+        for (int c = lane; c < steps * Logits::kGroups; c += 64) {
+            const int64_t at = begin + (int64_t)(c / Logits::kGroups) * kStep;
+            const int64_t i = Logits::id(at, c % Logits::kGroups, thread);
+            for (int64_t e = i; e < min(i + Logits::kPer, end); e++) {
+                const float l = logit<BF16>(row, e);
+                if (l == m) // one of them, or s were 1 at least
+                    continue;
+                const float x = fmaxf((l - m) * kLog2e, -250.0f); // where 2^x is 0
+                const float p = __builtin_amdgcn_exp2f(x);
+                s += p;
+                t += x * p;
+            }
+        }
+    });
+    if (WAVES > 1 && lane == 0)
+        wave_parts[wave] = all;
     if (TOP) {
         groups[wave][lane] = top;
         if (threadIdx.x == 0)
@@ -421,7 +467,8 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     float least = 0;
     double log_s = 0;
     if (wave == 0) {
-        const Part all = WAVES > 1 ? over_parts(wave_parts, WAVES) : everywhere(mine);
+        if (WAVES > 1)
+            all = over_parts(wave_parts, WAVES);
         if (parts == 1)
             log_s = log_sum(all);
         if (threadIdx.x == 0) {
@@ -430,7 +477,6 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
             else
                 out_parts[blockIdx.x] = all;
         }
-        mine = all;
     }
     if constexpr (!TOP)
         return;
@@ -474,7 +520,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
             which ? (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(which))
                   : (uint32_t)__builtin_amdgcn_readlane((int)other, __builtin_ctzll(where));
         least = logit_of((uint64_t)max(kth & ~127u, 0x007fffffu) << 32); // -inf at least
-        if (mine.m == -INFINITY)
+        if (all.m == -INFINITY)
             least = NAN; // nothing reaches it
         if (WAVES > 1 && threadIdx.x == 0)
             reach = least;
@@ -521,7 +567,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
             return;
         }
         p.ids[r * p.topk + rank] = (int32_t)(~(uint32_t)word);
-        p.top[r * p.topk + rank] = log_probability(mine, log_s, logit_of(word));
+        p.top[r * p.topk + rank] = log_probability(all, log_s, logit_of(word));
     };
     if (parts > 1 && (int)threadIdx.x >= k && (int)threadIdx.x < p.topk)
         out_words[(int64_t)blockIdx.x * p.topk + threadIdx.x] = 0; // none: below every logit

@@ -591,7 +591,9 @@ const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
  * A logit of -inf has probability 0.  A row with a NaN or +inf, or of -inf only,
  * has no distribution: its log probabilities and its entropy are NaN, and a NaN
  * counts as -inf in the order of its ids.  Exponentials are fp32, sums beyond a
- * thread's few fp64, results rounded once.
+ * thread's few fp64, results rounded once.  The largest logit's own term, 1, is
+ * kept out of the sums, so that log probabilities (never above 0) and entropies
+ * (never below) keep their digits where one token is nearly certain.
  *   logits     device, [rows][ldl] of dt, aligned to its type, ldl >= vocab
  *   tokens     device, int32 or int64 (token_dt) [rows], or NULL: no logprobs
  *   logprobs   device, fp32 [rows] (may be NULL if tokens is)

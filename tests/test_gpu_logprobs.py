@@ -238,3 +238,62 @@ def test_more_rows_than_a_grid_holds(torch):
         check(torch, logits[s], tokens[s], 1)
         for a, b in zip(out, bb.token_logprobs(logits[s], tokens[s], topk=1)):
             assert torch.equal(a[s], b)
+
+
+def confident(torch, rows, vocab, dtype, seed, beside):
+    """Rows whose largest logit stands 1 to 50 above the next; `beside`: the next is its neighbour
+    in memory, and alone."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, vocab, generator=g, device="cuda") * 1.5
+    at = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    row = torch.arange(rows, device="cuda")
+    gap = 1.0 + 49.0 * torch.rand(rows, generator=g, device="cuda")
+    if beside:
+        x -= 70.0
+        x[row, at ^ 1 if vocab % 2 == 0 else (at + 1) % vocab] = 3.3
+        x[row, at] = 3.3 + gap
+    else:
+        x[row, at] = x.amax(1) + gap
+    x += 20.0 * torch.rand(rows, 1, generator=g, device="cuda") - 10.0
+    return x.to(dtype), at
+
+
+@pytest.mark.parametrize("beside", [False, True])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab,topk", [
+    (300, 2, 1), (200, 33, 0), (100, 1000, 3), (64, 4096, 20), (40, 5001, 0), (300, 32000, 2),
+    (600, 32000, 1), (1, 131072, 20), (9, 131072, 0), (3, 262144, 5)])
+def test_confident_rows(torch, rows, vocab, topk, dtype, beside):
+    """Log probabilities and entropies near zero, to their own digits.
+
+    With R the sum of e^d, d = l - m, over all logits but the largest, log S = log1p(R) and H =
+    log S + (the sum of |d| e^d) / S.  Steps of v = 2^-24: an e^d carries 2.25 v |d| of its exponent
+    (a difference, a product, log2 e) and another v |d| of its rescaled sums, 2 v of the exponential,
+    4 v of the sum of 16 and 2 v a time that its sums are rescaled (36 of them at most): v (4 |d| +
+    80), and its product with d 5 v more.  From R = 1/16 on (1/32 with a margin) the largest logit's
+    own term may be off by 10 v of the sum."""
+    v = 2.0 ** -24
+    for seed in range(3):
+        logits, at = confident(torch, rows, vocab, getattr(torch, dtype), seed + vocab, beside)
+        l = logits.double()
+        first = torch.argmax(l, 1, keepdim=True)
+        m = torch.gather(l, 1, first)
+        d = l - m
+        e = d.exp().scatter(1, first, 0.0)
+        r, t = e.sum(1), (d.abs() * e).sum(1)
+        d1 = t / r
+        d2 = (d * d * e).sum(1) / torch.where(t > 0, t, 1.0)
+        log_s = torch.log1p(r)
+        near = torch.where(r > 1 / 32, 10 * v, 0.0)
+        tol_s = v * (4 * d1 + 80) * r / (1 + r) + near
+        h = log_s + t / (1 + r)
+        tol_h = tol_s + v * (4 * d2 + 85 + 4 * d1 + 80) * t / (1 + r) + near * (1 + d1) + v * h
+        tokens = torch.where(torch.arange(rows, device="cuda") % 3 == 2, (at + 1) % vocab, at)
+        lp, ent, ids, top = bb.token_logprobs(logits, tokens, topk=topk)
+        assert (lp <= 0).all() and (top <= 0).all() and (ent >= 0).all()
+        assert ((ent.double() - h).abs() <= tol_h).all(), ((ent.double() - h).abs() / tol_h).max()
+        for got, token in [(lp, tokens)] + [(top[:, j], ids[:, j].long()) for j in range(topk)]:
+            want = torch.gather(d, 1, token[:, None])[:, 0] - log_s
+            tol = tol_s + v * want.abs()
+            assert ((got.double() - want).abs() <= tol).all(), (
+                (got.double() - want).abs() / tol).max()
