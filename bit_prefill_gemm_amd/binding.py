@@ -793,8 +793,12 @@ def fp8_gemm_gated_quantize(codes, scales, gate: Fp8Weights, up: Fp8Weights,
 
 def fp8_gemm_kernel_name(m: int, n: int, k: int, dtype=None, gated: bool = False) -> str:
     """The kernel that fp8_gemm (or fp8_gemm_gated) runs (host only; see include/bpg.h); dtype:
-    torch.float32 unless given."""
-    dt = X_BF16 if dtype is not None and dtype == _torch().bfloat16 else X_F32
+    torch.float32 (unless given) or torch.bfloat16."""
+    torch = _torch()
+    if dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError("fp8_gemm_kernel_name: dtype must be torch.float32 or torch.bfloat16, got %s"
+                         % (dtype,))
+    dt = X_BF16 if dtype == torch.bfloat16 else X_F32
     r = _lib_handle().fp8_gemm_kernel_name(m, n, k, dt, int(gated))
     if r is None:
         raise ValueError("fp8_gemm_kernel_name: invalid sizes")

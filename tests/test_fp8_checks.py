@@ -201,6 +201,14 @@ def test_kernel_names_refuse_what_the_calls_refuse():
         bb.fp8_gemm_kernel_name(4, 64, 31)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float64, E4M3, "bf16", 1])
+def test_kernel_name_refuses_other_types(dtype):
+    for gated in (False, True):
+        with pytest.raises(ValueError, match="dtype must be"):
+            bb.fp8_gemm_kernel_name(4, 64, 64, dtype, gated)
+    assert bb.fp8_gemm_kernel_name(4, 64, 64) == bb.fp8_gemm_kernel_name(4, 64, 64, torch.float32)
+
+
 def test_every_kernel_has_a_tested_shape():
     """The shapes of the GPU tests reach every kernel in every form."""
     from test_gpu_fp8 import GATED, GATED_ODD, LONG, SHAPES
