@@ -862,6 +862,19 @@ bool fp8_shape(int64_t m, int64_t n, int64_t k)
            k >= 1 && k % 32 == 0 && k <= kMaxGemmK;
 }
 
+// a gated product as codes: f in whole 32s, scales numbered in 31 bits
+bool fp8_codes_shape(int64_t m, int64_t f, int64_t k)
+{
+    return fp8_shape(m, f, k) && f % 32 == 0 && m * bpg::fp8_blocks(f) < ((int64_t)1 << 31);
+}
+
+bool logprobs_shape(int64_t rows, int64_t vocab, int64_t topk)
+{
+    return rows >= 0 && rows < ((int64_t)1 << 31) && vocab >= 1 && vocab <= kMaxVocab && topk >= 0 &&
+           topk <= kMaxTopk && topk <= vocab && rows * topk < ((int64_t)1 << 31) &&
+           rows * vocab <= kMaxLogits;
+}
+
 // what a plan goes by (no pointer is followed)
 bpg::Fp8Problem shape_problem(int64_t m, int64_t n, int64_t k, bool gated)
 {
@@ -990,7 +1003,7 @@ bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,
 
 size_t fp8_gemm_gated_quantize_bytes(int64_t m, int64_t f, int64_t k)
 {
-    if (!fp8_shape(m, f, k) || f % 32 != 0)
+    if (!fp8_codes_shape(m, f, k))
         return 0;
     return bpg::fp8_gated_quantize_bytes(shape_problem(m, f, k, true));
 }
@@ -1017,7 +1030,7 @@ const char *fp8_gemm_kernel_name(int64_t m, int64_t n, int64_t k, bpg_x_dtype y_
 
 const char *fp8_gemm_gated_quantize_kernel_name(int64_t m, int64_t f, int64_t k)
 {
-    if (!fp8_shape(m, f, k) || f % 32 != 0)
+    if (!fp8_codes_shape(m, f, k))
         return nullptr;
     return bpg::fp8_plan_name(bpg::plan_fp8_codes(shape_problem(m, f, k, true)));
 }
@@ -1035,7 +1048,7 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
         check_fp8(codes, scales, m, gate_codes, gate_scales, true, up_codes, up_scales, f, k);
     if (s != BPG_OK)
         return s;
-    if (f % 32 != 0 || m * bpg::fp8_blocks(f) >= ((int64_t)1 << 31))
+    if (!fp8_codes_shape(m, f, k))
         return BPG_ERR_SHAPE;
     const size_t need = fp8_gemm_gated_quantize_bytes(m, f, k);
     if (m > 0 && (!out_codes || !out_scales || (need > 0 && !workspace)))
@@ -1057,8 +1070,7 @@ bpg_status fp8_gemm_gated_quantize(const void *codes, const float *scales, int64
 
 size_t token_logprobs_bytes(int64_t rows, int64_t vocab, int64_t topk)
 {
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || topk < 0 ||
-        topk > kMaxTopk || rows * vocab > kMaxLogits)
+    if (!logprobs_shape(rows, vocab, topk))
         return 0;
     return bpg::logprobs_bytes(rows, vocab, (int)topk);
 }
@@ -1070,9 +1082,7 @@ bpg_status token_logprobs(const void *logits, bpg_x_dtype dt, int64_t rows, int6
 {
     if (!dtype_ok(dt) || (tokens && token_dt != BPG_I32 && token_dt != BPG_I64))
         return BPG_ERR_DTYPE;
-    if (rows < 0 || rows >= ((int64_t)1 << 31) || vocab < 1 || vocab > kMaxVocab || ldl < vocab ||
-        ldl > ((int64_t)1 << 40) || topk < 0 || topk > kMaxTopk || topk > vocab ||
-        rows * topk >= ((int64_t)1 << 31) || rows * vocab > kMaxLogits)
+    if (!logprobs_shape(rows, vocab, topk) || ldl < vocab || ldl > ((int64_t)1 << 40))
         return BPG_ERR_SHAPE;
     const size_t need = rows > 0 ? bpg::logprobs_bytes(rows, vocab, (int)topk) : 0;
     if (rows > 0 && (!logits || (tokens && !logprobs) || (topk > 0 && (!ids || !top)) ||

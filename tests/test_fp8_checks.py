@@ -209,6 +209,21 @@ def test_kernel_name_refuses_other_types(dtype):
     assert bb.fp8_gemm_kernel_name(4, 64, 64) == bb.fp8_gemm_kernel_name(4, 64, 64, torch.float32)
 
 
+def test_queries_refuse_what_the_calls_refuse():
+    """Sizes that only one of the calls refuses: 2^31 blocks of codes, more alternatives than logits
+    or than 2^31 in all."""
+    m, f, k = 1 << 16, 1 << 22, 32
+    assert gated_quantize(m=m, n=f, k=k) == SHAPE
+    assert bb.lib().fp8_gemm_gated_quantize_kernel_name(m, f, k) is None
+    assert bb.lib().fp8_gemm_gated_quantize_bytes(m, f, k) == 0
+    with pytest.raises(ValueError, match="invalid sizes"):
+        bb.fp8_gemm_gated_quantize_kernel_name(m, f, k)
+    assert bb.fp8_gemm_gated_quantize_kernel_name(m - 1, f, k) != "none"
+    for rows, vocab, topk in ((1, 131072, 65), (1, 40, 41), (1 << 26, 8192, 32)):
+        assert logprobs(rows=rows, vocab=vocab, ldl=vocab, topk=topk) == SHAPE
+        assert bb.lib().token_logprobs_bytes(rows, vocab, topk) == 0
+
+
 def test_every_kernel_has_a_tested_shape():
     """The shapes of the GPU tests reach every kernel in every form."""
     from test_gpu_fp8 import GATED, GATED_ODD, LONG, SHAPES
