@@ -249,6 +249,27 @@ def test_every_kernel_has_a_tested_shape():
             (largest, False), (largest + ", then tile 64x256", False)} <= codes
 
 
+def test_every_pair_of_kernels_and_every_gated_kernel_over_long_k_has_a_tested_shape():
+    from test_gpu_fp8 import (GATED, GATED_LONG, GATED_ODD, GATED_SIDE_BY_SIDE, SHAPES,
+                              SIDE_BY_SIDE)
+    half = torch.bfloat16
+    name, codes = bb.fp8_gemm_kernel_name, bb.fp8_gemm_gated_quantize_kernel_name
+    largest, pair = "tile 256x256", "tile 128x128 pair"
+    rest = {"tile 128x128", "tile 64x128", "tile 64x64"}
+    behind = {largest + ", then " + t for t in rest | {pair}}
+    behind_pair = {pair + ", then " + t for t in ("tile 64x128", "tile 64x64")}
+    assert behind <= {name(*s, half) for s in SHAPES + SIDE_BY_SIDE}
+    assert behind_pair <= {name(*s) for s in SHAPES + SIDE_BY_SIDE}
+    gated = GATED + GATED_ODD + GATED_SIDE_BY_SIDE
+    assert behind <= {name(*s, half, gated=True) for s in gated}
+    assert behind_pair <= {name(*s, gated=True) for s in gated}
+    small = {"stream", pair, "tile 64x128", "tile 64x64"}
+    assert small | rest | {largest} <= {name(*s, half, gated=True) for s in GATED_LONG}
+    assert small | behind_pair <= {name(*s, gated=True) for s in GATED_LONG}
+    assert {"stream", largest, "tile 64x128", "tile 64x64", "tile 64x256",
+            largest + ", then tile 64x256"} <= {codes(*s) for s in GATED_LONG if s[1] % 32 == 0}
+
+
 # ------------------------------------------------------------------ binding
 
 def codes_of(m, k):

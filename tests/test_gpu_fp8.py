@@ -619,3 +619,49 @@ def test_inputs_that_require_gradients(torch):
     x = torch.randn(4, 64, device="cuda", requires_grad=True)
     codes, scales = bb.quantize_fp8(x)
     assert not scales.requires_grad
+
+
+# ------------------------------------------------------------------ every plan, more blocks of K than 60
+
+# gated: a wave loads the scales of both matrices anew every 60 blocks of K
+GATED_LONG = [(18, 32, 61 * 128), (33, 64, 120 * 128 + 32), (39, 33, 61 * 128), (67, 4864, 61 * 128),
+              (65, 4256, 120 * 128 + 32), (210, 4160, 61 * 128), (400, 4288, 61 * 128),
+              (514, 3776, 120 * 128 + 32), (712, 2784, 61 * 128), (952, 4128, 61 * 128),
+              (1171, 3309, 61 * 128), (1428, 3045, 120 * 128 + 32), (1557, 4832, 61 * 128),
+              (1574, 4887, 61 * 128), (1844, 4640, 61 * 128), (2029, 4571, 61 * 128)]
+# two kernels side by side that the shapes above do not reach
+SIDE_BY_SIDE = [(2078, 8226, 2080), (3105, 5277, 32), (2178, 7196, 32), (5400, 1630, 288)]
+GATED_SIDE_BY_SIDE = [(1611, 5326, 2080), (1812, 4447, 32), (2689, 3043, 32)]
+
+
+@pytest.mark.parametrize("m,f,k", GATED_LONG + GATED_SIDE_BY_SIDE)
+def test_gated_exact_relu_long_k(torch, m, f, k):
+    """Codes of 1, 0 and -1 under scales of 1/4 to 4: both projections are whole multiples of 2^-4
+    below 2^18, so their product rounds once."""
+    g = generator(torch, m + f + k)
+    c, s = small_codes(torch, g, m, k, 1), power_scales(torch, g, m, blocks(k))
+    gate, up = (bb.Fp8Weights(small_codes(torch, g, f, k, 1),
+                              power_scales(torch, g, blocks(f), blocks(k))) for _ in range(2))
+    a = wide_values(torch, c, s, 1)
+    wg, wu = (wide_values(torch, w.codes, w.scales, 128) for w in (gate, up))
+    h = (torch.relu(mm64(torch, a, wg)) * mm64(torch, a, wu)).float()
+    for dt in (torch.float32, torch.bfloat16):
+        got = bb.fp8_gemm_gated(c, s, gate, up, activation="relu", dtype=dt)
+        assert torch.equal(got, h.to(dt)), torch.nonzero(got != h.to(dt))[:4]
+    if f % 32 == 0:
+        codes, scales = bb.fp8_gemm_gated_quantize(c, s, gate, up, activation="relu")
+        q, d = plain_codes(torch, h.cpu(), 1)
+        assert torch.equal(scales.cpu(), d)
+        assert torch.equal(codes.cpu().view(torch.uint8) & 0x7f, q & 0x7f)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("m,n,k", SIDE_BY_SIDE)
+def test_product_exact_side_by_side(torch, m, n, k, dtype):
+    dt = getattr(torch, dtype)
+    g = generator(torch, m + n + k)
+    c, s = small_codes(torch, g, m, k), power_scales(torch, g, m, blocks(k))
+    w = bb.Fp8Weights(small_codes(torch, g, n, k), power_scales(torch, g, blocks(n), blocks(k)))
+    got = bb.fp8_gemm(c, s, w, dtype=dt)
+    ref = mm64(torch, wide_values(torch, c, s, 1), wide_values(torch, w.codes, w.scales, 128)).to(dt)
+    assert torch.equal(got, ref), torch.nonzero(got != ref)[:4]
