@@ -19,9 +19,15 @@
 // For the alternatives a thread leaves each 16's maximum in LDS.  The k-th
 // largest of 64 (or 128) groups' maxima is then below or at the k-th largest
 // logit, and few logits reach it (64 ln (64 / (64 - k)) on shuffled rows: 24 for
-// k = 20), so only the 16s that do are read again.  Where more than kCandidates
-// reach it (rows of equal logits, or with fewer than k above -inf) the
-// alternatives are found one scan of the part each.
+// k = 20), so only the 16s that do are read again.  A mask may leave fewer than k
+// groups open: then the open logits and the lowest masked ids are taken.  Where
+// many groups have the k-th maximum itself (a mask's finite value, rows of few
+// values), or more than kCandidates logits reach it, the logits above it are
+// taken and, in the order of their ids, as many equal ones as are missing.  With
+// ten open logits and 20 alternatives 64 x 131072 takes 21 to 22 us and 1024 rows
+// 59 to 61, as without a mask.  If too many are above it even so (thousands of
+// open logits in fewer than k groups), the alternatives are found one scan of the
+// part each.
 //
 // Few rows are split into parts of 8192 logits or more, a workgroup each, and
 // another launch joins them.
@@ -266,6 +272,13 @@ template <bool BF16> __device__ __forceinline__ float logit(const void *row, int
                 : static_cast<const float *>(row)[i];
 }
 
+// the next float above one that is not -inf; NaN above +inf
+__device__ __forceinline__ float next_above(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return __uint_as_float(v == 0.0f ? 1u : u & 0x80000000u ? u - 1 : u + 1);
+}
+
 // the upper half of a float, rounded up
 __device__ __forceinline__ uint16_t above(float v)
 {
@@ -368,7 +381,8 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     __shared__ float groups[WAVES][64], reach;
     __shared__ __attribute__((aligned(16))) uint64_t words[TOP ? kCandidates + 8 : 1];
     __shared__ uint64_t best[WAVES];
-    __shared__ int count;
+    __shared__ int count, equals[WAVES];
+    __shared__ bool many;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t r = blockIdx.x / parts, part = blockIdx.x % parts;
@@ -465,6 +479,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
         __syncthreads();
     // the first wave goes on; the others come back to read their logits again
     float least = 0;
+    bool tied = false;
     double log_s = 0;
     if (wave == 0) {
         if (WAVES > 1)
@@ -484,9 +499,9 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     // ---- the alternatives
     const int k = (int)min((int64_t)p.topk, end - begin);
     if (wave == 0) {
-        // the k-th largest of 64 groups' maxima, of 128 for many alternatives, or
-        // a little less: the lowest bits give way to the group, which makes the
-        // keys different
+        // the smallest of the k largest of 64 groups' maxima, of 128 for many
+        // alternatives: the lowest bits of a key give way to the group, which makes
+        // the keys different
         auto key_of = [](float g, int group) {
             return (uint32_t)(word_of(g, 0) >> 32 & ~(uint64_t)127) | (uint32_t)group;
         };
@@ -512,53 +527,82 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
                 rank += b > key;
                 rank_other += (a > other) + (b > other);
             }
-        } else {
-            rank_other = -1;
         }
-        const uint64_t which = __ballot(rank == k - 1), where = __ballot(rank_other == k - 1);
-        const uint32_t kth =
-            which ? (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(which))
-                  : (uint32_t)__builtin_amdgcn_readlane((int)other, __builtin_ctzll(where));
-        least = logit_of((uint64_t)max(kth & ~127u, 0x007fffffu) << 32); // -inf at least
-        if (all.m == -INFINITY)
-            least = NAN; // nothing reaches it
-        if (WAVES > 1 && threadIdx.x == 0)
+        float kth = rank < k ? even : INFINITY;
+        if (kinds == 2 && rank_other < k)
+            kth = fminf(kth, odd);
+        least = -wave_max(-kth);
+        tied = __popcll(__ballot(even == least)) + __popcll(__ballot(odd == least)) > 16;
+        if (WAVES > 1 && threadIdx.x == 0) {
             reach = least;
+            many = tied;
+        }
     }
     if constexpr (WAVES > 1) {
         __syncthreads();
         least = reach;
+        tied = many;
     }
-    if (least != least) { // a row of -inf: the first ones
-        if ((int)threadIdx.x < k)
-            words[threadIdx.x] = word_of(-INFINITY, (uint32_t)(begin + threadIdx.x));
-        if (threadIdx.x == 0)
-            count = k;
-    }
-    if (top >= least) {
-        for (int s = 0; s < steps; s++) {
-            const int64_t at = begin + (int64_t)s * kStep;
-            if (__uint_as_float((uint32_t)tops[s][threadIdx.x] << 16) < least)
-                continue;
-            Logits again;
-            again.load(row, at, end);
-            float v[kEach];
-            again.values(v, at, end);
+    auto take = [&](float l, int64_t id) {
+        const int slot = atomicAdd(&count, 1); // the order decides nothing
+        if (slot < kCandidates)
+            words[slot] = word_of(l, (uint32_t)id);
+    };
+    // With fewer than k open groups, `least` is -inf: the open logits, and of the
+    // masked ones the first k.  Where many groups have `least` itself, or too many
+    // logits reach it, those above it first.
+    const bool masks = least == -INFINITY;
+    float from = masks ? -FLT_MAX : tied ? next_above(least) : least;
+    int found;
+#pragma unroll 1
+    for (;;) {
+        if (top >= from) {
+            for (int s = 0; s < steps; s++) {
+                const int64_t at = begin + (int64_t)s * kStep;
+                if (__uint_as_float((uint32_t)tops[s][threadIdx.x] << 16) < from)
+                    continue;
+                Logits again;
+                again.load(row, at, end);
+                float v[kEach];
+                again.values(v, at, end); // -inf where not the thread's own
 #pragma unroll
-            for (int i = 0; i < kEach; i++) {
-                const int q = i / Logits::kPer, e = i % Logits::kPer;
-                const int64_t id = Logits::id_of(at, q, e, end);
-                const float l = v[i] == v[i] ? v[i] : -INFINITY;
-                if (l >= least && Logits::own(at, q, e, end)) {
-                    const int slot = atomicAdd(&count, 1); // the order decides nothing
-                    if (slot < kCandidates)
-                        words[slot] = word_of(l, (uint32_t)id);
-                }
+                for (int i = 0; i < kEach; i++)
+                    if (v[i] >= from)
+                        take(v[i], Logits::id_of(at, i / Logits::kPer, i % Logits::kPer, end));
             }
         }
+        if (masks && (int)threadIdx.x < k && !(logit<BF16>(row, begin + threadIdx.x) > -INFINITY))
+            take(-INFINITY, begin + threadIdx.x); // NaN is as masked
+        __syncthreads();
+        found = count;
+        if (found <= kCandidates || from != least)
+            break;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            count = 0;
+        __syncthreads();
+        from = next_above(least);
     }
-    __syncthreads();
-    const bool few = count <= kCandidates;
+    // then the equal ones in the order of their ids (everybody has the same found)
+    for (int64_t at = begin; found < k && at < end; at += kThreads) {
+        const int64_t id = at + threadIdx.x;
+        const bool equal = id < end && logit<BF16>(row, id) == least;
+        const uint64_t lanes = __ballot(equal);
+        if (lane == 0)
+            equals[wave] = __popcll(lanes);
+        __syncthreads();
+        int slot = found + __popcll(lanes & (((uint64_t)1 << lane) - 1));
+#pragma unroll
+        for (int w = 0; w < WAVES; w++) {
+            slot += w < wave ? equals[w] : 0;
+            found += equals[w];
+        }
+        if (equal && slot < k)
+            words[slot] = word_of(least, (uint32_t)id);
+        found = min(found, k);
+        __syncthreads();
+    }
+    const bool few = found <= kCandidates;
     if (few && wave > 0)
         return;
     auto emit = [&](int rank, uint64_t word) {
@@ -572,27 +616,27 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_kernel(const LogprobsProb
     if (parts > 1 && (int)threadIdx.x >= k && (int)threadIdx.x < p.topk)
         out_words[(int64_t)blockIdx.x * p.topk + threadIdx.x] = 0; // none: below every logit
     if (few) {
-        rank_words<64>(words, count, k, emit);
+        rank_words<64>(words, found, k, emit);
         return;
     }
     uint64_t last = ~(uint64_t)0;
     for (int j = 0; j < k; j++) {
-        uint64_t found = 0;
+        uint64_t next = 0;
         for (int64_t i = begin + threadIdx.x; i < end; i += kThreads) {
             const uint64_t w = word_of(logit<BF16>(row, i), (uint32_t)i);
-            found = w < last ? larger(found, w) : found;
+            next = w < last ? larger(next, w) : next;
         }
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1)
-            found = larger(found, __shfl_xor(found, d));
+            next = larger(next, __shfl_xor(next, d));
         __syncthreads();
         if (lane == 0)
-            best[wave] = found;
+            best[wave] = next;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WAVES; w++)
-            found = larger(found, best[w]);
-        last = found;
+            next = larger(next, best[w]);
+        last = next;
         if (threadIdx.x == 0)
             emit(j, last);
     }

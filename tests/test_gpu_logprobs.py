@@ -297,3 +297,98 @@ def test_confident_rows(torch, rows, vocab, topk, dtype, beside):
             tol = tol_s + v * want.abs()
             assert ((got.double() - want).abs() <= tol).all(), (
                 (got.double() - want).abs() / tol).max()
+
+
+MASKS = ["-inf", "lowest", "-1e4", "nan"]
+
+
+def mask_to(torch, x, keep, mask):
+    """x with one value (or none) wherever `keep` is not set."""
+    value = {"-inf": -math.inf, "lowest": torch.finfo(x.dtype).min, "-1e4": -1e4, "nan": math.nan}[mask]
+    return torch.where(keep, x, value)
+
+
+def check_ids(torch, logits, topk):
+    """Ids alone, NaN as -inf: by value, then by lowest id."""
+    ids = bb.token_logprobs(logits, None, topk=topk)[2]
+    l = torch.where(torch.isnan(logits), -math.inf, logits.float())
+    order = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :topk]
+    assert torch.equal(ids.long(), order), torch.nonzero(ids.long() != order)[:4]
+
+
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab", [(30, 70), (20, 1500), (12, 4096), (5, 20000), (2, 131072),
+                                        (140, 50001), (520, 33000)])
+def test_masks_that_leave_few(torch, rows, vocab, dtype, mask):
+    """0, 1, 19, 20, 21 and more open logits with 1, 20 and 64 alternatives, anywhere, first or last."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(getattr(torch, dtype))
+    at = torch.arange(vocab, device="cuda")
+    many = torch.tensor([1, 19, 20, 21, 0, 63, 64, 65, 200, 1100], device="cuda")
+    many = many.repeat(rows // 10 + 1)[:rows, None]
+    for where in ("anywhere", "first", "last"):
+        if where == "anywhere":
+            place = torch.argsort(torch.rand(rows, vocab, generator=g, device="cuda"), dim=1)
+        else:
+            place = (at if where == "first" else at.flip(0)).expand(rows, vocab)
+        masked = mask_to(torch, x, place < many, mask)
+        for topk in (1, 20, 64):
+            check_ids(torch, masked, topk)
+        if mask != "nan":
+            tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+            some = many[:, 0] > 0
+            check(torch, masked[some], tokens[some], 20)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("mask", MASKS)
+@pytest.mark.parametrize("vocab", [4000, 32768, 140000])
+def test_open_logits_of_a_few_threads(torch, vocab, mask, dtype):
+    """Thousands of open logits, all in the first ten of every 64 (or 128) threads' places."""
+    each = 4 if dtype == "float32" else 8
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    for rows in (3, 600):
+        x = (torch.randn(rows, vocab, generator=g, device="cuda") * 3).to(getattr(torch, dtype))
+        keep = (torch.arange(vocab, device="cuda") // each % 64 < 10).expand(rows, vocab)
+        for topk in (9, 20, 64):
+            check_ids(torch, mask_to(torch, x, keep, mask), topk)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab", [(4, 3000), (3, 50000), (200, 40000), (600, 20000)])
+def test_many_equal_ones_behind_the_largest(torch, rows, vocab, dtype):
+    """Equal logits from somewhere on, 5 to 700 larger ones beside them, smaller ones before."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    for first in (0, vocab // 2, vocab - 1400):
+        x = torch.randn(rows, vocab, generator=g, device="cuda") - 50.0
+        x[:, first:] = 0.5
+        for row in range(rows):
+            at = torch.randint(0, vocab, ((5, 18, 25, 700)[row % 4],), generator=g, device="cuda")
+            x[row, at] = torch.rand(at.shape, generator=g, device="cuda") + 1.0
+        x = x.to(getattr(torch, dtype))
+        for topk in (1, 20, 64):
+            check_ids(torch, x, topk)
+
+
+def test_masks_cost_no_scans(torch):
+    """Rows that a mask leaves ten logits of, or whose logits are equal, take little longer than
+    others: they took 60 times as long where each alternative was a scan of the row."""
+    rows, vocab = 1024, 131072
+    x = (torch.randn(rows, vocab, device="cuda") * 3).bfloat16()
+    keep = torch.zeros(rows, vocab, dtype=torch.bool, device="cuda")
+    keep.scatter_(1, torch.randint(0, vocab, (rows, 10), device="cuda"), True)
+
+    def time(logits):
+        times = []
+        for _ in range(7):
+            start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            bb.token_logprobs(logits, topk=20)
+            stop.record()
+            stop.synchronize()
+            times.append(start.elapsed_time(stop))
+        return min(times)
+    plain = time(x)
+    for masked in [mask_to(torch, x, keep, m) for m in MASKS] + [torch.full_like(x, -1.0)]:
+        assert time(masked) <= 8 * plain
