@@ -789,13 +789,17 @@ PyObject *fp8_gemm_gated(PyObject *, PyObject *const *a, Py_ssize_t)
     return fp8_product("fp8_gemm_gated", a, true);
 }
 
-// (codes, scales, gate, gate_scales, up, up_scales, activation, out_codes, out_scales)
+// (codes, scales, gate, gate_scales, up, up_scales, activation, out_codes, out_scales, exact)
 PyObject *fp8_gemm_gated_quantize(PyObject *, PyObject *const *a, Py_ssize_t)
 {
     return guarded([&]() -> PyObject * {
         const char *where = "fp8_gemm_gated_quantize";
         at::AutoDispatchBelowADInplaceOrView below;
         const bpg_activation act = activation_of(where, a[6]);
+        const int truth = PyObject_IsTrue(a[9]);
+        if (truth < 0)
+            throw Raised{};
+        const bool exact = truth > 0;
         const Fp8Operands o = fp8_operands(where, a, true);
         if (o.n % 32 != 0)
             fail(where, "F = %lld is not a multiple of 32", (long long)o.n);
@@ -817,9 +821,22 @@ PyObject *fp8_gemm_gated_quantize(PyObject *, PyObject *const *a, Py_ssize_t)
             where, {&o.codes, &o.scales, &o.w, &o.w_scales, &o.up, &o.up_scales, &codes, &scales});
         const c10::DeviceGuard guard(device);
         // on the current stream, like the call: free for the next one behind it
-        const int64_t bytes = (int64_t)::fp8_gemm_gated_quantize_bytes(o.m, o.n, o.k);
+        const int64_t bytes = exact ? 4 * o.m * o.n
+                                    : (int64_t)::fp8_gemm_gated_quantize_bytes(o.m, o.n, o.k);
         const at::Tensor workspace = bytes ? make({bytes}, at::kByte, o.codes) : at::Tensor();
         check_status(where, unlocked([&] {
+                         if (exact) { // fp32 values, and their codes
+                             const bpg_status s = ::fp8_gemm_gated(
+                                 address(o.codes), address<float>(o.scales), o.m, address(o.w),
+                                 address<float>(o.w_scales), address(o.up),
+                                 address<float>(o.up_scales), o.n, o.k, act, address(workspace),
+                                 BPG_X_F32, o.n, stream_of(device));
+                             if (s != BPG_OK)
+                                 return s;
+                             return ::quantize_fp8(address(workspace), BPG_X_F32, o.m, o.n, o.n, 1,
+                                                   address(codes), address<float>(scales),
+                                                   stream_of(device));
+                         }
                          return ::fp8_gemm_gated_quantize(
                              address(o.codes), address<float>(o.scales), o.m, address(o.w),
                              address<float>(o.w_scales), address(o.up), address<float>(o.up_scales),
@@ -938,7 +955,7 @@ PyMethodDef methods[] = {
     BPG_METHOD(quantize_fp8, 4),
     BPG_METHOD(fp8_gemm, 6),
     BPG_METHOD(fp8_gemm_gated, 9),
-    BPG_METHOD(fp8_gemm_gated_quantize, 9),
+    BPG_METHOD(fp8_gemm_gated_quantize, 10),
     BPG_METHOD(token_logprobs, 7),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},

@@ -552,10 +552,13 @@ bpg_status fp8_gemm(const void *codes, const float *scales, int64_t m, const voi
  * (x . up^T), both products as fp8_gemm's and one rounding at the store; gate
  * and up are [f][k] codes with scales of their own, y [m][ldy], ldy >= f.
  * fp8_gemm_gated_quantize: the same values in fp32, products as with y bf16 (few
- * rows, "stream": as with y fp32),
- * written as quantize_fp8 does: codes [m][f], scales [m][ceil(f/128)], f a
- * multiple of 32: what fp8_gemm reads for the down projection.  workspace as
- * fp8_gemm's, of fp8_gemm_gated_quantize_bytes(m, f, k) bytes at least.
+ * rows, "stream": as with y fp32), written as quantize_fp8 does: codes [m][f],
+ * scales [m][ceil(f/128)], f a multiple of 32: what fp8_gemm reads for the down
+ * projection.  Of many rows' codes about 0.2 % differ from those of the values
+ * with products added in fp32: values next to a border between two codes, about
+ * as far from either.  For the latter at any number of rows: fp8_gemm_gated with
+ * y fp32, and quantize_fp8 of its result.  workspace as fp8_gemm's, of
+ * fp8_gemm_gated_quantize_bytes(m, f, k) bytes at least.
  * Errors: NULL, SHAPE, ALIGN, DTYPE, BUFFER, DEVICE, LAUNCH.
  */
 bpg_status fp8_gemm_gated(const void *codes, const float *scales, int64_t m,

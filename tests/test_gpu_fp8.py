@@ -665,3 +665,52 @@ def test_product_exact_side_by_side(torch, m, n, k, dtype):
     got = bb.fp8_gemm(c, s, w, dtype=dt)
     ref = mm64(torch, wide_values(torch, c, s, 1), wide_values(torch, w.codes, w.scales, 128)).to(dt)
     assert torch.equal(got, ref), torch.nonzero(got != ref)[:4]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("m,f,k", [s for s in GATED if s[0] > 16] + [(0, 64, 64), (1, 64, 96)])
+def test_exact_codes_are_those_of_the_fp32_values(torch, m, f, k, act):
+    """exact=True, any number of rows: bit for bit the codes of the fp32 values, which lie within the
+    fp32 products' bound of h (as in test_gated_quantize, without the 8-bit instruction's part)."""
+    c, s, gate, up = gated_case(torch, max(m, 1), f, k, m + f + k)
+    c, s = c[:m], s[:m]
+    codes, scales = bb.fp8_gemm_gated_quantize(c, s, gate, up, activation=act, exact=True)
+    want = bb.quantize_fp8(bb.fp8_gemm_gated(c, s, gate, up, activation=act))
+    given = (torch.empty_like(codes), torch.empty_like(scales))
+    again = bb.fp8_gemm_gated_quantize(c, s, gate, up, act, *given, exact=True)
+    assert again[0] is given[0] and again[1] is given[1]
+    for a, b, d in zip((codes, scales), want, again):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert torch.equal(a.view(torch.uint8), d.view(torch.uint8))
+    if m == 0:
+        return
+    h, lim = gated_reference(torch, c, s, gate, up, act, True)
+    d = scales.double().repeat_interleave(128, 1)[:, :f]
+    size = h.abs() + lim
+    step = torch.maximum(size * 2.0 ** -4, 2.0 ** -10 * d)
+    assert ((codes.double() * d - h).abs() <= step + lim + 4 * U * size).all()
+
+
+def test_exact_codes_from_graphs(torch):
+    g = generator(torch, 8)
+    m, f, k = 70, 320, 544
+    c, s = real_codes(torch, g, m, k, 1, True)
+    ws = [bb.Fp8Weights(*real_codes(torch, g, f, k, 128, False)) for _ in range(3)]
+    calls = [lambda i=i: bb.fp8_gemm_gated_quantize(c, s, ws[i], ws[i + 1], exact=True) for i in range(2)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(call())
+        graphs.append(gr)
+    for _ in range(4):
+        for i in range(2):
+            for t in outs[i]:
+                t.view(torch.uint8).fill_(0)
+            graphs[i].replay()
+            other = calls[1 - i]()
+            torch.cuda.synchronize()
+            for a, b in zip(outs[i] + other, want[i] + want[1 - i]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
