@@ -715,11 +715,27 @@ hipError_t launch_part(const Fp8Problem &p, const Fp8Part &part, hipStream_t s)
     }
 }
 
-// Few rows, and few enough columns for a workgroup per 16 of them: 32 rows x
-// 5120 take 11.9 us either way, x 1024 6.7 (tiles 11.9), x 17408 34 (tiles 27).
+// Few rows, and few enough columns for a workgroup per 16 of them, or a long K
+// and 16 rows at most, which leave two workgroups a CU: otherwise workgroups that
+// begin and end take longer than the weights.  In us, streamed and (in tiles),
+// weights in the last cache where they fit, K = 5120 but where another is named:
+//   8192 columns     1 row 8.8 (12.8), 16 8.9 (13.4), 32 12.2 (13.7);
+//                    K = 160 16 rows 4.3 (5.3), 32 5.6 (5.4)
+//   17408            1 to 16 rows 17 (17), fp32 17 (27), 32 rows 26 (18);
+//                    K = 1024 16 rows 9.3 (6.5), fp32 9.3 (9.2), 1 row 7.5 (9.0)
+//   49152            16 rows 38 (41), fp32 38 (49); K = 1024 18 (13)
+//   131072           1 row 115 (121), 4 120 (122), 8 126 (119), 16 154 (120);
+//                    fp32 113 (129), 119 (130), 124 (126), 155 (129);
+//                    K = 160 16 rows 37 (11)
+// A gated product of 16 rows at most always streams: its codes come from products
+// added in fp32.
 bool streams(const Fp8Problem &p)
 {
-    return p.m <= 16 || (p.m <= kFp8StreamRows && p.n * (p.up ? 2 : 1) <= 8192);
+    if (p.m <= kFp8StreamRows && p.n * (p.up ? 2 : 1) <= 8192)
+        return true;
+    if (p.m > 16 || p.up)
+        return p.m <= 16;
+    return fp8_blocks(p.k) >= (p.exact ? 8 : 32) && (p.n <= 49152 || p.m <= 4);
 }
 
 Fp8Plan streamed(const Fp8Problem &p)

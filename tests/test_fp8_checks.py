@@ -249,6 +249,22 @@ def test_every_kernel_has_a_tested_shape():
             (largest, False), (largest + ", then tile 64x256", False)} <= codes
 
 
+def test_few_rows_of_many_columns():
+    """Few rows stream their weights unless the workgroups' beginnings and ends are what counts:
+    many columns of a short K, or so many that more than four rows are better off in tiles."""
+    half, name = torch.bfloat16, bb.fp8_gemm_kernel_name
+    for dt in (half, None):
+        for m, n, k in ((1, 5120, 5120), (16, 8192, 160), (16, 17408, 5120), (16, 49152, 5120),
+                        (1, 131072, 5120), (4, 262144, 5120), (32, 8192, 5120)):
+            assert name(m, n, k, dt) == "stream", (m, n, k, dt)
+        for m, n, k in ((1, 17408, 160), (16, 131072, 5120), (5, 65536, 5120), (16, 131072, 160),
+                        (32, 17408, 5120)):
+            assert name(m, n, k, dt).startswith("tile"), (m, n, k, dt)
+        assert name(16, 17408, 1024, dt, gated=True) == "stream"
+    assert name(16, 17408, 1024, half).startswith("tile") and name(16, 17408, 1024) == "stream"
+    assert bb.fp8_gemm_gated_quantize_kernel_name(16, 17408, 160) == "stream"
+
+
 def test_every_pair_of_kernels_and_every_gated_kernel_over_long_k_has_a_tested_shape():
     from test_gpu_fp8 import (GATED, GATED_LONG, GATED_ODD, GATED_SIDE_BY_SIDE, SHAPES,
                               SIDE_BY_SIDE)

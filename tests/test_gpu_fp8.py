@@ -633,6 +633,10 @@ GATED_LONG = [(18, 32, 61 * 128), (33, 64, 120 * 128 + 32), (39, 33, 61 * 128), 
 SIDE_BY_SIDE = [(2078, 8226, 2080), (3105, 5277, 32), (2178, 7196, 32), (5400, 1630, 288)]
 GATED_SIDE_BY_SIDE = [(1611, 5326, 2080), (1812, 4447, 32), (2689, 3043, 32)]
 
+# few rows of so many columns that they are made in tiles
+FEW_OF_MANY = [(1, 17408, 160), (3, 17409, 96), (16, 20003, 1024), (9, 65540, 160), (16, 65539, 4128),
+               (5, 131072, 544)]
+
 
 @pytest.mark.parametrize("m,f,k", GATED_LONG + GATED_SIDE_BY_SIDE)
 def test_gated_exact_relu_long_k(torch, m, f, k):
@@ -656,7 +660,7 @@ def test_gated_exact_relu_long_k(torch, m, f, k):
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
-@pytest.mark.parametrize("m,n,k", SIDE_BY_SIDE)
+@pytest.mark.parametrize("m,n,k", SIDE_BY_SIDE + FEW_OF_MANY)
 def test_product_exact_side_by_side(torch, m, n, k, dtype):
     dt = getattr(torch, dtype)
     g = generator(torch, m + n + k)
