@@ -28,7 +28,13 @@ __device__ __forceinline__ uint32_t lds_address(const void *p)
 constexpr uint32_t kPastBuffer = 0x80000000u; // an offset past the end of every buffer
 
 // [rows][row_bytes] from `row` on, `most` rows at most (below 2^31 bytes), as a
-// buffer: reads past its last row give zeros.
+// buffer: reads past its last row give zeros and touch no memory.  The loads below
+// have a part of their offset, rows by the eight and the block of K, in the scalar
+// offset.  The bounds check counts it (the CDNA manuals compare the lane's offset
+// with the number of records less the scalar one), does not wrap where it alone is
+// past the end, and is made for each of a load's four words by itself: measured on
+// gfx950 with buffers that end inside an allocation, at 1000 bytes with scalar
+// offsets of 0, 512, 992, 1024 and 2048, and at 1004 and 1008.
 __device__ __forceinline__ v4i buffer_of(const void *at, int64_t row, int64_t rows, int64_t row_bytes,
                                          int most)
 {
