@@ -54,7 +54,7 @@ __device__ __forceinline__ void load16(v4i from, uint32_t to, uint32_t lane_at, 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(to), "v"(lane_at), "s"(from), "s"(at)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 // the same for some lanes (all of them are on around it)
@@ -67,7 +67,7 @@ __device__ __forceinline__ void load16_lanes(uint64_t lanes, v4i from, uint32_t 
                  "buffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b64 exec, -1"
                  :
                  : "s"(to), "v"(lane_at), "s"(from), "s"(at), "s"(lo), "s"(hi)
-                 : "memory");
+                 : "memory", "m0");
 }
 
 template <class V> __device__ __forceinline__ V lds_read(uint32_t at, int offset)
