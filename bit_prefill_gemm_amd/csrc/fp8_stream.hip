@@ -8,12 +8,14 @@
 // a ring of its own in LDS by direct loads, two blocks on the way.  No wave waits
 // for another before the end, where their sums are added in wave order.
 //
-// Bound by memory where there are many columns (1 x 17408 x 5120, 89 MB: 19.7 us,
-// 4.5 TB/s; gated to codes 43.8 us, 4.1 TB/s) and by the time to fill and drain
-// where there are few (1 x 5120 x 5120: 7.9 us, 3.3 TB/s; 1 x 1024 x 5120: 4.6 us).
-// Blocks of K dealt to the waves in turn, straight to registers, took 20.7 us for
-// the first and 14.2 instead of 8.7 for 16 x 5120 x 5120, where a load of x or w
-// in the operands' shape keeps the load unit for 47 clocks (fp8_lds.h).
+// Bound by memory where there are many columns (rows x columns x K 1 x 17408 x
+// 5120, 89 MB: 20.5 us, 4.4 TB/s; gated to codes 44 us, 4.0 TB/s) and by the time
+// to fill and drain where there are few (1 x 5120 x 5120: 8.8 us, 3.0 TB/s; 1 x
+// 1024 x 5120: 5.1 us).  With the weights in the last cache these take 16.6, 35.5,
+// 5.5 and 3.8 us.  Blocks of K dealt to the waves in turn, straight to registers,
+// took a microsecond more for the first and 14.2 instead of 8.7 for 16 x 5120 x
+// 5120, where a load of x or w in the operands' shape keeps the load unit for 47
+// clocks (fp8_lds.h).
 #include "fp8.h"
 
 #include "epilogue.h"

@@ -19,9 +19,10 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // KS groups of such waves take a part of K each; S stages of one block of K are
 // in LDS, and P waves of a group do nothing but load them (0: the others do).
 //
-// What the tiles reach (bf16 results): 256x256 2400 TF at 8192 x 17408 x 5120
-// (602 to 620 us; the library's product of the same size under one scale for
-// everything 2500 TF), 128x128 1190 TF at 512 x 5120 x 5120 (22.5 us, 160
+// What the tiles reach (bf16 results, rows x columns x K, weights in the last
+// cache): 256x256 2290 to 2380 TF at 8192 x 17408 x 5120 (614 to 637 us with the
+// rest of the columns; the library's product of the same size under one scale for
+// everything 2500 TF), 128x128 1210 TF at 512 x 5120 x 5120 (22.1 us, 160
 // workgroups).  A block of 256x256 takes 2700 clocks of the matrix unit's 2048,
 // one of 128x128 1080 of 512.  What bounds them is the vector unit beside the
 // matrix unit: the block scales cost four additions per instruction, and while a
@@ -29,7 +30,7 @@ typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 // that two waves of a SIMD need 37 clocks for 32 and one, alone, 45; the rest is
 // barriers and the first and last block.  32 x 32 instructions (half the reads,
 // but twice the registers per operand, so fewer of them in flight) took 663 us
-// at the first size and 22.9 at the second.
+// at the first size beside 614, and 22.9 at the second beside 22.5.
 template <int NI_, int MJ_, int NW_, int MW_, int KS_, int S_, int P_ = 0>
 struct Tile {
     static constexpr int NI = NI_, MJ = MJ_, NW = NW_, MW = MW_, KS = KS_, S = S_;
@@ -528,7 +529,9 @@ hipError_t launch_values(const Fp8Problem &p, const Fp8Part &part, hipStream_t s
 // What a tile costs, in us on an MI355X: `fixed`, and per block of K with few
 // tiles on the chip (`light`) and with as many as it holds at once (`full`,
 // `slots` of them).  Fitted to 5120 x 5120 to 17408 x 5120 with 128 to 8192
-// rows; products whose codes are widened take longer.
+// rows; products whose codes are widened take longer.  A head's 131072 columns of
+// K = 5120 take 313, 323 and 600 us for 333, 512 and 1024 rows with them (1430,
+// 2130 and 2290 TF), fp32 469, 622 and 1198; 64 rows 150 and 162 (4.5 TB/s).
 struct Cost {
     int kernel, rows, cols, slots;
     float fixed, light, full;
@@ -594,7 +597,7 @@ template <int N> float plan(const Cost (&costs)[N], const Fp8Problem &p, Fp8Plan
     plan->part[0].cols = p.n;
     const float whole = best_of(costs, p, p.n, &plan->part[0].kernel);
     // The largest tiles (the first of the list) for as many columns as fill the
-    // chip in whole rounds, and the quickest for the rest: 1024 x 5120 x 17408
+    // chip in whole rounds, and the quickest for the rest: 1024 x 17408 x 5120
     // gated is 2.1 rounds, 208 us as three and 192 us as two and a rest.
     const Cost &c = costs[0];
     const int64_t each = c.cols / (p.up ? 2 : 1), down = (p.m + c.rows - 1) / c.rows;
@@ -615,9 +618,9 @@ template <int N> float plan(const Cost (&costs)[N], const Fp8Problem &p, Fp8Plan
 }
 
 // Tiles over a part of K each, where there are few of them: the sums are written
-// and read again, at 5 TB/s.  In us, without and with: rows x K x columns
-// 1024 x 17408 x 5120, 80 tiles of 256x256, 143 and 101; 64 x 17408 x 5120 35 and
-// 25; 96 x 16384 x 1024 29 and 14; fp32 results 256 x 17408 x 5120 79 and 58.
+// and read again, at 5 TB/s.  In us, without and with: rows x columns x K
+// 1024 x 5120 x 17408, 80 tiles of 256x256, 143 and 101; 64 x 5120 x 17408 35 and
+// 25; 96 x 1024 x 16384 29 and 14; fp32 results 256 x 5120 x 17408 79 and 58.
 // Replaces *plan where that is quicker than `best`.
 template <int N>
 void split_k(const Cost (&costs)[N], const Fp8Problem &p, float best, Fp8Plan *plan)
@@ -626,7 +629,7 @@ void split_k(const Cost (&costs)[N], const Fp8Problem &p, float best, Fp8Plan *p
     const float value = p.y_bf16 ? 2 : 4; // bytes of a result
     for (const Cost &c : costs) {
         // one 128x128 a CU, with its loads further ahead, is the quicker of the two
-        // there: 520 x 7808 x 5000 33 us, two a CU 44
+        // there: 520 x 5000 x 7808 33 us, two a CU 44
         if (c.kernel == kFp8Tile128x128Pair && !p.exact)
             continue;
         const int64_t tiles = tiles_of(c, p.m, p.n, 1);

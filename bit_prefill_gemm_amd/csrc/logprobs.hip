@@ -32,11 +32,14 @@
 // Few rows are split into parts of 8192 logits or more, a workgroup each, and
 // another launch joins them.
 //
-// Bound by memory where there are many rows: 4096 x 131072 bf16, 1.07 GB, 189 us
-// (5.7 TB/s; 196 with an alternative), fp32 2048 x 131072 181 us (5.9 TB/s).  Few or short rows are bound by
-// the chain of their steps: the sums over a workgroup, the k-th of the groups'
-// maxima, the ranks, the join (1 x 131072 with 20 alternatives 12 us, 333 x 50001
-// with 5 19 us, masked or not, 16 x 262144 with 64 26 us).
+// Bound by memory where there are many rows: 4096 x 131072 bf16, 1.07 GB, 200 us
+// (5.4 TB/s; 195 to 215 with an alternative), fp32 2048 x 131072 186 us (5.8 TB/s).
+// Few or short rows are bound by the chain of their steps: the sums over a
+// workgroup, the k-th of the groups' maxima, the ranks, the join (1 x 131072 with
+// 20 alternatives 12 us, 333 x 50001 with 5 18 us, a quarter of it masked 19, 16 x
+// 262144 with 64 25 us).  Rows whose largest logit has nearly all of the
+// probability read a thread's logits again: 333 x 50001 19 us, 4096 x 131072 207,
+// 8192 x 1000 fp32 with 5 alternatives 23.6 instead of 21.
 #include "fp8.h"
 
 #include <algorithm>
