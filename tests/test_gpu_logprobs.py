@@ -392,3 +392,22 @@ def test_masks_cost_no_scans(torch):
     plain = time(x)
     for masked in [mask_to(torch, x, keep, m) for m in MASKS] + [torch.full_like(x, -1.0)]:
         assert time(masked) <= 8 * plain
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab", [(3, 700), (4, 4000), (2, 40000), (300, 20000)])
+def test_many_at_the_ends_of_the_order(torch, rows, vocab, dtype):
+    """Most logits zero (of both signs), the type's largest, +inf, or its smallest step above zero,
+    with a few on either side."""
+    dt = getattr(torch, dtype)
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps  # the smallest subnormal
+    for value in (0.0, -0.0, torch.finfo(dt).max, math.inf, tiny, -tiny):
+        x = torch.full((rows, vocab), value, dtype=dt, device="cuda")
+        if value == 0.0:
+            x[:, 1::2] = -value
+        for other in (1.0, -1.0, tiny, -tiny, 2 * tiny):
+            at = torch.randint(0, vocab, (rows, 9), generator=g, device="cuda")
+            x.scatter_(1, at, torch.full((rows, 9), other, dtype=dt, device="cuda"))
+        for topk in (1, 20, 64):
+            check_ids(torch, x, topk)
